@@ -26,7 +26,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfp8fg.so")
 
-SOURCES = ["abi.cpp", "quant.hip", "gemm.hip"]
+SOURCES = ["abi.cpp", "quant.hip", "gemm.hip", "norm.hip", "route.hip", "dispatch.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -7,6 +7,8 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <cmath>
+#include <initializer_list>
 
 #include "fp8fg.h"
 #include "launch.h"
@@ -90,6 +92,58 @@ int check_gemm_common(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t
     if (b_scale_mode == FP8FG_BSCALE_COL && sb_ns >= kMaxScaleRowStride) return FP8FG_EUNSUPPORTED;
   }
   return FP8FG_OK;
+}
+
+bool is_xtype(int t) { return t == FP8FG_BF16 || t == FP8FG_F32; }
+
+// A [rows][cols] operand whose rows are read and written 16 bytes at a time:
+// its status (a null one passes unless it is needed).
+int check_rows(const void* p, bool needed, int64_t ld, int64_t cols, int size) {
+  if (!p) return needed ? FP8FG_EINVAL : FP8FG_OK;
+  if (ld < cols) return FP8FG_ESHAPE;
+  if (!aligned(p, 16) || (ld % 16 * size) % 16) return FP8FG_EALIGN;
+  return FP8FG_OK;
+}
+
+// The first status that is not FP8FG_OK.
+template <typename... S>
+int first_of(S... st) {
+  int rc = FP8FG_OK;
+  ((rc = rc != FP8FG_OK ? rc : st), ...);
+  return rc;
+}
+
+bool negative(std::initializer_list<int64_t> v) {
+  for (const int64_t x : v)
+    if (x < 0) return true;
+  return false;
+}
+
+bool beyond(int64_t limit, std::initializer_list<int64_t> v) {
+  for (const int64_t x : v)
+    if (x > limit) return true;
+  return false;
+}
+
+// Row pitches whose byte offsets stay in 64 bits for every int32 row.
+constexpr int64_t kMaxPitch = (int64_t)1 << 29;
+constexpr int64_t kMaxI32 = 0x7FFFFFFF;
+// Columns whose 16-byte vectors a 32-bit index counts.
+constexpr int64_t kMaxMoveCols = (int64_t)1 << 28;
+
+int check_route(int l_type, int64_t rows, int64_t experts, int64_t ldl, int score, int64_t k,
+                int renorm, float scale) {
+  if (!is_xtype(l_type)) return FP8FG_EINVAL;
+  if (score != FP8FG_SCORE_SOFTMAX && score != FP8FG_SCORE_SIGMOID) return FP8FG_EINVAL;
+  if (renorm != 0 && renorm != 1) return FP8FG_EINVAL;
+  if (negative({rows, ldl}) || experts < 1 || k < 1 || !std::isfinite(scale)) return FP8FG_EINVAL;
+  if (k > experts || ldl < experts) return FP8FG_ESHAPE;
+  return FP8FG_OK;
+}
+
+// The last row's code, -2 - (tokens * k - 1), has to fit an int32 too.
+bool dispatch_fits(int64_t tokens, int64_t k, int64_t experts) {
+  return k <= kMaxI32 && tokens <= (kMaxI32 - 2) / k && experts <= fp8fg::kRouteMaxExperts;
 }
 
 // HIP takes at most 2^32 - 1 work-items along a grid dimension.
@@ -215,6 +269,189 @@ int fp8_grouped_gemm_blockscaled(int64_t G, const int32_t* offsets, int64_t M_to
   const fp8fg::GemmPlan plan = fp8fg::plan_gemm(g, fp8fg::device_cu_count());
   if (!grid_fits(plan)) return FP8FG_EUNSUPPORTED;
   return launched(fp8fg::launch_gemm(g, plan, reinterpret_cast<hipStream_t>(stream)));
+}
+
+int fp8_rmsnorm_quantize(const void* x, int x_type, int64_t rows, int64_t cols, int64_t ldx,
+                         const void* r, int64_t ldr, const void* gamma, int g_type, float eps,
+                         int scale_rule, void* h, int64_t ldh, void* y, int64_t ldy, uint8_t* q,
+                         int64_t ldq, float* s, int64_t s_rs, int64_t s_ts, float* rstd,
+                         void* stream) {
+  if (!is_xtype(x_type) || !is_xtype(g_type)) return FP8FG_EINVAL;
+  if (scale_rule != FP8FG_SCALE_AMAX && scale_rule != FP8FG_SCALE_POW2) return FP8FG_EINVAL;
+  if (negative({rows, cols, ldx, ldr, ldh, ldy, ldq, s_rs, s_ts})) return FP8FG_EINVAL;
+  if (!(eps >= 0.0f) || !std::isfinite(eps)) return FP8FG_EINVAL;
+  if (cols % 128) return FP8FG_ESHAPE;
+  if (rows == 0 || cols == 0) return FP8FG_OK;
+  if (!gamma || (q && !s)) return FP8FG_EINVAL;
+  const int size = elem_size(x_type);
+  const int rc = first_of(check_rows(x, true, ldx, cols, size), check_rows(r, false, ldr, cols, size),
+                          check_rows(h, false, ldh, cols, size), check_rows(y, false, ldy, cols, size),
+                          check_rows(q, false, ldq, cols, 1));
+  if (rc != FP8FG_OK) return rc;
+  if (!aligned(gamma, 16) || !aligned(s, 4) || !aligned(rstd, 4)) return FP8FG_EALIGN;
+  if (cols > fp8fg::kNormMaxCols || rows > kMaxI32 || beyond(kMaxPitch, {ldx, ldr, ldh, ldy, ldq, s_rs}) ||
+      s_ts > kMaxI32)
+    return FP8FG_EUNSUPPORTED;
+  const fp8fg::NormArgs a{x, x_type, rows, cols, ldx, r,   ldr, gamma, g_type, eps, scale_rule,
+                          h, ldh,    y,    ldy,  q,   ldq, s,   s_rs,  s_ts,   rstd};
+  return launched(fp8fg::launch_norm(a, reinterpret_cast<hipStream_t>(stream)));
+}
+
+int64_t fp8_rmsnorm_backward_workspace(int64_t rows, int64_t cols) {
+  if (rows < 0 || cols < 0 || cols > fp8fg::kNormMaxCols) return 0;
+  return fp8fg::norm_grad_strips(rows) * cols * (int64_t)sizeof(float);
+}
+
+int fp8_rmsnorm_backward(const void* dy, int x_type, int64_t rows, int64_t cols, int64_t lddy,
+                         const void* dh, int64_t lddh, const void* h, int64_t ldh,
+                         const void* gamma, int g_type, const float* rstd, void* dx, int64_t lddx,
+                         float* dgamma, void* workspace, int64_t workspace_bytes, void* stream) {
+  if (!is_xtype(x_type) || !is_xtype(g_type)) return FP8FG_EINVAL;
+  if (negative({rows, cols, lddy, lddh, ldh, lddx, workspace_bytes})) return FP8FG_EINVAL;
+  if (cols % 8) return FP8FG_ESHAPE;
+  if (cols == 0) return FP8FG_OK;
+  if (!dgamma) return FP8FG_EINVAL;
+  if (!aligned(dgamma, 4)) return FP8FG_EALIGN;
+  if (rows > 0) {
+    if (!gamma || !rstd || !workspace) return FP8FG_EINVAL;
+    const int size = elem_size(x_type);
+    const int rc = first_of(check_rows(dy, true, lddy, cols, size), check_rows(dh, false, lddh, cols, size),
+                            check_rows(h, true, ldh, cols, size), check_rows(dx, true, lddx, cols, size));
+    if (rc != FP8FG_OK) return rc;
+    if (!aligned(gamma, 16) || !aligned(rstd, 4) || !aligned(workspace, 16)) return FP8FG_EALIGN;
+  }
+  if (cols > fp8fg::kNormMaxCols || rows > kMaxI32 || beyond(kMaxPitch, {lddy, lddh, ldh, lddx}))
+    return FP8FG_EUNSUPPORTED;
+  if (workspace_bytes < fp8_rmsnorm_backward_workspace(rows, cols)) return FP8FG_ESHAPE;
+  const fp8fg::NormGradArgs a{dy,    x_type, rows, cols, lddy, dh,     lddh,  h,
+                              ldh,   gamma,  g_type, rstd, dx, lddx, dgamma,
+                              reinterpret_cast<float*>(workspace)};
+  return launched(fp8fg::launch_norm_grad(a, reinterpret_cast<hipStream_t>(stream)));
+}
+
+int fp8_route(const void* logits, int l_type, int64_t rows, int64_t experts, int64_t ldl,
+              const float* bias, int score, int64_t groups, int64_t top_groups, int group_top,
+              int64_t k, int renorm, float scale, int32_t* idx, int64_t ld_idx, float* w,
+              int64_t ldw, void* stream) {
+  const int rc = check_route(l_type, rows, experts, ldl, score, k, renorm, scale);
+  if (rc != FP8FG_OK) return rc;
+  if (groups < 1 || top_groups < 1 || (group_top != 1 && group_top != 2)) return FP8FG_EINVAL;
+  if (ld_idx < 0 || ldw < 0) return FP8FG_EINVAL;
+  if (experts % groups || top_groups > groups || ld_idx < k || ldw < k) return FP8FG_ESHAPE;
+  if (rows == 0) return FP8FG_OK;
+  if (!logits || !idx || !w) return FP8FG_EINVAL;
+  if (!aligned(logits, elem_size(l_type)) || !aligned(bias, 4) || !aligned(idx, 4) || !aligned(w, 4))
+    return FP8FG_EALIGN;
+  if (experts > fp8fg::kRouteMaxExperts || k > fp8fg::kRouteMaxK || rows > kMaxI32 ||
+      beyond(kMaxPitch, {ldl, ld_idx, ldw}))
+    return FP8FG_EUNSUPPORTED;
+  const fp8fg::RouteArgs a{logits, l_type, rows, (int)experts, ldl, bias, score, (int)groups, (int)top_groups,
+                           group_top, (int)k, renorm, scale, idx, ld_idx, w, ldw};
+  return launched(fp8fg::launch_route(a, reinterpret_cast<hipStream_t>(stream)));
+}
+
+int fp8_route_backward(const void* logits, int l_type, int64_t rows, int64_t experts, int64_t ldl,
+                       int score, int64_t k, int renorm, float scale, const int32_t* idx,
+                       int64_t ld_idx, const float* dw, int64_t lddw, void* dlogits,
+                       int64_t lddl, void* stream) {
+  const int rc = check_route(l_type, rows, experts, ldl, score, k, renorm, scale);
+  if (rc != FP8FG_OK) return rc;
+  if (negative({ld_idx, lddw, lddl})) return FP8FG_EINVAL;
+  if (ld_idx < k || lddw < k || lddl < experts) return FP8FG_ESHAPE;
+  if (rows == 0) return FP8FG_OK;
+  if (!logits || !idx || !dw || !dlogits) return FP8FG_EINVAL;
+  const int size = elem_size(l_type);
+  if (!aligned(logits, size) || !aligned(dlogits, size) || !aligned(idx, 4) || !aligned(dw, 4))
+    return FP8FG_EALIGN;
+  if (experts > fp8fg::kRouteMaxExperts || k > fp8fg::kRouteMaxK || rows > kMaxI32 ||
+      beyond(kMaxPitch, {ldl, ld_idx, lddw, lddl}))
+    return FP8FG_EUNSUPPORTED;
+  const fp8fg::RouteGradArgs a{logits, l_type, rows, (int)experts, ldl, score, (int)k, renorm, scale,
+                               idx, ld_idx, dw, lddw, dlogits, lddl};
+  return launched(fp8fg::launch_route_grad(a, reinterpret_cast<hipStream_t>(stream)));
+}
+
+int64_t fp8_dispatch_workspace(int64_t tokens, int64_t k, int64_t experts) {
+  if (tokens < 0 || k < 1 || experts < 1 || !dispatch_fits(tokens, k, experts)) return 0;
+  return fp8fg::dispatch_chunks(tokens * k) * (experts + 1) * (int64_t)sizeof(int32_t);
+}
+
+int fp8_dispatch(const int32_t* idx, int64_t ld_idx, int64_t tokens, int64_t k, int64_t experts,
+                 const void* x, int x_type, int64_t cols, int64_t ldx, const float* xs,
+                 int64_t xs_rs, int64_t xs_ts, int32_t* offsets, int32_t* pos, int32_t* token,
+                 void* out, int64_t ldo, float* os, int64_t os_rs, int64_t os_ts, void* workspace,
+                 int64_t workspace_bytes, void* stream) {
+  if (!is_xtype(x_type) && x_type != FP8FG_E4M3) return FP8FG_EINVAL;
+  if (negative({ld_idx, tokens, cols, ldx, xs_rs, xs_ts, ldo, os_rs, os_ts, workspace_bytes}) || k < 1 || experts < 1)
+    return FP8FG_EINVAL;
+  const bool e4m3 = x_type == FP8FG_E4M3;
+  if (x && cols % (e4m3 ? 128 : 8)) return FP8FG_ESHAPE;
+  if (ld_idx < k) return FP8FG_ESHAPE;
+  if (!offsets || !workspace) return FP8FG_EINVAL;
+  if (!aligned(offsets, 4) || !aligned(workspace, 4)) return FP8FG_EALIGN;
+  const bool rows = x && cols > 0 && tokens > 0;
+  if (tokens > 0) {
+    if (!idx || !pos || !token) return FP8FG_EINVAL;
+    if (!aligned(idx, 4) || !aligned(pos, 4) || !aligned(token, 4)) return FP8FG_EALIGN;
+  }
+  if (rows) {
+    if (e4m3 && (!xs || !os)) return FP8FG_EINVAL;
+    const int size = elem_size(x_type);
+    const int rc = first_of(check_rows(x, true, ldx, cols, size), check_rows(out, true, ldo, cols, size));
+    if (rc != FP8FG_OK) return rc;
+    if (e4m3 && (!aligned(xs, 4) || !aligned(os, 4))) return FP8FG_EALIGN;
+  }
+  if (!dispatch_fits(tokens, k, experts) || beyond(kMaxPitch, {ld_idx, ldx, xs_rs, ldo, os_rs}) ||
+      beyond(kMaxI32, {xs_ts, os_ts}) || (x && cols > kMaxMoveCols))
+    return FP8FG_EUNSUPPORTED;
+  if (workspace_bytes < fp8_dispatch_workspace(tokens, k, experts)) return FP8FG_ESHAPE;
+  const fp8fg::DispatchArgs a{idx, ld_idx, tokens, (int)k, (int)experts, rows ? x : nullptr, x_type, cols,
+                              ldx, xs, xs_rs, xs_ts, offsets, pos, token, out, ldo, os, os_rs, os_ts,
+                              reinterpret_cast<int32_t*>(workspace)};
+  return launched(fp8fg::launch_dispatch(a, reinterpret_cast<hipStream_t>(stream)));
+}
+
+int fp8_combine(const void* z, int type, int64_t z_rows, int64_t tokens, int64_t k, int64_t cols,
+                int64_t ldz, const int32_t* pos, const float* w, int64_t ldw, const void* base,
+                int64_t ldb, void* out, int64_t ldo, void* stream) {
+  if (!is_xtype(type)) return FP8FG_EINVAL;
+  if (negative({z_rows, tokens, cols, ldz, ldw, ldb, ldo}) || k < 1) return FP8FG_EINVAL;
+  if (cols % 8) return FP8FG_ESHAPE;
+  if (tokens == 0 || cols == 0) return FP8FG_OK;
+  if (!pos) return FP8FG_EINVAL;
+  if (w && ldw < k) return FP8FG_ESHAPE;
+  const int size = elem_size(type);
+  const int rc = first_of(check_rows(z, z_rows > 0, ldz, cols, size), check_rows(base, false, ldb, cols, size),
+                          check_rows(out, true, ldo, cols, size));
+  if (rc != FP8FG_OK) return rc;
+  if (!aligned(pos, 4) || !aligned(w, 4)) return FP8FG_EALIGN;
+  if (beyond(kMaxI32, {z_rows, tokens, k}) || cols > kMaxMoveCols || beyond(kMaxPitch, {ldz, ldw, ldb, ldo}))
+    return FP8FG_EUNSUPPORTED;
+  const fp8fg::CombineArgs a{z, type, z_rows, tokens, (int)k, cols, ldz, pos, w, ldw, base, ldb, out, ldo};
+  return launched(fp8fg::launch_combine(a, reinterpret_cast<hipStream_t>(stream)));
+}
+
+int fp8_combine_backward(const void* dy, int type, int64_t z_rows, int64_t tokens, int64_t k,
+                         int64_t cols, int64_t lddy, const void* z, int64_t ldz,
+                         const int32_t* pos, const float* w, int64_t ldw, void* dz, int64_t lddz,
+                         float* dw, int64_t lddw, void* stream) {
+  if (!is_xtype(type)) return FP8FG_EINVAL;
+  if (negative({z_rows, tokens, cols, lddy, ldz, ldw, lddz, lddw}) || k < 1) return FP8FG_EINVAL;
+  if (cols % 8) return FP8FG_ESHAPE;
+  if (tokens == 0) return FP8FG_OK;
+  if (!pos) return FP8FG_EINVAL;
+  if ((w && ldw < k) || (dw && lddw < k)) return FP8FG_ESHAPE;
+  const int size = elem_size(type);
+  const int rc = first_of(check_rows(dy, cols > 0, lddy, cols, size),
+                          check_rows(z, dw && z_rows > 0 && cols > 0, ldz, cols, size),
+                          check_rows(dz, z_rows > 0 && cols > 0, lddz, cols, size));
+  if (rc != FP8FG_OK) return rc;
+  if (!aligned(pos, 4) || !aligned(w, 4) || !aligned(dw, 4)) return FP8FG_EALIGN;
+  if (beyond(kMaxI32, {z_rows, tokens, k}) || cols > kMaxMoveCols ||
+      beyond(kMaxPitch, {lddy, ldz, ldw, lddz, lddw}))
+    return FP8FG_EUNSUPPORTED;
+  const fp8fg::CombineGradArgs a{dy, type, z_rows, tokens, (int)k, cols, lddy, z, ldz, pos, w, ldw, dz, lddz, dw, lddw};
+  return launched(fp8fg::launch_combine_grad(a, reinterpret_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

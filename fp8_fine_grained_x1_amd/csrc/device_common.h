@@ -138,4 +138,144 @@ __device__ __forceinline__ void unpack4_e4m3(uint32_t w, float out[4]) {
   out[3] = hi[1];
 }
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+// Non-temporal 16- and 8-byte accesses, for data that streams through once.
+__device__ __forceinline__ uint4 ld_nt16(const void* p) {
+  const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ uint2 ld_nt8(const void* p) {
+  const u32x2 v = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p));
+  return make_uint2(v[0], v[1]);
+}
+__device__ __forceinline__ void st_nt8(void* p, uint2 v) {
+  const u32x2 w = {v.x, v.y};
+  __builtin_nontemporal_store(w, reinterpret_cast<u32x2*>(p));
+}
+__device__ __forceinline__ void st_nt16(void* p, uint4 v) {
+  const u32x4 w = {v.x, v.y, v.z, v.w};
+  __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(p));
+}
+
+// 8 consecutive elements as fp32 (XT 0: bf16, 1: f32), non-temporal.
+template <int XT>
+__device__ __forceinline__ void load8(const void* __restrict__ x, int64_t off, float v[8]) {
+  if constexpr (XT == 0) {
+    const uint4 w = ld_nt16(reinterpret_cast<const uint16_t*>(x) + off);
+    v[0] = bf16_lo(w.x); v[1] = bf16_hi(w.x);
+    v[2] = bf16_lo(w.y); v[3] = bf16_hi(w.y);
+    v[4] = bf16_lo(w.z); v[5] = bf16_hi(w.z);
+    v[6] = bf16_lo(w.w); v[7] = bf16_hi(w.w);
+  } else {
+    const float* p = reinterpret_cast<const float*>(x) + off;
+    const uint4 a = ld_nt16(p), b = ld_nt16(p + 4);
+    v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y);
+    v[2] = __uint_as_float(a.z); v[3] = __uint_as_float(a.w);
+    v[4] = __uint_as_float(b.x); v[5] = __uint_as_float(b.y);
+    v[6] = __uint_as_float(b.z); v[7] = __uint_as_float(b.w);
+  }
+}
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+// Two fp32 values -> bf16 pair (round-to-nearest-even), first in the low half.
+__device__ __forceinline__ uint32_t pack2_bf16(float a, float b) {
+  const bf16x2 v = {(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(uint32_t, v);
+}
+
+// 8 consecutive elements in their own encoding (XT 0: bf16, 1: f32): kept
+// undecoded where they wait in registers for a second use.
+template <int XT>
+struct Raw8;
+template <>
+struct Raw8<0> {
+  uint4 w;
+};
+template <>
+struct Raw8<1> {
+  uint4 a, b;
+};
+
+template <int XT>
+__device__ __forceinline__ void decode8(const Raw8<XT>& r, float v[8]) {
+  if constexpr (XT == 0) {
+    v[0] = bf16_lo(r.w.x); v[1] = bf16_hi(r.w.x);
+    v[2] = bf16_lo(r.w.y); v[3] = bf16_hi(r.w.y);
+    v[4] = bf16_lo(r.w.z); v[5] = bf16_hi(r.w.z);
+    v[6] = bf16_lo(r.w.w); v[7] = bf16_hi(r.w.w);
+  } else {
+    v[0] = __uint_as_float(r.a.x); v[1] = __uint_as_float(r.a.y);
+    v[2] = __uint_as_float(r.a.z); v[3] = __uint_as_float(r.a.w);
+    v[4] = __uint_as_float(r.b.x); v[5] = __uint_as_float(r.b.y);
+    v[6] = __uint_as_float(r.b.z); v[7] = __uint_as_float(r.b.w);
+  }
+}
+
+// fp32 values rounded to the element type (bf16: nearest-even; f32: as is).
+template <int XT>
+__device__ __forceinline__ Raw8<XT> encode8(const float v[8]) {
+  Raw8<XT> r;
+  if constexpr (XT == 0) {
+    r.w = make_uint4(pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]), pack2_bf16(v[4], v[5]), pack2_bf16(v[6], v[7]));
+  } else {
+    r.a = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+    r.b = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
+  }
+  return r;
+}
+
+// Ordinary (cached) and non-temporal forms; p + off is 16-byte aligned.
+template <int XT, bool NT>
+__device__ __forceinline__ Raw8<XT> load_raw8(const void* __restrict__ p, int64_t off) {
+  Raw8<XT> r;
+  if constexpr (XT == 0) {
+    const uint16_t* q = reinterpret_cast<const uint16_t*>(p) + off;
+    r.w = NT ? ld_nt16(q) : *reinterpret_cast<const uint4*>(q);
+  } else {
+    const float* q = reinterpret_cast<const float*>(p) + off;
+    r.a = NT ? ld_nt16(q) : *reinterpret_cast<const uint4*>(q);
+    r.b = NT ? ld_nt16(q + 4) : *reinterpret_cast<const uint4*>(q + 4);
+  }
+  return r;
+}
+
+template <int XT, bool NT>
+__device__ __forceinline__ void store_raw8(void* __restrict__ p, int64_t off, const Raw8<XT>& r) {
+  if constexpr (XT == 0) {
+    uint16_t* q = reinterpret_cast<uint16_t*>(p) + off;
+    if constexpr (NT) st_nt16(q, r.w); else *reinterpret_cast<uint4*>(q) = r.w;
+  } else {
+    float* q = reinterpret_cast<float*>(p) + off;
+    if constexpr (NT) {
+      st_nt16(q, r.a);
+      st_nt16(q + 4, r.b);
+    } else {
+      *reinterpret_cast<uint4*>(q) = r.a;
+      *reinterpret_cast<uint4*>(q + 4) = r.b;
+    }
+  }
+}
+
+// Orders the wave's LDS accesses before and after it (a wave runs its LDS
+// instructions in order; this keeps the compiler from moving them).
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// Sum over the 64 lanes of a wave; every lane gets the result.  The order of
+// additions is fixed.
+__device__ __forceinline__ float wave_sum(float v) {
+  v += dpp_mov<kDppQuadXor1>(v);
+  v += dpp_mov<kDppQuadXor2>(v);
+  v += dpp_mov<kDppRowHalfMirror>(v);
+  v += dpp_mov<kDppRowMirror>(v);
+  v += __shfl_xor(v, 16);
+  v += __shfl_xor(v, 32);
+  return v;
+}
+
 }  // namespace fp8fg

@@ -86,4 +86,148 @@ struct ColumnPlan {
 };
 ColumnPlan plan_columns(int64_t tiles_m, int64_t N, int cus);
 
+// ------------------------------------------------- norm (norm.hip)
+struct NormArgs {
+  const void* x;
+  int x_type;          // 0 bf16, 1 f32 (also r, h, y)
+  int64_t rows, cols, ldx;
+  const void* r;       // added to x; null: none
+  int64_t ldr;
+  const void* gamma;
+  int g_type;          // 0 bf16, 1 f32
+  float eps;
+  int rule;            // 0 amax, 1 pow2
+  void* h;             // x + r; null: not stored
+  int64_t ldh;
+  void* y;             // the norm itself; null: not stored
+  int64_t ldy;
+  uint8_t* q;          // null: no quantized output
+  int64_t ldq;
+  float* s;
+  int64_t s_rs, s_ts;
+  float* rstd;         // null: not stored
+};
+hipError_t launch_norm(const NormArgs& a, hipStream_t st);
+
+struct NormGradArgs {
+  const void* dy;
+  int x_type;          // of dy, dh, h, dx
+  int64_t rows, cols, lddy;
+  const void* dh;      // added to dx; null: none
+  int64_t lddh;
+  const void* h;
+  int64_t ldh;
+  const void* gamma;
+  int g_type;
+  const float* rstd;
+  void* dx;
+  int64_t lddx;
+  float* dgamma;
+  float* partial;      // [norm_grad_strips(rows)][cols]
+};
+// Row strips of the gradient kernel, each with its own partial sum of
+// dgamma; a function of the row count alone.
+int64_t norm_grad_strips(int64_t rows);
+hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t st);
+// Widest row a workgroup holds in registers.
+constexpr int64_t kNormMaxCols = 32768;
+
+// ------------------------------------------------- router (route.hip)
+struct RouteArgs {
+  const void* logits;
+  int l_type;          // 0 bf16, 1 f32
+  int64_t rows;
+  int experts;
+  int64_t ldl;
+  const float* bias;   // null: none
+  int score;           // 0 softmax, 1 sigmoid
+  int groups, top_groups, group_top;
+  int k;
+  int renorm;
+  float scale;
+  int32_t* idx;
+  int64_t ld_idx;
+  float* w;
+  int64_t ldw;
+};
+hipError_t launch_route(const RouteArgs& a, hipStream_t st);
+
+struct RouteGradArgs {
+  const void* logits;
+  int l_type;          // of logits and dlogits
+  int64_t rows;
+  int experts;
+  int64_t ldl;
+  int score;
+  int k;
+  int renorm;
+  float scale;
+  const int32_t* idx;
+  int64_t ld_idx;
+  const float* dw;
+  int64_t lddw;
+  void* dl;
+  int64_t lddl;
+};
+hipError_t launch_route_grad(const RouteGradArgs& a, hipStream_t st);
+constexpr int64_t kRouteMaxExperts = 1024;
+constexpr int64_t kRouteMaxK = 64;
+
+// ------------------------------------------------- dispatch and combine (dispatch.hip)
+struct DispatchArgs {
+  const int32_t* idx;
+  int64_t ld_idx, tokens;
+  int k, experts;
+  const void* x;       // null: places only
+  int x_type;          // 0 bf16, 1 f32, 2 e4m3
+  int64_t cols, ldx;
+  const float* xs;     // 1x128 scales of e4m3 rows
+  int64_t xs_rs, xs_ts;
+  int32_t* offsets;
+  int32_t* pos;        // [tokens][k]
+  int32_t* token;      // [tokens * k]
+  void* out;
+  int64_t ldo;
+  float* os;
+  int64_t os_rs, os_ts;
+  int32_t* counts;     // [dispatch_chunks][experts + 1]
+};
+// Chunks of the (token, choice) list; each has its own expert counts.
+int64_t dispatch_chunks(int64_t entries);
+hipError_t launch_dispatch(const DispatchArgs& a, hipStream_t st);
+
+struct CombineArgs {
+  const void* z;
+  int type;            // 0 bf16, 1 f32: z, base, out
+  int64_t z_rows, tokens;
+  int k;
+  int64_t cols, ldz;
+  const int32_t* pos;  // [tokens][k]
+  const float* w;      // null: ones
+  int64_t ldw;
+  const void* base;    // null: none
+  int64_t ldb;
+  void* out;
+  int64_t ldo;
+};
+hipError_t launch_combine(const CombineArgs& a, hipStream_t st);
+
+struct CombineGradArgs {
+  const void* dy;
+  int type;            // dy, z, dz
+  int64_t z_rows, tokens;
+  int k;
+  int64_t cols, lddy;
+  const void* z;       // null with dw: not needed
+  int64_t ldz;
+  const int32_t* pos;
+  const float* w;      // null: ones
+  int64_t ldw;
+  void* dz;
+  int64_t lddz;
+  float* dw;           // null: not wanted
+  int64_t lddw;
+};
+hipError_t launch_combine_grad(const CombineGradArgs& a, hipStream_t st);
+
 }  // namespace fp8fg

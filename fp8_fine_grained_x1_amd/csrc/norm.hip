@@ -1,0 +1,251 @@
+// Root-mean-square norm with the residual's addition and an E4M3 output with
+// 1x128 scales, and its gradient, for gfx950.
+//
+// Forward, per row:  h = RN(x + r) in x's type,  rstd = 1 / sqrt(mean(h^2) + eps),
+//   y = (h * rstd) * gamma in fp32;  per 1x128 tile the quantizers' scale
+//   s = max(amax |y| / 448, 2^-126) (or its power of two) and
+//   q = E4M3(RN32(y / s)).  y is rounded once into each output: q comes from
+//   the fp32 value, not from the stored y.  The norm is taken of the rounded
+//   h, so that the gradient, which reads h, differentiates what was computed.
+// Backward:  xh = h * rstd,  a = dy * gamma,
+//   dx = rstd * (a - xh * mean(a * xh)) + dh,  dgamma = sum over rows dy * xh.
+//   (The quantizer is passed straight through; dh is the gradient that
+//   reaches h along the residual stream.)
+//
+// Both are bound by HBM: a row's elements are read once and stay in
+// registers, undecoded, between the statistics and the outputs.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "device_common.h"
+#include "launch.h"
+
+namespace fp8fg {
+
+namespace {
+
+constexpr int kMaxWaves = 16;
+
+// Sum over the workgroup's waves; every thread gets the result.  `part` has
+// kMaxWaves slots and is free again after the call's second barrier of the
+// next use: callers alternate between two of them.
+__device__ __forceinline__ float block_sum(float v, float* part) {
+  v = wave_sum(v);
+  const int waves = blockDim.x >> 6;
+  if (waves == 1) return v;
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+  __syncthreads();
+  float t = part[0];
+  for (int i = 1; i < waves; ++i) t += part[i];
+  return t;
+}
+
+__device__ __forceinline__ void load_gamma8(const void* __restrict__ g, int g_type, int64_t off, float v[8]) {
+  if (g_type == 0)
+    decode8<0>(load_raw8<0, false>(g, off), v);
+  else
+    decode8<1>(load_raw8<1, false>(g, off), v);
+}
+
+// One row per workgroup iteration; thread t holds the 8-element vectors
+// t, t + blockDim, ..: 16 consecutive lanes hold one 1x128 tile.
+template <int XT, int NV>
+__global__ __launch_bounds__(1024) void norm_kernel(NormArgs p) {
+  __shared__ float part[2][kMaxWaves];
+  const int nvec = (int)(p.cols >> 3);
+  int flip = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, flip ^= 1) {
+    Raw8<XT> raw[NV];
+    float ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = threadIdx.x + i * blockDim.x;
+      if (v >= nvec) continue;
+      raw[i] = load_raw8<XT, true>(p.x, row * p.ldx + v * 8);
+      if (p.r) {
+        float a[8], b[8];
+        decode8<XT>(raw[i], a);
+        load8<XT>(p.r, row * p.ldr + v * 8, b);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a[e] += b[e];
+        raw[i] = encode8<XT>(a);
+      }
+      if (p.h) store_raw8<XT, true>(p.h, row * p.ldh + v * 8, raw[i]);
+      float f[8];
+      decode8<XT>(raw[i], f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss += f[e] * f[e];
+    }
+    ss = block_sum(ss, part[flip]);
+    const float rstd = 1.0f / sqrtf(ss / (float)p.cols + p.eps);
+    if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
+    if (!p.q && !p.y) continue;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = threadIdx.x + i * blockDim.x;
+      if (v >= nvec) continue;
+      float f[8], g[8];
+      decode8<XT>(raw[i], f);
+      load_gamma8(p.gamma, p.g_type, (int64_t)v * 8, g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = f[e] * rstd * g[e];
+      if (p.y) store_raw8<XT, true>(p.y, row * p.ldy + v * 8, encode8<XT>(f));
+      if (p.q) {
+        float m = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]));
+        m = row16_max(m);
+        TileScale sc;
+        if (p.rule == 0) {
+          sc = scale_amax(m);
+          quotient8<0>(f, sc);
+        } else {
+          sc = scale_pow2(m);
+          quotient8<1>(f, sc);
+        }
+        uint2 out;
+        out.x = pack4_e4m3(f[0], f[1], f[2], f[3]);
+        out.y = pack4_e4m3(f[4], f[5], f[6], f[7]);
+        st_nt8(p.q + row * p.ldq + v * 8, out);
+        if ((threadIdx.x & 15) == 0) p.s[row * p.s_rs + (int64_t)(v >> 4) * p.s_ts] = sc.s;
+      }
+    }
+  }
+}
+
+// A workgroup takes the rows blockIdx.x, blockIdx.x + gridDim.x, ..; its
+// threads keep their columns' part of dgamma in registers and write it once.
+template <int XT, int NV>
+__global__ __launch_bounds__(1024) void norm_grad_kernel(NormGradArgs p) {
+  __shared__ float part[2][kMaxWaves];
+  const int nvec = (int)(p.cols >> 3);
+  float g[NV][8], acc[NV][8];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int v = threadIdx.x + i * blockDim.x;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) g[i][e] = acc[i][e] = 0.0f;
+    if (v < nvec) load_gamma8(p.gamma, p.g_type, (int64_t)v * 8, g[i]);
+  }
+  int flip = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, flip ^= 1) {
+    const float rstd = p.rstd[row];
+    Raw8<XT> rd[NV], rh[NV];
+    float c = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = threadIdx.x + i * blockDim.x;
+      if (v >= nvec) continue;
+      rd[i] = load_raw8<XT, true>(p.dy, row * p.lddy + v * 8);
+      rh[i] = load_raw8<XT, true>(p.h, row * p.ldh + v * 8);
+      float d[8], h[8];
+      decode8<XT>(rd[i], d);
+      decode8<XT>(rh[i], h);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float xh = h[e] * rstd;
+        c += d[e] * g[i][e] * xh;
+        acc[i][e] += d[e] * xh;
+      }
+    }
+    c = block_sum(c, part[flip]) / (float)p.cols;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = threadIdx.x + i * blockDim.x;
+      if (v >= nvec) continue;
+      float d[8], h[8], o[8];
+      decode8<XT>(rd[i], d);
+      decode8<XT>(rh[i], h);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = rstd * (d[e] * g[i][e] - h[e] * rstd * c);
+      if (p.dh) {
+        float b[8];
+        load8<XT>(p.dh, row * p.lddh + v * 8, b);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] += b[e];
+      }
+      store_raw8<XT, true>(p.dx, row * p.lddx + v * 8, encode8<XT>(o));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int v = threadIdx.x + i * blockDim.x;
+    if (v < nvec) store_raw8<1, false>(p.partial, blockIdx.x * p.cols + v * 8, encode8<1>(acc[i]));
+  }
+}
+
+// dgamma[c] = sum over the strips' partial sums, in strip order per thread
+// row, then over the 16 thread rows.
+__global__ __launch_bounds__(256) void norm_grad_sum_kernel(const float* __restrict__ partial, int strips,
+                                                            int64_t cols, float* __restrict__ dgamma) {
+  __shared__ float part[16][17];
+  const int c = threadIdx.x & 15, s0 = threadIdx.x >> 4;
+  const int64_t col = (int64_t)blockIdx.x * 16 + c;
+  float t = 0.0f;
+  if (col < cols)
+    for (int s = s0; s < strips; s += 16) t += partial[s * cols + col];
+  part[s0][c] = t;
+  __syncthreads();
+  if (s0 == 0 && col < cols) {
+#pragma unroll
+    for (int s = 1; s < 16; ++s) t += part[s][c];
+    dgamma[col] = t;
+  }
+}
+
+constexpr int64_t kMaxRowBlocks = 1 << 20;
+constexpr int64_t kGradStrips = 1024;
+
+// Vectors per thread and threads per workgroup for rows of `nvec` vectors.
+struct RowShape {
+  int nv, threads;
+};
+RowShape row_shape(int64_t nvec) {
+  const int nv = nvec <= 512 ? 1 : nvec <= 2048 ? 2 : 4;
+  const int64_t t = (nvec + nv - 1) / nv;
+  return {nv, (int)((t + 63) / 64 * 64)};
+}
+
+template <int XT>
+hipError_t norm_t(const NormArgs& a, hipStream_t st) {
+  const RowShape sh = row_shape(a.cols / 8);
+  const dim3 grid((unsigned)(a.rows < kMaxRowBlocks ? a.rows : kMaxRowBlocks)), block(sh.threads);
+  switch (sh.nv) {
+    case 1: hipLaunchKernelGGL((norm_kernel<XT, 1>), grid, block, 0, st, a); break;
+    case 2: hipLaunchKernelGGL((norm_kernel<XT, 2>), grid, block, 0, st, a); break;
+    default: hipLaunchKernelGGL((norm_kernel<XT, 4>), grid, block, 0, st, a); break;
+  }
+  return hipGetLastError();
+}
+
+template <int XT>
+hipError_t norm_grad_t(const NormGradArgs& a, hipStream_t st) {
+  const RowShape sh = row_shape(a.cols / 8);
+  const dim3 grid((unsigned)norm_grad_strips(a.rows)), block(sh.threads);
+  switch (sh.nv) {
+    case 1: hipLaunchKernelGGL((norm_grad_kernel<XT, 1>), grid, block, 0, st, a); break;
+    case 2: hipLaunchKernelGGL((norm_grad_kernel<XT, 2>), grid, block, 0, st, a); break;
+    default: hipLaunchKernelGGL((norm_grad_kernel<XT, 4>), grid, block, 0, st, a); break;
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t norm_grad_strips(int64_t rows) { return rows < kGradStrips ? rows : kGradStrips; }
+
+hipError_t launch_norm(const NormArgs& a, hipStream_t st) {
+  return a.x_type == 0 ? norm_t<0>(a, st) : norm_t<1>(a, st);
+}
+
+hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t st) {
+  if (a.rows > 0) {
+    const hipError_t e = a.x_type == 0 ? norm_grad_t<0>(a, st) : norm_grad_t<1>(a, st);
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(norm_grad_sum_kernel, dim3((unsigned)((a.cols + 15) / 16)), dim3(256), 0, st, a.partial,
+                     (int)norm_grad_strips(a.rows), a.cols, a.dgamma);
+  return hipGetLastError();
+}
+
+}  // namespace fp8fg

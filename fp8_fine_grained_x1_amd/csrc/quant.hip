@@ -65,45 +65,6 @@ __device__ __forceinline__ uint32_t fast_div(uint32_t n, const FastDiv& f) {
   return (uint32_t)(t >> f.l);
 }
 
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-
-// Non-temporal 16- and 8-byte accesses.
-__device__ __forceinline__ uint4 ld_nt16(const void* p) {
-  const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
-  return make_uint4(v[0], v[1], v[2], v[3]);
-}
-__device__ __forceinline__ uint2 ld_nt8(const void* p) {
-  const u32x2 v = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p));
-  return make_uint2(v[0], v[1]);
-}
-__device__ __forceinline__ void st_nt8(void* p, uint2 v) {
-  const u32x2 w = {v.x, v.y};
-  __builtin_nontemporal_store(w, reinterpret_cast<u32x2*>(p));
-}
-__device__ __forceinline__ void st_nt16(void* p, uint4 v) {
-  const u32x4 w = {v.x, v.y, v.z, v.w};
-  __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(p));
-}
-
-template <int XT>
-__device__ __forceinline__ void load8(const void* __restrict__ x, int64_t off, float v[8]) {
-  if constexpr (XT == 0) {
-    const uint4 w = ld_nt16(reinterpret_cast<const uint16_t*>(x) + off);
-    v[0] = bf16_lo(w.x); v[1] = bf16_hi(w.x);
-    v[2] = bf16_lo(w.y); v[3] = bf16_hi(w.y);
-    v[4] = bf16_lo(w.z); v[5] = bf16_hi(w.z);
-    v[6] = bf16_lo(w.w); v[7] = bf16_hi(w.w);
-  } else {
-    const float* p = reinterpret_cast<const float*>(x) + off;
-    const uint4 a = ld_nt16(p), b = ld_nt16(p + 4);
-    v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y);
-    v[2] = __uint_as_float(a.z); v[3] = __uint_as_float(a.w);
-    v[4] = __uint_as_float(b.x); v[5] = __uint_as_float(b.y);
-    v[6] = __uint_as_float(b.z); v[7] = __uint_as_float(b.w);
-  }
-}
-
 // Lane group g of the grid handles tiles g, g + G, ... (G = number of lane
 // groups), two per iteration so that both loads are in flight before either
 // is processed.  ORDER 0 numbers the tiles row-major (t = r * tiles_per_row

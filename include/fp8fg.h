@@ -25,10 +25,14 @@
  *   - Sizes and strides are in ELEMENTS of the pointed-to type.
  *   - FP8 is OCP E4M3 (bias 7, largest finite 448, no infinity); bytes are
  *     produced with round-to-nearest-even and saturation.
+ *   - Scratch memory is the caller's too: an entry point that needs some has a
+ *     ..._workspace function that gives its size in bytes (0 for arguments
+ *     that it would refuse).
  *   - Return value: FP8FG_OK (0) or an error code.  On any error other than
  *     FP8FG_ELAUNCH nothing was enqueued.  FP8FG_ELAUNCH reports a HIP
  *     launch failure after enqueue (the stream state is then undefined).
- *   - Inputs must be finite; results for NaN/Inf inputs are unspecified.
+ *   - Inputs must be finite, except where an entry point says what it does
+ *     with others; results for NaN/Inf inputs are unspecified.
  *   - Outputs must not alias inputs.
  *   - Calls are thread-safe; the only global state is a per-device cache of
  *     the compute-unit count, filled once.
@@ -65,6 +69,8 @@ enum { FP8FG_TILE_1x128 = 0, FP8FG_TILE_128x1 = 1 };
 enum { FP8FG_SCALE_AMAX = 0, FP8FG_SCALE_POW2 = 1 };
 /* how the B operand of the GEMM is scaled along N */
 enum { FP8FG_BSCALE_BLOCK128 = 0, FP8FG_BSCALE_COL = 1 };
+/* score of the router */
+enum { FP8FG_SCORE_SOFTMAX = 0, FP8FG_SCORE_SIGMOID = 1 };
 /* GEMM flags (bit set) */
 enum {
   FP8FG_GEMM_DEFAULT = 0,
@@ -229,7 +235,9 @@ FP8FG_API int fp8_gemm_blockscaled(int64_t M, int64_t N, int64_t K, const uint8_
  *   offsets : DEVICE int32 [G + 1]; expert e owns rows [offsets[e],
  *             offsets[e+1]) of a and c.  Caller contract (not checked --
  *             that would need a synchronization): offsets[0] == 0,
- *             nondecreasing, offsets[G] == M_total.  Empty experts are legal.
+ *             nondecreasing, offsets[G] <= M_total.  Empty experts are
+ *             legal.  Rows of c from offsets[G] on (fp8_dispatch puts its
+ *             dropped entries there) are not written.
  *   b_e  = b + e * b_gs   ([N][K], K contiguous, pitch ldb)
  *   sb_e = sb + e * sb_gs (128x128 block scales, indexed as BLOCK128 above)
  *   Other arguments as for fp8_gemm_blockscaled (B scaling is BLOCK128).
@@ -246,6 +254,172 @@ FP8FG_API int fp8_grouped_gemm_blockscaled(int64_t G, const int32_t* offsets,
                                  const float* sb, int64_t sb_ns, int64_t sb_ks,
                                  int64_t sb_gs, void* c, int c_type,
                                  int64_t ldc, int flags, void* stream);
+
+/*
+ * fp8_rmsnorm_quantize -- root-mean-square norm with the residual's addition
+ * and an E4M3 output in 1x128 tiles: the producer of the activations that
+ * the GEMMs read ([why-be], [thedaegu]: every GEMM input is quantized per
+ * 1x128 tile), without the bf16 tensor in between.
+ *
+ *   h[m][c]  = RN(x[m][c] + r[m][c]) in x_type (h = x where r is null)
+ *   rstd[m]  = 1 / sqrt(sum_c h^2 / cols + eps)
+ *   y[m][c]  = (h * rstd) * gamma[c], in fp32
+ *   s, q     = the 1x128 scale and E4M3 bytes of the fp32 y, by the rules of
+ *              fp8_quantize_rowtile
+ *
+ *   x, r, h, y : x_type BF16 or F32 with row pitches ldx, ldr, ldh, ldy.
+ *            r may be null (nothing is added).  h may be null (not stored);
+ *            so may y (the norm rounded to x_type), q with s (no quantized
+ *            output) and rstd.
+ *   gamma    : [cols], g_type BF16 or F32.  eps >= 0, finite.
+ *   Requires cols % 128 == 0.  rows == 0 or cols == 0 is a valid no-op.
+ *   Alignment: x, r, h, y, gamma, q 16-byte aligned, their pitches multiples
+ *   of 16 bytes; s and rstd 4-byte aligned.
+ *   Limits (FP8FG_EUNSUPPORTED): cols <= 32768 (a row stays in one
+ *   workgroup's registers).
+ */
+FP8FG_API int fp8_rmsnorm_quantize(const void* x, int x_type, int64_t rows, int64_t cols,
+                         int64_t ldx, const void* r, int64_t ldr, const void* gamma,
+                         int g_type, float eps, int scale_rule, void* h, int64_t ldh,
+                         void* y, int64_t ldy, uint8_t* q, int64_t ldq, float* s,
+                         int64_t s_rs, int64_t s_ts, float* rstd, void* stream);
+
+/*
+ * fp8_rmsnorm_backward -- gradient of the norm above, passed straight
+ * through the quantizer.
+ *
+ *   xh = h * rstd,  a = dy * gamma,  dx = rstd * (a - xh * mean_c(a * xh)) + dh
+ *   dgamma[c] = sum_m dy * xh
+ *
+ *   dy, dh, h, dx : x_type, as above.  dh (the gradient reaching h along the
+ *            residual stream) may be null.  dx is the gradient of both x and
+ *            r.
+ *   rstd     : as the forward stored it.
+ *   dgamma   : fp32 [cols], overwritten (zeros for rows == 0).
+ *   workspace: at least fp8_rmsnorm_backward_workspace(rows, cols) bytes,
+ *            16-byte aligned: partial sums of dgamma, added in a fixed
+ *            order.  FP8FG_ESHAPE if workspace_bytes is less.
+ *   Requires cols % 8 == 0.  Alignment and limits as above.
+ */
+FP8FG_API int64_t fp8_rmsnorm_backward_workspace(int64_t rows, int64_t cols);
+FP8FG_API int fp8_rmsnorm_backward(const void* dy, int x_type, int64_t rows, int64_t cols,
+                         int64_t lddy, const void* dh, int64_t lddh, const void* h,
+                         int64_t ldh, const void* gamma, int g_type,
+                         const float* rstd, void* dx, int64_t lddx, float* dgamma,
+                         void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * fp8_route -- the experts of each token and their weights: [thedaegu]
+ * passages on the gating of routed experts and on the bias that balances
+ * their load without an auxiliary loss.
+ *
+ *   logits : [rows][experts], l_type BF16 or F32, row pitch ldl.  A logit of
+ *            -inf or NaN masks its expert.
+ *   score  : s = softmax or sigmoid of the logits, to fp32.
+ *   bias   : fp32 [experts] or null, added to s for the choice alone:
+ *            c = s + bias (a NaN masks the expert).
+ *   groups : the experts form `groups` equal runs.  If top_groups < groups,
+ *            only the experts of the top_groups groups with the largest sums
+ *            of their group_top (1 or 2) best c are candidates.
+ *   k      : idx[m][0..k) are the candidates with the largest c, in
+ *            descending order.  On equal values the lower index comes first,
+ *            of groups as of experts.
+ *   w      : scale * s, divided by the sum of the chosen s if renorm is 1
+ *            (0 where that sum is 0).
+ *   A masked expert is never chosen: with fewer candidates than k the last
+ *   slots are idx = -1, w = 0.
+ *   Requires 1 <= k <= experts, groups dividing experts, 1 <= top_groups <=
+ *   groups, scale finite.  No alignment beyond the element's.
+ *   Limits (FP8FG_EUNSUPPORTED): experts <= 1024, k <= 64.
+ */
+FP8FG_API int fp8_route(const void* logits, int l_type, int64_t rows, int64_t experts,
+              int64_t ldl, const float* bias, int score, int64_t groups,
+              int64_t top_groups, int group_top, int64_t k, int renorm, float scale,
+              int32_t* idx, int64_t ld_idx, float* w, int64_t ldw, void* stream);
+
+/*
+ * fp8_route_backward -- gradient of fp8_route's weights with respect to the
+ * logits (the choice itself is constant, and the bias has no gradient).
+ *
+ *   idx    : the forward's indexes; entries outside [0, experts) have no
+ *            part.  A row's other entries must be distinct.
+ *   dw     : [rows][k] fp32, row pitch lddw.
+ *   dlogits: [rows][experts] of l_type, row pitch lddl, overwritten.
+ *   Other arguments and limits as for fp8_route.
+ */
+FP8FG_API int fp8_route_backward(const void* logits, int l_type, int64_t rows, int64_t experts,
+                       int64_t ldl, int score, int64_t k, int renorm, float scale,
+                       const int32_t* idx, int64_t ld_idx, const float* dw,
+                       int64_t lddw, void* dlogits, int64_t lddl, void* stream);
+
+/*
+ * fp8_dispatch -- rows into expert order: the sorted activations and the
+ * offsets that fp8_grouped_gemm_blockscaled takes ([hearaon]: activations
+ * are quantized before they are dispatched to the experts).
+ *
+ *   idx    : DEVICE int32 [tokens][k], row pitch ld_idx: entry (t, j) goes to
+ *            expert idx[t][j]; an index outside [0, experts) drops it.
+ *   The entries are ordered by expert, within an expert by (t, j), dropped
+ *   ones last.  Entry (t, j) being the r-th:
+ *   offsets: int32 [experts + 1], entries of the experts below e; the last
+ *            one counts the entries that are not dropped.
+ *   pos    : int32 [tokens][k], contiguous: r, or -2 - r for a dropped entry.
+ *   token  : int32 [tokens * k]: token[r] = t, or -1 for a dropped entry.
+ *   x      : [tokens][cols] of x_type E4M3 (with 1x128 scales xs), BF16 or
+ *            F32 (xs, os ignored), or null: the places alone.
+ *   out, os: [tokens * k][cols] and its scales: out[r] = x[t]; zero bytes and
+ *            the scale 2^-126 for a dropped entry.
+ *   workspace: at least fp8_dispatch_workspace(tokens, k, experts) bytes,
+ *            4-byte aligned; FP8FG_ESHAPE if workspace_bytes is less.
+ *   Requires k >= 1, experts >= 1; with x, cols a multiple of 128 (E4M3) or
+ *   8.  tokens == 0 writes zero offsets.
+ *   Alignment: x, out 16-byte aligned, pitches multiples of 16 bytes; idx,
+ *   offsets, pos, token, xs, os 4-byte aligned.
+ *   Limits (FP8FG_EUNSUPPORTED): tokens * k <= 2^31 - 3 (the rows are int32),
+ *   experts <= 1024, cols <= 2^28.
+ */
+FP8FG_API int64_t fp8_dispatch_workspace(int64_t tokens, int64_t k, int64_t experts);
+FP8FG_API int fp8_dispatch(const int32_t* idx, int64_t ld_idx, int64_t tokens, int64_t k,
+                 int64_t experts, const void* x, int x_type, int64_t cols, int64_t ldx,
+                 const float* xs, int64_t xs_rs, int64_t xs_ts, int32_t* offsets,
+                 int32_t* pos, int32_t* token, void* out, int64_t ldo, float* os,
+                 int64_t os_rs, int64_t os_ts, void* workspace, int64_t workspace_bytes,
+                 void* stream);
+
+/*
+ * fp8_combine -- the experts' rows back in token order.
+ *
+ *   out[t][c] = base[t][c] + sum_j w[t][j] * z[pos[t][j]][c], in fp32 in the
+ *   order of j, rounded once to `type`; places outside [0, z_rows) have no
+ *   part (their rows are not read).
+ *   z, base, out: type BF16 or F32; base may be null (nothing is added), w
+ *            too (ones: the gradient of fp8_dispatch).
+ *   pos    : int32 [tokens][k], contiguous.
+ *   Requires k >= 1, cols % 8 == 0.  Alignment: z, base, out 16-byte aligned,
+ *   pitches multiples of 16 bytes; pos and w 4-byte aligned.
+ *   Limits (FP8FG_EUNSUPPORTED): z_rows, tokens, k <= 2^31 - 1, cols <= 2^28.
+ */
+FP8FG_API int fp8_combine(const void* z, int type, int64_t z_rows, int64_t tokens, int64_t k,
+                int64_t cols, int64_t ldz, const int32_t* pos, const float* w,
+                int64_t ldw, const void* base, int64_t ldb, void* out, int64_t ldo,
+                void* stream);
+
+/*
+ * fp8_combine_backward -- gradients of fp8_combine's z and w (base's is dy).
+ *
+ *   dz[pos[t][j]] = w[t][j] * dy[t],  dw[t][j] = sum_c dy[t][c] * z[pos[t][j]][c]
+ *   for places in [0, z_rows); otherwise dw = 0, and if -2 - pos[t][j] is in
+ *   [0, z_rows) (an entry that fp8_dispatch dropped) that row of dz is zeroed.
+ *   With the places of one fp8_dispatch and z_rows = tokens * k every row of
+ *   dz is written; rows that no place names are left as they are.  The
+ *   places must be distinct.
+ *   dw may be null (then z may be too); w may be null (ones).
+ *   Other arguments, alignment and limits as for fp8_combine.
+ */
+FP8FG_API int fp8_combine_backward(const void* dy, int type, int64_t z_rows, int64_t tokens,
+                         int64_t k, int64_t cols, int64_t lddy, const void* z,
+                         int64_t ldz, const int32_t* pos, const float* w, int64_t ldw,
+                         void* dz, int64_t lddz, float* dw, int64_t lddw, void* stream);
 
 /* Static, thread-safe description of a status code. */
 FP8FG_API const char* fp8fg_status_string(int status);

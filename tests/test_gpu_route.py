@@ -1,0 +1,211 @@
+"""GPU parity of the router and its gradient against the 64-bit oracle.
+
+The indexes have to be the oracle's exactly: scores are rounded once to
+fp32, choices are one fp32 addition, ties go to the lower index.
+
+Tolerances (u = 2^-24): weights: k <= 64 additions of positive scores, their
+own rounding, a quotient and a product: 70 u relative.  Gradient: with the
+fp32 exponential within 2 ulp and at most 1024 / 64 + 6 additions on any
+term, |err| <= 64 u (|v_e| + sum_i |v_i| s_i) s_e (scores normalised as in the
+formula), then the type's rounding."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import moe
+from fp8_fine_grained_x1_amd import tensors as T
+from gpu_util import DEV, say
+
+pytestmark = pytest.mark.gpu
+
+U, UB = 2.0 ** -24, 2.0 ** -8
+TYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def dev(x, dtype=torch.float32):
+    return torch.from_numpy(np.ascontiguousarray(x, dtype=np.float32)).to(DEV).to(dtype)
+
+
+def check(l, k, dtype="f32", **kw):
+    l = moe.round_to(l, dtype == "bf16")
+    bias = kw.pop("bias", None)
+    idx, w = T.route(dev(l, TYPES[dtype]), k, bias=None if bias is None else dev(bias), **kw)
+    io, wo = moe.route(l, k, bias=bias, **kw)
+    got = idx.cpu().numpy()
+    bad = np.flatnonzero(np.any(got != io, axis=1))
+    assert bad.size == 0, (bad[:4], got[bad[:2]], io[bad[:2]])
+    assert np.all(np.abs(w.cpu().numpy() - wo) <= 70 * U * np.abs(wo) + 1e-37)
+    return l, io
+
+
+# experts, k, groups, top_groups, group_top
+SHAPES = [(1, 1, 1, 1, 2), (2, 2, 2, 1, 1), (8, 2, 1, 1, 2), (16, 8, 1, 1, 2), (60, 4, 1, 1, 2), (64, 6, 8, 3, 1),
+          (65, 5, 5, 2, 2), (72, 8, 8, 4, 2), (128, 8, 4, 4, 2), (160, 6, 8, 3, 1), (192, 8, 6, 2, 2),
+          (252, 7, 6, 3, 2), (256, 8, 8, 4, 2), (256, 1, 64, 5, 2), (257, 64, 1, 1, 2), (300, 8, 100, 9, 2),
+          (384, 8, 1, 1, 2), (512, 10, 16, 4, 2), (1000, 33, 8, 7, 2), (1024, 64, 1024, 100, 2), (1024, 8, 2, 1, 1)]
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "E%d_k%d_g%d_%d_%d" % s)
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_route(shape, score):
+    E, k, groups, top_groups, group_top = shape
+    say("route %s %s" % (shape, score))
+    rng = np.random.default_rng(E + k)
+    for rows, dtype, with_bias, renorm in ((1, "f32", True, True), (67, "bf16", False, True), (130, "f32", True, False)):
+        l = rng.standard_normal((rows, E)) * 2
+        bias = (rng.standard_normal(E) * 0.1).astype(np.float32) if with_bias else None
+        check(l, k, dtype, bias=bias, score=score, groups=groups, top_groups=top_groups, group_top=group_top,
+              renorm=renorm, scale=2.5)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("groups,top_groups", [(1, 1), (8, 3)])
+def test_ties_go_to_the_lower_index(score, groups, top_groups):
+    rng = np.random.default_rng(5)
+    l = np.round(rng.standard_normal((64, 96)))
+    l[0] = 0.0
+    check(l, 12, score=score, groups=groups, top_groups=top_groups)
+    check(l, 12, score=score, groups=groups, top_groups=top_groups, bias=np.zeros(96, np.float32) - np.float32(0))
+    check(l, 12, score=score, groups=groups, top_groups=top_groups, group_top=1,
+          bias=(np.round(rng.standard_normal(96)) / 4).astype(np.float32))
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,groups,top_groups", [(40, 1, 1), (40, 8, 3), (160, 4, 2), (320, 8, 2)])
+def test_masks_and_extreme_logits(score, E, groups, top_groups):
+    rng = np.random.default_rng(E)
+    low = float(np.finfo(np.float32).min)
+    rows = []
+    base = rng.standard_normal((12, E))
+    rows.append(np.full(E, -np.inf))                      # nothing left
+    rows.append(np.full(E, np.nan))
+    rows.append(np.full(E, low))                          # numbers all the same
+    rows.append(np.full(E, np.inf))
+    for i, v in enumerate((-np.inf, np.nan, low, np.inf)):
+        a = base[i].copy()
+        a[rng.permutation(E)[: E - 3]] = v                # three ordinary ones
+        rows.append(a)
+        a = base[i + 4].copy()
+        a[rng.permutation(E)[:2]] = v
+        rows.append(a)
+    a = np.full(E, -np.inf)
+    a[E - 1] = 0.5                                        # one candidate, in the last group
+    rows.append(a)
+    a = base[9] * 200                                     # scores that underflow
+    rows.append(a)
+    a = np.full(E, -np.inf)
+    a[: E // max(groups, 2)] = base[10][: E // max(groups, 2)]  # whole groups masked
+    rows.append(a)
+    l = np.stack(rows)
+    bias = (rng.standard_normal(E) * 0.1).astype(np.float32)
+    with np.errstate(all="ignore"):
+        for renorm in (False, True):
+            for b in (None, bias):
+                check(l, 6, score=score, groups=groups, top_groups=top_groups, renorm=renorm, bias=b)
+    nb = bias.copy()
+    nb[3], nb[7], nb[9] = np.nan, -np.inf, np.inf
+    check(base, 6, score=score, groups=groups, top_groups=top_groups, bias=nb)
+
+
+def test_near_scores_are_told_apart():
+    # choices one fp32 step apart, reached through the score's rounding: the
+    # bias undoes all but the last bits of the score
+    rng = np.random.default_rng(6)
+    l = (rng.standard_normal((400, 64))).astype(np.float32)
+    for row in range(0, 400, 8):
+        s = moe.scores(l[row], "sigmoid").astype(np.float32)
+        check(l[row:row + 8], 8, score="sigmoid", bias=(np.float32(1.0) - s))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_strides_and_rows(dtype):
+    rng = np.random.default_rng(7)
+    wide = moe.round_to(rng.standard_normal((33, 200)), dtype == "bf16")
+    d = dev(wide, TYPES[dtype])
+    for E, at in ((100, 3), (64, 1), (129, 7)):
+        idx, w = T.route(d[:, at:at + E], 5)
+        io, wo = moe.route(wide[:, at:at + E], 5)
+        assert np.array_equal(idx.cpu().numpy(), io)
+        dl = T.route_backward(torch.ones_like(w), d[:, at:at + E], idx, renorm=False)
+        dc = T.route_backward(torch.ones_like(w), d[:, at:at + E].contiguous(), idx, renorm=False)
+        assert torch.equal(dl, dc)
+    idx, w = T.route(d[:0], 5)
+    assert idx.shape == (0, 5) and w.shape == (0, 5)
+    assert T.route_backward(w, d[:0], idx).shape == (0, 200)
+
+
+@pytest.mark.parametrize("E,k", [(1, 1), (8, 2), (60, 4), (64, 64), (65, 5), (160, 6), (256, 8), (257, 33), (1000, 8),
+                                 (1024, 64)])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gradient(E, k, score, renorm, dtype):
+    rng = np.random.default_rng(E + k)
+    rows = 29
+    l = moe.round_to(rng.standard_normal((rows, E)) * 2, dtype == "bf16")
+    idx = np.stack([rng.permutation(E)[:k] for _ in range(rows)]).astype(np.int32)
+    idx[3, k // 2:] = -1
+    idx[4, :] = -1
+    idx[5, 0] = E
+    if E > 4:
+        l[6, rng.permutation(E)[: E // 2]] = -np.inf
+        l[7, 2] = np.nan
+        l[8, 1] = np.inf
+        l[9] = -np.inf
+        l[10] = np.finfo(np.float32).min if dtype == "f32" else -3.0e38
+    l = moe.round_to(l, dtype == "bf16")
+    dw = rng.standard_normal((rows, k)).astype(np.float32)
+    got = T.route_backward(dev(dw), dev(l, TYPES[dtype]), torch.from_numpy(idx).to(DEV), score=score, renorm=renorm,
+                           scale=1.5).float().cpu().numpy()
+    with np.errstate(all="ignore"):
+        ref = moe.route_grad(dw, l, idx, score=score, renorm=renorm, scale=1.5)
+    size = np.zeros((rows, E))
+    for t in range(rows):
+        keep = [j for j in range(k) if 0 <= idx[t, j] < E]
+        at = idx[t, keep]
+        v = np.zeros(E)
+        v[at] = np.abs(dw[t, keep]) * 1.5
+        if renorm:
+            s = np.zeros(E)
+            if score == "softmax":
+                s[at] = moe.scores(l[t, at], "softmax")
+            else:
+                s[at] = moe.scores(l[t], score)[at]
+                s = s / max(s.sum(), 1e-300)
+            size[t, at] = (s * (v + np.sum(v * s)))[at]
+        else:
+            s = moe.scores(l[t], score)
+            size[t] = s * (v + (np.sum(v * s) if score == "softmax" else 0))
+    tol = 64 * U * size + (UB * np.abs(ref) if dtype == "bf16" else 0) + 1e-37
+    bad = np.argwhere(~(np.abs(got - ref) <= tol))
+    assert bad.size == 0, [(int(t), int(e), got[t, e], ref[t, e]) for t, e in bad[:5]]
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_gradient_against_differences_of_the_kernel(score, renorm):
+    # loss = sum of w dw over the kernel's own weights; a wide gap around the
+    # k-th expert keeps the choice constant
+    rng = np.random.default_rng(9)
+    rows, E, k = 6, 24, 4
+    l = rng.standard_normal((rows, E)).astype(np.float32) * 0.5
+    for t in range(rows):
+        l[t, rng.permutation(E)[:k]] += 2.5
+    dw = rng.standard_normal((rows, k))
+    idx, w = T.route(dev(l), k, score=score, renorm=renorm, scale=1.3)
+
+    def loss(a):
+        i, v = T.route(dev(a), k, score=score, renorm=renorm, scale=1.3)
+        v = v.cpu().numpy().astype(np.float64)
+        order = np.argsort(i.cpu().numpy(), axis=1)
+        assert np.array_equal(np.take_along_axis(i.cpu().numpy(), order, 1), np.sort(idx.cpu().numpy(), axis=1))
+        first = np.argsort(idx.cpu().numpy(), axis=1)
+        return np.sum(np.take_along_axis(v, order, 1) * np.take_along_axis(dw, first, 1))
+
+    dl = T.route_backward(dev(dw), dev(l), idx, score=score, renorm=renorm, scale=1.3).cpu().numpy().astype(np.float64)
+    noise = 2.0 ** -20 * np.sum(np.abs(dw) * w.cpu().numpy())
+    for _ in range(4):
+        v = rng.uniform(-1, 1, (rows, E))
+        diff = [(loss(l + d * v) - loss(l - d * v)) / (2 * d) for d in (2.0 ** -4, 2.0 ** -5)]
+        assert abs(diff[1] - np.sum(dl * v)) <= abs(diff[0] - diff[1]) + noise / 2.0 ** -5 + 2.0 ** -20
