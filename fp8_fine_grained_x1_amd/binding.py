@@ -13,7 +13,6 @@ there is no fallback: if the library is missing, the import of its handle
 raises.
 """
 
-import contextlib
 import ctypes
 import os
 
@@ -101,21 +100,17 @@ def status_string(status):
     return lib().fp8fg_status_string(int(status)).decode()
 
 
-def _is_tensor(x):
-    return hasattr(x, "data_ptr") and hasattr(x, "device")
-
-
 def _ptr(x):
-    if x is None:
-        return None
-    if _is_tensor(x):
+    if x is None or type(x) is int:
+        return x
+    if hasattr(x, "data_ptr"):
         return x.data_ptr()
     return int(x)
 
 
 def _cuda_device(args):
     for a in args:
-        if _is_tensor(a) and a.device.type == "cuda":
+        if getattr(a, "is_cuda", False):
             return a.device
     return None
 
@@ -125,27 +120,27 @@ def _stream(stream, device):
         if device is None:
             return None
         import torch
-        return torch.cuda.current_stream(device).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(device.index)
     if hasattr(stream, "cuda_stream"):
         return stream.cuda_stream
     return int(stream)
 
 
-@contextlib.contextmanager
-def _on(device):
-    if device is None:
-        yield
-        return
-    import torch
-    with torch.cuda.device(device):
-        yield
-
-
 def _call(name, check, ptr_args, build):
+    # A call costs a few microseconds of host time, which is what the calls
+    # on few rows take altogether: the device is made current only where it
+    # is not already.
     dev = _cuda_device(ptr_args)
-    with _on(dev):
-        st = build(dev)
-        rc = getattr(lib(), name)(*st)
+    fn = getattr(_lib or lib(), name)
+    if dev is None:
+        rc = fn(*build(None))
+    else:
+        import torch
+        if torch.cuda.current_device() == dev.index:
+            rc = fn(*build(dev))
+        else:
+            with torch.cuda.device(dev):
+                rc = fn(*build(dev))
     if check and rc != FP8FG_OK:
         raise Fp8fgError(rc, name)
     return rc

@@ -46,7 +46,7 @@ def _rule(pow2):
 def _scales(rows, groups, layout, device):
     """Scale tensor indexed [row][group]."""
     if layout == "group_major":
-        return torch.empty((groups, rows), dtype=torch.float32, device=device).t()
+        return torch.empty_strided((rows, groups), (1, rows), dtype=torch.float32, device=device)
     if layout == "row_major":
         return torch.empty((rows, groups), dtype=torch.float32, device=device)
     raise ValueError("scale_layout must be 'group_major' or 'row_major'")
@@ -143,6 +143,15 @@ def _need(ok, what):
         raise ValueError(what)
 
 
+def _alloc(rows, cols, dtype, device):
+    # empty_strided is the cheapest of torch's allocating calls
+    return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
+
+
+def _alloc1(n, dtype, device):
+    return torch.empty_strided((n,), (1,), dtype=dtype, device=device)
+
+
 def _rows2d(name, x, like=None, dtypes=None):
     """x is a 2-d GPU tensor with contiguous rows, where `like` is given of
     its shape, type and device."""
@@ -183,11 +192,11 @@ def rmsnorm_quantize(x, gamma, residual=None, eps=1e-6, pow2=False, scale_layout
     if residual is not None:
         _rows2d("residual", residual, like=x)
     dev = x.device
-    q = torch.empty((M, C), dtype=torch.uint8, device=dev)
+    q = _alloc(M, C, torch.uint8, dev)
     s = _scales(M, C // 128, scale_layout, dev)
-    h = x if residual is None else torch.empty((M, C), dtype=x.dtype, device=dev)
-    y = torch.empty((M, C), dtype=x.dtype, device=dev) if want_y else None
-    rstd = torch.empty(M, dtype=torch.float32, device=dev)
+    h = x if residual is None else _alloc(M, C, x.dtype, dev)
+    y = _alloc(M, C, x.dtype, dev) if want_y else None
+    rstd = _alloc1(M, torch.float32, dev)
     B.fp8_rmsnorm_quantize(x, _XTYPE[x.dtype], M, C, _pitch(x), residual,
                            0 if residual is None else _pitch(residual), gamma, _XTYPE[gamma.dtype],
                            eps, _rule(pow2), None if residual is None else h, C, y, C, q, C, s,
@@ -208,10 +217,10 @@ def rmsnorm_backward(dy, h, gamma, rstd, dh=None, stream=None):
           gamma.device == h.device, "gamma must be a contiguous vector of the columns")
     _need(rstd.shape == (M,) and rstd.dtype == torch.float32 and rstd.is_contiguous() and rstd.device == h.device,
           "rstd must be a contiguous f32 vector of the rows")
-    dx = torch.empty((M, C), dtype=h.dtype, device=h.device)
-    dgamma = torch.empty(C, dtype=torch.float32, device=h.device)
+    dx = _alloc(M, C, h.dtype, h.device)
+    dgamma = _alloc1(C, torch.float32, h.device)
     n = B.fp8_rmsnorm_backward_workspace(M, C)
-    ws = torch.empty(max(n, 16), dtype=torch.uint8, device=h.device)
+    ws = _alloc1(max(n, 16), torch.uint8, h.device)
     B.fp8_rmsnorm_backward(dy, _XTYPE[h.dtype], M, C, _pitch(dy), dh, 0 if dh is None else _pitch(dh), h,
                            _pitch(h), gamma, _XTYPE[gamma.dtype], rstd, dx, C, dgamma, ws, n, stream)
     _on_stream(stream, dx, dgamma, ws)
@@ -231,8 +240,8 @@ def route(logits, k, bias=None, score="softmax", groups=1, top_groups=1, group_t
     if bias is not None:
         _need(bias.shape == (E,) and bias.dtype == torch.float32 and bias.is_contiguous() and
               bias.device == logits.device, "bias must be a contiguous f32 vector of the experts")
-    idx = torch.empty((M, k), dtype=torch.int32, device=logits.device)
-    w = torch.empty((M, k), dtype=torch.float32, device=logits.device)
+    idx = _alloc(M, k, torch.int32, logits.device)
+    w = _alloc(M, k, torch.float32, logits.device)
     B.fp8_route(logits, _XTYPE[logits.dtype], M, E, _pitch(logits), bias, _SCORE[score], groups,
                 top_groups, group_top, k, int(renorm), scale, idx, k, w, k, stream)
     _on_stream(stream, idx, w)
@@ -249,7 +258,7 @@ def route_backward(dw, logits, idx, score="softmax", renorm=True, scale=1.0, str
     k = idx.shape[1]
     _need(idx.shape == (M, k) and dw.shape == (M, k) and idx.device == logits.device and dw.device == logits.device,
           "idx and dw must be [tokens][k] on the logits' device")
-    dl = torch.empty((M, E), dtype=logits.dtype, device=logits.device)
+    dl = _alloc(M, E, logits.dtype, logits.device)
     B.fp8_route_backward(logits, _XTYPE[logits.dtype], M, E, _pitch(logits), _SCORE[score], k, int(renorm),
                          scale, idx, _pitch(idx), dw, _pitch(dw), dl, E, stream)
     _on_stream(stream, dl)
@@ -277,12 +286,12 @@ def dispatch(idx, experts, x, s=None, scale_layout="group_major", stream=None):
         _need(s.shape == (M, C // 128) and s.dtype == torch.float32 and s.device == dev,
               "s must be the f32 [tokens][columns / 128] scales of x")
         out_s = _scales(M * k, C // 128, scale_layout, dev)
-    out = torch.empty((M * k, C), dtype=x.dtype, device=dev)
-    offsets = torch.empty(experts + 1, dtype=torch.int32, device=dev)
-    pos = torch.empty((M, k), dtype=torch.int32, device=dev)
-    token = torch.empty(M * k, dtype=torch.int32, device=dev)
+    out = _alloc(M * k, C, x.dtype, dev)
+    offsets = _alloc1(experts + 1, torch.int32, dev)
+    pos = _alloc(M, k, torch.int32, dev)
+    token = _alloc1(M * k, torch.int32, dev)
     n = B.fp8_dispatch_workspace(M, k, experts)
-    ws = torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
+    ws = _alloc1(max(n, 16), torch.uint8, dev)
     st = (s.stride(0), s.stride(1), out_s.stride(0), out_s.stride(1)) if e4m3 else (0, 0, 0, 0)
     B.fp8_dispatch(idx, _pitch(idx), M, k, experts, x, _MOVE[x.dtype], C, _pitch(x), s, st[0], st[1],
                    offsets, pos, token, out, C, out_s, st[2], st[3], ws, n, stream)
@@ -305,7 +314,7 @@ def combine(z, pos, w=None, base=None, stream=None):
     _check_places(pos, w, z)
     M, k = pos.shape
     R, C = z.shape
-    out = torch.empty((M, C), dtype=z.dtype, device=z.device)
+    out = _alloc(M, C, z.dtype, z.device)
     if base is not None:
         _rows2d("base", base, like=out)
     B.fp8_combine(z, _XTYPE[z.dtype], R, M, k, C, _pitch(z), pos, w, 0 if w is None else _pitch(w),
@@ -325,8 +334,8 @@ def combine_backward(dy, z, pos, w, stream=None):
     _need(dy.shape == (M, C) and dy.dtype == z.dtype and dy.device == z.device,
           "dy must be [tokens][columns] of z's type and device")
     _need(R == M * k, "z must have tokens * k rows")
-    dz = torch.empty((R, C), dtype=z.dtype, device=z.device)
-    dw = torch.empty((M, k), dtype=torch.float32, device=z.device)
+    dz = _alloc(R, C, z.dtype, z.device)
+    dw = _alloc(M, k, torch.float32, z.device)
     B.fp8_combine_backward(dy, _XTYPE[z.dtype], R, M, k, C, _pitch(dy), z, _pitch(z), pos, w,
                            0 if w is None else _pitch(w), dz, C, dw, k, stream)
     _on_stream(stream, dz, dw)
