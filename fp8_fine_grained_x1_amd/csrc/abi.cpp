@@ -299,7 +299,7 @@ int fp8_rmsnorm_quantize(const void* x, int x_type, int64_t rows, int64_t cols, 
 
 int64_t fp8_rmsnorm_backward_workspace(int64_t rows, int64_t cols) {
   if (rows < 0 || cols < 0 || cols > fp8fg::kNormMaxCols) return 0;
-  return fp8fg::norm_grad_strips(rows) * cols * (int64_t)sizeof(float);
+  return fp8fg::norm_grad_strips(rows, cols) * cols * (int64_t)sizeof(float);
 }
 
 int fp8_rmsnorm_backward(const void* dy, int x_type, int64_t rows, int64_t cols, int64_t lddy,
@@ -373,7 +373,7 @@ int fp8_route_backward(const void* logits, int l_type, int64_t rows, int64_t exp
 
 int64_t fp8_dispatch_workspace(int64_t tokens, int64_t k, int64_t experts) {
   if (tokens < 0 || k < 1 || experts < 1 || !dispatch_fits(tokens, k, experts)) return 0;
-  return fp8fg::dispatch_chunks(tokens * k) * (experts + 1) * (int64_t)sizeof(int32_t);
+  return fp8fg::dispatch_counts(tokens * k, experts) * (int64_t)sizeof(int32_t);
 }
 
 int fp8_dispatch(const int32_t* idx, int64_t ld_idx, int64_t tokens, int64_t k, int64_t experts,
@@ -388,7 +388,7 @@ int fp8_dispatch(const int32_t* idx, int64_t ld_idx, int64_t tokens, int64_t k, 
   if (x && cols % (e4m3 ? 128 : 8)) return FP8FG_ESHAPE;
   if (ld_idx < k) return FP8FG_ESHAPE;
   if (!offsets || !workspace) return FP8FG_EINVAL;
-  if (!aligned(offsets, 4) || !aligned(workspace, 4)) return FP8FG_EALIGN;
+  if (!aligned(offsets, 4) || !aligned(workspace, 16)) return FP8FG_EALIGN;
   const bool rows = x && cols > 0 && tokens > 0;
   if (tokens > 0) {
     if (!idx || !pos || !token) return FP8FG_EINVAL;

@@ -26,41 +26,52 @@ namespace fp8fg {
 
 namespace {
 
-constexpr int kChunkThreads = 256;
-constexpr int kChunkWaves = kChunkThreads / 64;
+constexpr int kPlanThreads = 512;
+constexpr int kPlanWaves = kPlanThreads / 64;
 constexpr int kMaxChunks = 256;
 constexpr int kMinChunk = 1024;
 constexpr int kMaxBuckets = 1025;  // experts and the bucket of dropped entries
+// Lists of up to this many entries are placed by every token's workgroup for
+// itself, in the launch that moves the rows.
+constexpr int kSmallEntries = 4096;
+constexpr int kSmallK = 16;
 
 struct Plan {
   const int32_t* idx;
   int64_t ld_idx;
-  int64_t entries;
-  int64_t chunk;  // entries per chunk, a multiple of kChunkThreads
+  int entries;
+  int chunk;    // entries per chunk, a multiple of kPlanThreads
+  int chunks;
+  int pitch;    // of counts: chunks, rounded up to 4
   int k, experts;
-  int32_t* counts;
+  int32_t* counts;  // [bucket][chunk]
   int32_t* offsets;
   int32_t* pos;
   int32_t* token;
 };
 
-__device__ __forceinline__ int bucket_of(const Plan& p, int64_t i) {
-  const int64_t t = i / p.k;
-  const int e = p.idx[t * p.ld_idx + (i - t * p.k)];
+__device__ __forceinline__ int bucket_of(const Plan& p, int i) {
+  const int t = i / p.k;
+  const int e = p.idx[p.ld_idx == p.k ? (int64_t)i : t * p.ld_idx + (i - t * p.k)];
   return (uint32_t)e < (uint32_t)p.experts ? e : p.experts;
 }
 
-// counts[chunk][e]
-__global__ __launch_bounds__(kChunkThreads) void count_kernel(Plan p) {
+// counts[e][chunk]: a bucket's counts lie side by side for place_kernel.
+__global__ __launch_bounds__(kPlanThreads) void count_kernel(Plan p) {
   __shared__ int32_t n[kMaxBuckets];
   const int B = p.experts + 1;
-  for (int e = threadIdx.x; e < B; e += kChunkThreads) n[e] = 0;
+  for (int e = threadIdx.x; e < B; e += kPlanThreads) n[e] = 0;
   __syncthreads();
   const int64_t i0 = (int64_t)blockIdx.x * p.chunk;
   const int64_t i1 = i0 + p.chunk < p.entries ? i0 + p.chunk : p.entries;
-  for (int64_t i = i0 + threadIdx.x; i < i1; i += kChunkThreads) atomicAdd(&n[bucket_of(p, i)], 1);
+  for (int64_t i = i0 + threadIdx.x; i < i1; i += kPlanThreads) atomicAdd(&n[bucket_of(p, (int)i)], 1);
   __syncthreads();
-  for (int e = threadIdx.x; e < B; e += kChunkThreads) p.counts[(int64_t)blockIdx.x * B + e] = n[e];
+  for (int e = threadIdx.x; e < B; e += kPlanThreads) {
+    p.counts[(int64_t)e * p.pitch + blockIdx.x] = n[e];
+    // the padding that place_kernel reads with the last chunks
+    if ((int)blockIdx.x == p.chunks - 1)
+      for (int c = p.chunks; c < p.pitch; ++c) p.counts[(int64_t)e * p.pitch + c] = 0;
+  }
 }
 
 // Lanes of the wave whose bucket is this lane's, among the `valid` ones.
@@ -73,60 +84,73 @@ __device__ __forceinline__ uint64_t same_bucket(int b, bool valid, int bits) {
   return m;
 }
 
+// Exclusive prefix sum over the workgroup, plus `carry`, which grows by the
+// workgroup's sum.  Ends behind a barrier.
+template <int WAVES>
+__device__ __forceinline__ int32_t block_prefix(int32_t v, int32_t* wsum, int32_t& carry) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int32_t incl = v;
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) {
+    const int32_t o = __shfl_up(incl, m);
+    incl += lane >= m ? o : 0;
+  }
+  if (lane == 63) wsum[wave] = incl;
+  __syncthreads();
+  int32_t first = carry + incl - v;
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) {
+    const int32_t n = wsum[w];
+    first += w < wave ? n : 0;
+    carry += n;
+  }
+  __syncthreads();
+  return first;
+}
+
 // Each chunk: start of every bucket (all chunks' counts), then the entries
-// in order: wave w takes the w-th quarter of the chunk, 64 at a time.
-__global__ __launch_bounds__(kChunkThreads) void place_kernel(Plan p) {
+// in order: wave w takes the w-th eighth of the chunk, 64 at a time, and
+// ranks an entry among its 64 by ballots over the bits of the bucket.
+__global__ __launch_bounds__(kPlanThreads) void place_kernel(Plan p) {
   __shared__ int32_t start[kMaxBuckets];
-  __shared__ int32_t base[kChunkWaves][kMaxBuckets];
-  __shared__ int32_t wsum[kChunkWaves];
+  __shared__ int32_t base[kPlanWaves][kMaxBuckets];
+  __shared__ int32_t wsum[kPlanWaves];
   const int B = p.experts + 1;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  // counts of the whole list and of the chunks before this one
   int32_t carry = 0;
-  for (int e0 = 0; e0 < B; e0 += kChunkThreads) {
+  for (int e0 = 0; e0 < B; e0 += kPlanThreads) {
     const int e = e0 + tid;
     int32_t total = 0, before = 0;
-    if (e < B)
-      for (int c = 0; c < (int)gridDim.x; ++c) {
-        const int32_t n = p.counts[(int64_t)c * B + e];
-        total += n;
-        before += c < (int)blockIdx.x ? n : 0;
+    if (e < B) {
+      const int4* row = reinterpret_cast<const int4*>(p.counts + (int64_t)e * p.pitch);
+#pragma unroll 8
+      for (int c = 0; c < p.pitch; c += 4) {
+        const int4 n = row[c >> 2];
+        const int b = (int)blockIdx.x - c;
+        total += n.x + n.y + n.z + n.w;
+        before += (b > 0 ? n.x : 0) + (b > 1 ? n.y : 0) + (b > 2 ? n.z : 0) + (b > 3 ? n.w : 0);
       }
-    int32_t incl = total;
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-      const int32_t o = __shfl_up(incl, m);
-      incl += lane >= m ? o : 0;
     }
-    if (lane == 63) wsum[wave] = incl;
-    __syncthreads();
-    int32_t first = carry + incl - total;
-    for (int w = 0; w < wave; ++w) first += wsum[w];
+    const int32_t first = block_prefix<kPlanWaves>(total, wsum, carry);
     if (e < B) {
       start[e] = first + before;
       if (blockIdx.x == 0) p.offsets[e] = first;  // offsets[experts]: entries with an expert
     }
-    for (int w = 0; w < kChunkWaves; ++w) carry += wsum[w];
-    __syncthreads();
   }
-  for (int e = tid; e < B; e += kChunkThreads)
+  for (int e = tid; e < B; e += kPlanThreads)
 #pragma unroll
-    for (int w = 0; w < kChunkWaves; ++w) base[w][e] = 0;
+    for (int w = 0; w < kPlanWaves; ++w) base[w][e] = 0;
   __syncthreads();
-  const int64_t i0 = (int64_t)blockIdx.x * p.chunk + wave * (p.chunk / kChunkWaves);
-  const int64_t i1 = min(i0 + p.chunk / kChunkWaves, p.entries);
+  const int64_t i0 = (int64_t)blockIdx.x * p.chunk + wave * (p.chunk / kPlanWaves);
+  const int64_t i1 = min(i0 + p.chunk / kPlanWaves, (int64_t)p.entries);
   int bits = 0;
   while ((1 << bits) < B) ++bits;
-  // the wave's own counts
-  for (int64_t i = i0; i < i1; i += 64) {
-    const bool valid = i + lane < i1;
-    if (valid) atomicAdd(&base[wave][bucket_of(p, i + lane)], 1);
-  }
+  for (int64_t i = i0 + lane; i < i1; i += 64) atomicAdd(&base[wave][bucket_of(p, (int)i)], 1);
   __syncthreads();
-  for (int e = tid; e < B; e += kChunkThreads) {
+  for (int e = tid; e < B; e += kPlanThreads) {
     int32_t at = start[e];
 #pragma unroll
-    for (int w = 0; w < kChunkWaves; ++w) {
+    for (int w = 0; w < kPlanWaves; ++w) {
       const int32_t n = base[w][e];
       base[w][e] = at;
       at += n;
@@ -135,7 +159,8 @@ __global__ __launch_bounds__(kChunkThreads) void place_kernel(Plan p) {
   __syncthreads();
   for (int64_t i = i0; i < i1; i += 64) {
     const bool valid = i + lane < i1;
-    const int b = valid ? bucket_of(p, i + lane) : 0;
+    const int at = (int)(i + lane);
+    const int b = valid ? bucket_of(p, at) : 0;
     const uint64_t same = same_bucket(b, valid, bits);
     const int rank = __popcll(same & ((1ull << lane) - 1));
     int32_t r = 0;
@@ -144,116 +169,242 @@ __global__ __launch_bounds__(kChunkThreads) void place_kernel(Plan p) {
     if (valid && rank == 0) base[wave][b] += __popcll(same);
     wave_fence();
     if (valid) {
-      const int32_t t = (int32_t)((i + lane) / p.k);
-      p.pos[i + lane] = b < p.experts ? r : -2 - r;
-      p.token[r] = b < p.experts ? t : -1;
+      p.pos[at] = b < p.experts ? r : -2 - r;
+      p.token[r] = b < p.experts ? at / p.k : -1;
     }
   }
 }
 
 struct Move {
-  const uint8_t* x;
+  const uint8_t* x;    // null: nothing to move
   int64_t pitch;       // bytes
-  int64_t vecs;        // 16-byte vectors per row
+  int vecs;            // 16-byte vectors per row
   const float* xs;
   int64_t xs_rs, xs_ts;
   int tiles;           // scales per row (0: none)
   int64_t tokens;
+  int rows;            // tokens * k
   int k;
   const int32_t* pos;
+  const int32_t* token;
   uint8_t* out;
   int64_t opitch;
   float* os;
   int64_t os_rs, os_ts;
+  int scale_blocks;    // workgroups that move scales by output row (0: the tokens' do)
 };
 
-// One workgroup per token: the row is read once and written to its k places.
-__global__ __launch_bounds__(256) void move_kernel(Move p) {
-  for (int64_t t = blockIdx.x; t < p.tokens; t += gridDim.x) {
-    const int32_t* pos = p.pos + t * p.k;
-    for (int64_t v = threadIdx.x; v < p.vecs; v += 256) {
-      const uint4 w = ld_nt16(p.x + t * p.pitch + v * 16);
-      for (int j = 0; j < p.k; ++j) {
-        const int32_t r = pos[j];
-        if (r >= 0)
-          st_nt16(p.out + (int64_t)r * p.opitch + v * 16, w);
-        else
-          st_nt16(p.out + (int64_t)(-2 - r) * p.opitch + v * 16, make_uint4(0, 0, 0, 0));
-      }
-    }
-    for (int i = threadIdx.x; i < p.tiles; i += 256) {
-      const float s = p.xs[t * p.xs_rs + i * p.xs_ts];
-      for (int j = 0; j < p.k; ++j) {
-        const int32_t r = pos[j];
-        p.os[(r >= 0 ? r : -2 - r) * p.os_rs + i * p.os_ts] = r >= 0 ? s : kFltMinNormal;
-      }
-    }
-  }
-}
-
-template <int XT>
-__global__ __launch_bounds__(256) void combine_kernel(CombineArgs p) {
-  const int nvec = (int)(p.cols >> 3);
-  for (int64_t t = blockIdx.x; t < p.tokens; t += gridDim.x) {
-    for (int v = threadIdx.x; v < nvec; v += 256) {
-      float acc[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
-      for (int j = 0; j < p.k; ++j) {
-        const int32_t r = p.pos[t * p.k + j];
-        if (r < 0 || r >= p.z_rows) continue;
-        const float w = p.w ? p.w[t * p.ldw + j] : 1.0f;
-        float z[8];
-        load8<XT>(p.z, r * p.ldz + v * 8, z);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] += w * z[e];
-      }
-      if (p.base) {
-        float b[8];
-        load8<XT>(p.base, t * p.ldb + v * 8, b);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] += b[e];
-      }
-      store_raw8<XT, true>(p.out, t * p.ldo + v * 8, encode8<XT>(acc));
-    }
-  }
-}
-
-template <int XT>
-__global__ __launch_bounds__(256) void combine_grad_kernel(CombineGradArgs p) {
-  __shared__ float part[4];
-  const int nvec = (int)(p.cols >> 3);
-  for (int64_t t = blockIdx.x; t < p.tokens; t += gridDim.x) {
+// The row of token t to its places: read once, written k times.
+__device__ __forceinline__ void move_row(const Move& p, int64_t t, const int32_t* pos) {
+  for (int v = threadIdx.x; v < p.vecs; v += blockDim.x) {
+    const uint4 w = ld_nt16(p.x + t * p.pitch + (int64_t)v * 16);
     for (int j = 0; j < p.k; ++j) {
-      const int32_t r = p.pos[t * p.k + j];
-      const bool here = r >= 0 && r < p.z_rows;
-      const int64_t row = here ? r : -2 - (int64_t)r;
-      const bool zero = !here && row >= 0 && row < p.z_rows;
-      const float w = p.w ? p.w[t * p.ldw + j] : 1.0f;
-      float dot = 0.0f;
-      for (int v = threadIdx.x; v < nvec; v += 256) {
-        float d[8];
-        if (here) {
-          load8<XT>(p.dy, t * p.lddy + v * 8, d);
-          if (p.dw) {
-            float z[8];
-            load8<XT>(p.z, row * p.ldz + v * 8, z);
+      const int32_t r = pos[j];
+      const int64_t row = r >= 0 ? r : -2 - r;
+      st_nt16(p.out + row * p.opitch + (int64_t)v * 16, r >= 0 ? w : make_uint4(0, 0, 0, 0));
+    }
+  }
+}
+
+__device__ __forceinline__ void move_scales_of(const Move& p, int64_t t, const int32_t* pos) {
+  for (int i = threadIdx.x; i < p.tiles; i += blockDim.x) {
+    const float s = p.xs[t * p.xs_rs + i * p.xs_ts];
+    for (int j = 0; j < p.k; ++j) {
+      const int32_t r = pos[j];
+      p.os[(r >= 0 ? r : -2 - r) * p.os_rs + i * p.os_ts] = r >= 0 ? s : kFltMinNormal;
+    }
+  }
+}
+
+// Workgroups 0 .. scale_blocks - 1 move the scales of 64 output rows each, a
+// lane to a row: with group-major scales a wave then writes 256 contiguous
+// bytes, where a token's workgroup would write single floats into lines that
+// it shares with 15 other tokens.  The others take a token each.
+__global__ __launch_bounds__(512) void move_kernel(Move p) {
+  if ((int)blockIdx.x < p.scale_blocks) {
+    const int waves = blockDim.x >> 6;
+    for (int64_t r = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63); r < p.rows; r += (int64_t)p.scale_blocks * 64) {
+      const int32_t t = p.token[r];
+#pragma unroll 4
+      for (int i = threadIdx.x >> 6; i < p.tiles; i += waves) {
+        const float s = t >= 0 ? p.xs[t * p.xs_rs + i * p.xs_ts] : kFltMinNormal;
+        p.os[r * p.os_rs + i * p.os_ts] = s;
+      }
+    }
+    return;
+  }
+  const int64_t step = gridDim.x - p.scale_blocks;
+  for (int64_t t = (int64_t)blockIdx.x - p.scale_blocks; t < p.tokens; t += step) {
+    move_row(p, t, p.pos + t * p.k);
+    if (p.scale_blocks == 0) move_scales_of(p, t, p.pos + t * p.k);
+  }
+}
+
+// The whole dispatch of a short list in one launch: workgroup t counts, for
+// each of token t's entries, the entries before it in the order; the last
+// workgroup writes the offsets.
+__global__ __launch_bounds__(512) void dispatch_small_kernel(Plan p, Move m) {
+  __shared__ int32_t n[kMaxBuckets];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  if ((int64_t)blockIdx.x == m.tokens) {
+    __shared__ int32_t wsum[kPlanWaves];
+    const int B = p.experts + 1;
+    for (int e = tid; e < B; e += kPlanThreads) n[e] = 0;
+    __syncthreads();
+    for (int i = tid; i < p.entries; i += kPlanThreads) atomicAdd(&n[bucket_of(p, i)], 1);
+    __syncthreads();
+    int32_t carry = 0;
+    for (int e0 = 0; e0 < B; e0 += kPlanThreads) {
+      const int32_t first = block_prefix<kPlanWaves>(e0 + tid < B ? n[e0 + tid] : 0, wsum, carry);
+      if (e0 + tid < B) p.offsets[e0 + tid] = first;
+    }
+    return;
+  }
+  const int t = blockIdx.x;
+  __shared__ int32_t part[kPlanWaves][kSmallK];
+  __shared__ int32_t place[kSmallK];
+  int before[kSmallK], mine[kSmallK];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dot += d[e] * z[e];
+  for (int j = 0; j < kSmallK; ++j) {
+    before[j] = 0;
+    mine[j] = j < p.k ? bucket_of(p, t * p.k + j) : 0;
+  }
+  for (int i0 = wave * 64; i0 < p.entries; i0 += kPlanThreads) {
+    const int i = i0 + lane;
+    const int b = i < p.entries ? bucket_of(p, i) : kMaxBuckets;
+#pragma unroll
+    for (int j = 0; j < kSmallK; ++j)
+      if (j < p.k) before[j] += __popcll(__builtin_amdgcn_ballot_w64(b < mine[j] || (b == mine[j] && i < t * p.k + j)));
+  }
+  if (lane == 0)
+#pragma unroll
+    for (int j = 0; j < kSmallK; ++j) part[wave][j] = before[j];
+  __syncthreads();
+  if (tid < p.k) {
+    int32_t r = 0;
+#pragma unroll
+    for (int w = 0; w < kPlanWaves; ++w) r += part[w][tid];
+    const bool here = bucket_of(p, t * p.k + tid) < p.experts;
+    place[tid] = here ? r : -2 - r;
+    p.pos[t * p.k + tid] = place[tid];
+    p.token[r] = here ? t : -1;
+  }
+  __syncthreads();
+  if (!m.x) return;
+  move_row(m, t, place);
+  move_scales_of(m, t, place);
+}
+
+// A thread sums one 8-element vector over the token's places, the loads of
+// kAhead of them in flight together: a decode batch has few tokens, so the
+// columns are spread over workgroups too.
+constexpr int kAhead = 8;
+constexpr int kCombineThreads = 128;
+
+template <int XT>
+__global__ __launch_bounds__(kCombineThreads) void combine_kernel(CombineArgs p, int64_t units, int blocks) {
+  const int nvec = (int)(p.cols >> 3);
+  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    const int64_t t = u / blocks;
+    const int v = (int)(u - t * blocks) * kCombineThreads + threadIdx.x;
+    if (v >= nvec) continue;
+    float acc[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
+    Raw8<XT> base = {};
+    if (p.base) base = load_raw8<XT, true>(p.base, t * p.ldb + (int64_t)v * 8);
+    for (int j0 = 0; j0 < p.k; j0 += kAhead) {
+      Raw8<XT> z[kAhead];
+      float w[kAhead];
+      bool here[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int64_t r = j0 + j < p.k ? p.pos[t * p.k + j0 + j] : -1;
+        here[j] = r >= 0 && r < p.z_rows;
+        z[j] = {};
+        w[j] = 1.0f;
+        if (here[j]) {
+          z[j] = load_raw8<XT, true>(p.z, r * p.ldz + (int64_t)v * 8);
+          if (p.w) w[j] = p.w[t * p.ldw + j0 + j];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        if (!here[j]) continue;
+        float f[8];
+        decode8<XT>(z[j], f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] = __builtin_fmaf(w[j], f[e], acc[e]);
+      }
+    }
+    if (p.base) {
+      float f[8];
+      decode8<XT>(base, f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] += f[e];
+    }
+    store_raw8<XT, true>(p.out, t * p.ldo + (int64_t)v * 8, encode8<XT>(acc));
+  }
+}
+
+// A workgroup per token: dy's vector is read once for kAhead places, whose
+// rows of z are in flight together; the places' dot products stay in
+// registers and meet once per kAhead of them.
+template <int XT>
+__global__ __launch_bounds__(512) void combine_grad_kernel(CombineGradArgs p) {
+  __shared__ float part[8][kAhead];
+  const int nvec = (int)(p.cols >> 3);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  for (int64_t t = blockIdx.x; t < p.tokens; t += gridDim.x) {
+    for (int j0 = 0; j0 < p.k; j0 += kAhead) {
+      int64_t row[kAhead];  // -1: nothing to write
+      float w[kAhead], dot[kAhead];
+      bool here[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int64_t r = j0 + j < p.k ? p.pos[t * p.k + j0 + j] : -1;
+        here[j] = r >= 0 && r < p.z_rows;
+        row[j] = r >= 0 ? r : -2 - r;
+        if (row[j] >= p.z_rows) row[j] = -1;
+        w[j] = here[j] && p.w ? p.w[t * p.ldw + j0 + j] : 1.0f;
+        dot[j] = 0.0f;
+      }
+      for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
+        float d[8];
+        const Raw8<XT> dy = load_raw8<XT, true>(p.dy, t * p.lddy + (int64_t)v * 8);
+        Raw8<XT> z[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          z[j] = {};
+          if (here[j] && p.dw) z[j] = load_raw8<XT, true>(p.z, row[j] * p.ldz + (int64_t)v * 8);
+        }
+        decode8<XT>(dy, d);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          if (row[j] < 0) continue;
+          float f[8];
+          if (here[j]) {
+            decode8<XT>(z[j], f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dot[j] = __builtin_fmaf(d[e], f[e], dot[j]);
           }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) d[e] *= w;
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) d[e] = 0.0f;
+          for (int e = 0; e < 8; ++e) f[e] = here[j] ? w[j] * d[e] : 0.0f;
+          store_raw8<XT, true>(p.dz, row[j] * p.lddz + (int64_t)v * 8, encode8<XT>(f));
         }
-        if (here || zero) store_raw8<XT, true>(p.dz, row * p.lddz + v * 8, encode8<XT>(d));
       }
       if (p.dw) {
-        dot = wave_sum(dot);
-        if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = dot;
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          dot[j] = wave_sum(dot[j]);
+          if (lane == 0) part[wave][j] = dot[j];
+        }
         __syncthreads();
-        if (threadIdx.x == 0) p.dw[t * p.lddw + j] = ((part[0] + part[1]) + part[2]) + part[3];
+        if (threadIdx.x < kAhead && j0 + (int)threadIdx.x < p.k) {
+          float s = part[0][threadIdx.x];
+          for (int i = 1; i < waves; ++i) s += part[i][threadIdx.x];
+          p.dw[t * p.lddw + j0 + threadIdx.x] = s;
+        }
         __syncthreads();
       }
     }
@@ -261,48 +412,77 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(CombineGradArgs p) {
 }
 
 constexpr int64_t kMaxTokenBlocks = 1 << 20;
+constexpr int64_t kMaxCombineBlocks = 1 << 24;
 
-dim3 token_grid(int64_t tokens) { return dim3((unsigned)(tokens < kMaxTokenBlocks ? tokens : kMaxTokenBlocks)); }
+unsigned token_blocks(int64_t tokens) { return (unsigned)(tokens < kMaxTokenBlocks ? tokens : kMaxTokenBlocks); }
+
+// Threads (at most 512, whole waves) that split `vecs` evenly.
+unsigned row_threads(int64_t vecs) {
+  const int64_t rounds = (vecs + 511) / 512;
+  const int64_t t = rounds > 0 ? (vecs + rounds - 1) / rounds : 1;
+  return (unsigned)((t + 63) / 64 * 64);
+}
 
 }  // namespace
 
 // At most kMaxChunks chunks: each chunk's workgroup reads all their counts.
-int64_t dispatch_chunks(int64_t entries) {
+static int64_t dispatch_chunks(int64_t entries) {
   const int64_t n = (entries + kMinChunk - 1) / kMinChunk;
   return n < 1 ? 1 : n < kMaxChunks ? n : kMaxChunks;
+}
+
+static int64_t count_pitch(int64_t chunks) { return (chunks + 3) / 4 * 4; }
+
+int64_t dispatch_counts(int64_t entries, int64_t experts) {
+  return count_pitch(dispatch_chunks(entries)) * (experts + 1);
 }
 
 hipError_t launch_dispatch(const DispatchArgs& a, hipStream_t st) {
   const int64_t entries = a.tokens * a.k;
   const int64_t chunks = dispatch_chunks(entries);
   const int64_t per = (entries + chunks - 1) / chunks;
-  const int64_t chunk = (per + kChunkThreads - 1) / kChunkThreads * kChunkThreads;
-  const Plan p{a.idx, a.ld_idx, entries, chunk, a.k, a.experts, a.counts, a.offsets, a.pos, a.token};
-  hipLaunchKernelGGL(count_kernel, dim3((unsigned)chunks), dim3(kChunkThreads), 0, st, p);
-  hipLaunchKernelGGL(place_kernel, dim3((unsigned)chunks), dim3(kChunkThreads), 0, st, p);
-  if (a.x && a.tokens > 0) {
-    const int size = a.x_type == 2 ? 1 : a.x_type == 0 ? 2 : 4;
-    const Move m{reinterpret_cast<const uint8_t*>(a.x), a.ldx * size, a.cols * size / 16, a.xs, a.xs_rs, a.xs_ts,
-                 a.x_type == 2 ? (int)(a.cols / 128) : 0, a.tokens, a.k, a.pos,
-                 reinterpret_cast<uint8_t*>(a.out), a.ldo * size, a.os, a.os_rs, a.os_ts};
-    hipLaunchKernelGGL(move_kernel, token_grid(a.tokens), dim3(256), 0, st, m);
+  const int64_t chunk = (per + kPlanThreads - 1) / kPlanThreads * kPlanThreads;
+  const Plan p{a.idx,    a.ld_idx,  (int)entries, (int)chunk, (int)chunks, (int)count_pitch(chunks), a.k,
+               a.experts, a.counts, a.offsets,    a.pos,      a.token};
+  const int size = a.x_type == 2 ? 1 : a.x_type == 0 ? 2 : 4;
+  Move m{reinterpret_cast<const uint8_t*>(a.x), a.ldx * size, (int)(a.cols * size / 16), a.xs, a.xs_rs, a.xs_ts,
+         a.x_type == 2 ? (int)(a.cols / 128) : 0, a.tokens, (int)entries, a.k, a.pos, a.token,
+         reinterpret_cast<uint8_t*>(a.out), a.ldo * size, a.os, a.os_rs, a.os_ts, 0};
+  if (entries <= kSmallEntries && a.k <= kSmallK) {
+    hipLaunchKernelGGL(dispatch_small_kernel, dim3((unsigned)a.tokens + 1), dim3(kPlanThreads), 0, st, p, m);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL(count_kernel, dim3((unsigned)chunks), dim3(kPlanThreads), 0, st, p);
+  hipLaunchKernelGGL(place_kernel, dim3((unsigned)chunks), dim3(kPlanThreads), 0, st, p);
+  if (a.x) {
+    if (m.tiles > 0 && a.os_rs == 1) m.scale_blocks = (int)token_blocks((entries + 63) / 64);
+    hipLaunchKernelGGL(move_kernel, dim3(m.scale_blocks + token_blocks(a.tokens)), dim3(row_threads(m.vecs)), 0, st, m);
   }
   return hipGetLastError();
 }
 
+template <int XT>
+static void combine_t(const CombineArgs& a, hipStream_t st) {
+  const int64_t blocks = (a.cols / 8 + kCombineThreads - 1) / kCombineThreads;
+  const int64_t units = a.tokens * blocks;
+  const unsigned grid = (unsigned)(units < kMaxCombineBlocks ? units : kMaxCombineBlocks);
+  hipLaunchKernelGGL(combine_kernel<XT>, dim3(grid), dim3(kCombineThreads), 0, st, a, units, (int)blocks);
+}
+
 hipError_t launch_combine(const CombineArgs& a, hipStream_t st) {
   if (a.type == 0)
-    hipLaunchKernelGGL(combine_kernel<0>, token_grid(a.tokens), dim3(256), 0, st, a);
+    combine_t<0>(a, st);
   else
-    hipLaunchKernelGGL(combine_kernel<1>, token_grid(a.tokens), dim3(256), 0, st, a);
+    combine_t<1>(a, st);
   return hipGetLastError();
 }
 
 hipError_t launch_combine_grad(const CombineGradArgs& a, hipStream_t st) {
+  const dim3 grid(token_blocks(a.tokens)), block(row_threads(a.cols / 8));
   if (a.type == 0)
-    hipLaunchKernelGGL(combine_grad_kernel<0>, token_grid(a.tokens), dim3(256), 0, st, a);
+    hipLaunchKernelGGL(combine_grad_kernel<0>, grid, block, 0, st, a);
   else
-    hipLaunchKernelGGL(combine_grad_kernel<1>, token_grid(a.tokens), dim3(256), 0, st, a);
+    hipLaunchKernelGGL(combine_grad_kernel<1>, grid, block, 0, st, a);
   return hipGetLastError();
 }
 

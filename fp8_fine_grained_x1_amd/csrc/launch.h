@@ -123,11 +123,11 @@ struct NormGradArgs {
   void* dx;
   int64_t lddx;
   float* dgamma;
-  float* partial;      // [norm_grad_strips(rows)][cols]
+  float* partial;      // [norm_grad_strips(rows, cols)][cols]
 };
 // Row strips of the gradient kernel, each with its own partial sum of
-// dgamma; a function of the row count alone.
-int64_t norm_grad_strips(int64_t rows);
+// dgamma; a function of the sizes alone.
+int64_t norm_grad_strips(int64_t rows, int64_t cols);
 hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t st);
 // Widest row a workgroup holds in registers.
 constexpr int64_t kNormMaxCols = 32768;
@@ -190,10 +190,10 @@ struct DispatchArgs {
   int64_t ldo;
   float* os;
   int64_t os_rs, os_ts;
-  int32_t* counts;     // [dispatch_chunks][experts + 1]
+  int32_t* counts;     // dispatch_counts(tokens * k, experts) of them
 };
-// Chunks of the (token, choice) list; each has its own expert counts.
-int64_t dispatch_chunks(int64_t entries);
+// Counts of entries per expert and chunk of the (token, choice) list.
+int64_t dispatch_counts(int64_t entries, int64_t experts);
 hipError_t launch_dispatch(const DispatchArgs& a, hipStream_t st);
 
 struct CombineArgs {

@@ -115,10 +115,32 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs p) {
 
 // A workgroup takes the rows blockIdx.x, blockIdx.x + gridDim.x, ..; its
 // threads keep their columns' part of dgamma in registers and write it once.
+// The next row is loaded before the reduction of this one (PREFETCH: where
+// the registers hold both).
 template <int XT, int NV>
-__global__ __launch_bounds__(1024) void norm_grad_kernel(NormGradArgs p) {
+struct GradRow {
+  Raw8<XT> d[NV], h[NV], b[NV];
+  float rstd;
+};
+
+template <int XT, int NV>
+__device__ __forceinline__ void load_grad_row(const NormGradArgs& p, int64_t row, int nvec, GradRow<XT, NV>& r) {
+  r.rstd = p.rstd[row];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int v = threadIdx.x + i * blockDim.x;
+    if (v >= nvec) continue;
+    r.d[i] = load_raw8<XT, true>(p.dy, row * p.lddy + v * 8);
+    r.h[i] = load_raw8<XT, true>(p.h, row * p.ldh + v * 8);
+    if (p.dh) r.b[i] = load_raw8<XT, true>(p.dh, row * p.lddh + v * 8);
+  }
+}
+
+template <int XT, int NV, int THREADS, bool PREFETCH>
+__global__ __launch_bounds__(THREADS) void norm_grad_kernel(NormGradArgs p) {
   __shared__ float part[2][kMaxWaves];
   const int nvec = (int)(p.cols >> 3);
+  const float inv_cols = 1.0f / (float)p.cols;
   float g[NV][8], acc[NV][8];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -128,44 +150,47 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(NormGradArgs p) {
     if (v < nvec) load_gamma8(p.gamma, p.g_type, (int64_t)v * 8, g[i]);
   }
   int flip = 0;
-  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, flip ^= 1) {
-    const float rstd = p.rstd[row];
-    Raw8<XT> rd[NV], rh[NV];
+  GradRow<XT, NV> r;
+  int64_t row = blockIdx.x;
+  if (PREFETCH && row < p.rows) load_grad_row(p, row, nvec, r);
+  for (; row < p.rows; row += gridDim.x, flip ^= 1) {
+    if (!PREFETCH) load_grad_row(p, row, nvec, r);
     float c = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
       if (v >= nvec) continue;
-      rd[i] = load_raw8<XT, true>(p.dy, row * p.lddy + v * 8);
-      rh[i] = load_raw8<XT, true>(p.h, row * p.ldh + v * 8);
       float d[8], h[8];
-      decode8<XT>(rd[i], d);
-      decode8<XT>(rh[i], h);
+      decode8<XT>(r.d[i], d);
+      decode8<XT>(r.h[i], h);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float xh = h[e] * rstd;
-        c += d[e] * g[i][e] * xh;
-        acc[i][e] += d[e] * xh;
+        const float dx = d[e] * (h[e] * r.rstd);
+        c = __builtin_fmaf(dx, g[i][e], c);
+        acc[i][e] += dx;
       }
     }
-    c = block_sum(c, part[flip]) / (float)p.cols;
+    GradRow<XT, NV> next;
+    if (PREFETCH && row + gridDim.x < p.rows) load_grad_row(p, row + gridDim.x, nvec, next);
+    c = block_sum(c, part[flip]) * inv_cols * r.rstd;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
       if (v >= nvec) continue;
       float d[8], h[8], o[8];
-      decode8<XT>(rd[i], d);
-      decode8<XT>(rh[i], h);
+      decode8<XT>(r.d[i], d);
+      decode8<XT>(r.h[i], h);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = rstd * (d[e] * g[i][e] - h[e] * rstd * c);
+      for (int e = 0; e < 8; ++e) o[e] = r.rstd * __builtin_fmaf(-h[e], c, d[e] * g[i][e]);
       if (p.dh) {
         float b[8];
-        load8<XT>(p.dh, row * p.lddh + v * 8, b);
+        decode8<XT>(r.b[i], b);
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] += b[e];
       }
       store_raw8<XT, true>(p.dx, row * p.lddx + v * 8, encode8<XT>(o));
     }
+    if (PREFETCH) r = next;
   }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -174,34 +199,53 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(NormGradArgs p) {
   }
 }
 
-// dgamma[c] = sum over the strips' partial sums, in strip order per thread
-// row, then over the 16 thread rows.
-__global__ __launch_bounds__(256) void norm_grad_sum_kernel(const float* __restrict__ partial, int strips,
-                                                            int64_t cols, float* __restrict__ dgamma) {
-  __shared__ float part[16][17];
-  const int c = threadIdx.x & 15, s0 = threadIdx.x >> 4;
-  const int64_t col = (int64_t)blockIdx.x * 16 + c;
-  float t = 0.0f;
-  if (col < cols)
-    for (int s = s0; s < strips; s += 16) t += partial[s * cols + col];
-  part[s0][c] = t;
-  __syncthreads();
-  if (s0 == 0 && col < cols) {
+// dgamma[c] = sum over the strips' partial sums: 4 lanes hold 16 columns,
+// 128 thread rows take every 128th strip, then the rows are added, 16 of a
+// wave and the 8 waves.  Narrow columns make many workgroups.
+constexpr int kSumThreads = 512;
+
+__global__ __launch_bounds__(kSumThreads) void norm_grad_sum_kernel(const float* __restrict__ partial, int strips,
+                                                                    int64_t cols, float* __restrict__ dgamma) {
+  __shared__ float part[kSumThreads / 64][16];
+  const int c = threadIdx.x & 3, s0 = threadIdx.x >> 2;
+  const int64_t col = (int64_t)blockIdx.x * 16 + c * 4;
+  float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (col < cols) {
+#pragma unroll 8
+    for (int s = s0; s < strips; s += kSumThreads / 4) {
+      const float4 v = *reinterpret_cast<const float4*>(partial + s * cols + col);
+      t[0] += v.x;
+      t[1] += v.y;
+      t[2] += v.z;
+      t[3] += v.w;
+    }
+  }
 #pragma unroll
-    for (int s = 1; s < 16; ++s) t += part[s][c];
-    dgamma[col] = t;
+  for (int e = 0; e < 4; ++e) {
+#pragma unroll
+    for (int m = 4; m < 64; m <<= 1) t[e] += __shfl_xor(t[e], m);
+    if ((threadIdx.x & 63) < 4) part[threadIdx.x >> 6][c * 4 + e] = t[e];
+  }
+  __syncthreads();
+  if (threadIdx.x < 16) {
+    const int64_t at = (int64_t)blockIdx.x * 16 + threadIdx.x;
+    float s = part[0][threadIdx.x];
+#pragma unroll
+    for (int w = 1; w < kSumThreads / 64; ++w) s += part[w][threadIdx.x];
+    if (at < cols) dgamma[at] = s;
   }
 }
 
 constexpr int64_t kMaxRowBlocks = 1 << 20;
-constexpr int64_t kGradStrips = 1024;
 
-// Vectors per thread and threads per workgroup for rows of `nvec` vectors.
+// Vectors per thread and threads per workgroup for rows of `nvec` vectors:
+// at most 512 threads, whose register budget holds a row of up to 2048
+// vectors, and 1024 beyond.
 struct RowShape {
   int nv, threads;
 };
 RowShape row_shape(int64_t nvec) {
-  const int nv = nvec <= 512 ? 1 : nvec <= 2048 ? 2 : 4;
+  const int nv = nvec <= 512 ? 1 : nvec <= 1024 ? 2 : 4;
   const int64_t t = (nvec + nv - 1) / nv;
   return {nv, (int)((t + 63) / 64 * 64)};
 }
@@ -221,18 +265,25 @@ hipError_t norm_t(const NormArgs& a, hipStream_t st) {
 template <int XT>
 hipError_t norm_grad_t(const NormGradArgs& a, hipStream_t st) {
   const RowShape sh = row_shape(a.cols / 8);
-  const dim3 grid((unsigned)norm_grad_strips(a.rows)), block(sh.threads);
-  switch (sh.nv) {
-    case 1: hipLaunchKernelGGL((norm_grad_kernel<XT, 1>), grid, block, 0, st, a); break;
-    case 2: hipLaunchKernelGGL((norm_grad_kernel<XT, 2>), grid, block, 0, st, a); break;
-    default: hipLaunchKernelGGL((norm_grad_kernel<XT, 4>), grid, block, 0, st, a); break;
-  }
+  const dim3 grid((unsigned)norm_grad_strips(a.rows, a.cols)), block(sh.threads);
+  if (sh.nv == 1)
+    hipLaunchKernelGGL((norm_grad_kernel<XT, 1, 512, true>), grid, block, 0, st, a);
+  else if (sh.nv == 2)
+    hipLaunchKernelGGL((norm_grad_kernel<XT, 2, 512, true>), grid, block, 0, st, a);
+  else if (sh.threads <= 512)
+    hipLaunchKernelGGL((norm_grad_kernel<XT, 4, 512, false>), grid, block, 0, st, a);
+  else
+    hipLaunchKernelGGL((norm_grad_kernel<XT, 4, 1024, false>), grid, block, 0, st, a);
   return hipGetLastError();
 }
 
 }  // namespace
 
-int64_t norm_grad_strips(int64_t rows) { return rows < kGradStrips ? rows : kGradStrips; }
+// Two to eight workgroups per CU, more of them where rows are short.
+int64_t norm_grad_strips(int64_t rows, int64_t cols) {
+  const int64_t most = cols <= 2048 ? 2048 : cols <= 4096 ? 1024 : 512;
+  return rows < most ? rows : most;
+}
 
 hipError_t launch_norm(const NormArgs& a, hipStream_t st) {
   return a.x_type == 0 ? norm_t<0>(a, st) : norm_t<1>(a, st);
@@ -243,8 +294,8 @@ hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t st) {
     const hipError_t e = a.x_type == 0 ? norm_grad_t<0>(a, st) : norm_grad_t<1>(a, st);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(norm_grad_sum_kernel, dim3((unsigned)((a.cols + 15) / 16)), dim3(256), 0, st, a.partial,
-                     (int)norm_grad_strips(a.rows), a.cols, a.dgamma);
+  hipLaunchKernelGGL(norm_grad_sum_kernel, dim3((unsigned)((a.cols + 15) / 16)), dim3(kSumThreads), 0, st, a.partial,
+                     (int)norm_grad_strips(a.rows, a.cols), a.cols, a.dgamma);
   return hipGetLastError();
 }
 

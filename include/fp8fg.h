@@ -370,7 +370,7 @@ FP8FG_API int fp8_route_backward(const void* logits, int l_type, int64_t rows, i
  *   out, os: [tokens * k][cols] and its scales: out[r] = x[t]; zero bytes and
  *            the scale 2^-126 for a dropped entry.
  *   workspace: at least fp8_dispatch_workspace(tokens, k, experts) bytes,
- *            4-byte aligned; FP8FG_ESHAPE if workspace_bytes is less.
+ *            16-byte aligned; FP8FG_ESHAPE if workspace_bytes is less.
  *   Requires k >= 1, experts >= 1; with x, cols a multiple of 128 (E4M3) or
  *   8.  tokens == 0 writes zero offsets.
  *   Alignment: x, out 16-byte aligned, pitches multiples of 16 bytes; idx,
