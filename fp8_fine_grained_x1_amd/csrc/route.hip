@@ -12,8 +12,9 @@
 // Slots that find no expert get index -1 and weight 0.
 //
 // The choice is discrete, so the scores' last bits matter: they are formed
-// in fp64 to about 2^-40 and rounded once, which gives the correctly rounded
-// fp32 value for all but a few of a million logits.  (gfx950 issues fp64
+// in fp64 to about 2^-36 and rounded once, which gives the correctly rounded
+// fp32 value for all but one in some thousand logits; the others are one step off,
+// and choices that lie so close to another are rarer still.  (gfx950 issues fp64
 // FMAs at the fp32 rate.)
 //
 // Gradient of w with respect to l, from the logits and the indexes alone:
@@ -33,16 +34,14 @@ namespace {
 
 constexpr int kRouteWaves = 4;
 
-// exp(x) for x <= 709, relative error below 2^-41: exp(x) = 2^n exp(r),
-// |r| <= ln(2)/2, with the Taylor polynomial of degree 11 (remainder
-// r^12/12! < 2^-47 of the sum).
+// exp(x) for x <= 709, relative error below 2^-36: exp(x) = 2^n exp(r),
+// |r| <= ln(2)/2, with the Taylor polynomial of degree 9 (remainder
+// r^10/10! < 2^-37).
 __device__ __forceinline__ double exp_acc(double x) {
   if (x < -745.0) return 0.0;
   const double n = __builtin_rint(x * 1.4426950408889634);
   const double r = __builtin_fma(n, -0.6931471805599453, x);
-  double p = 1.0 / 39916800.0;
-  p = __builtin_fma(p, r, 1.0 / 3628800.0);
-  p = __builtin_fma(p, r, 1.0 / 362880.0);
+  double p = 1.0 / 362880.0;
   p = __builtin_fma(p, r, 1.0 / 40320.0);
   p = __builtin_fma(p, r, 1.0 / 5040.0);
   p = __builtin_fma(p, r, 1.0 / 720.0);
@@ -53,6 +52,16 @@ __device__ __forceinline__ double exp_acc(double x) {
   p = __builtin_fma(p, r, 1.0);
   p = __builtin_fma(p, r, 1.0);
   return __builtin_ldexp(p, (int)n);
+}
+
+// RN32(1 / (1 + exp(-l))): the reciprocal from fp32's and one Newton step in
+// fp64 (error squared: 2^-44).  The denominator's fp32 overflow (l < -88)
+// ends in fp32's denormals, where the quotient is formed as it is.
+__device__ __forceinline__ float sigmoid_acc(float l) {
+  if (l < -80.0f) return l < -700.0f ? 0.0f : (float)(1.0 / (1.0 + exp_acc(-(double)l)));
+  const double d = 1.0 + exp_acc(-(double)l);
+  const double y = (double)__builtin_amdgcn_rcpf((float)d);
+  return (float)__builtin_fma(y, __builtin_fma(-d, y, 1.0), y);
 }
 
 // fp32 -> unsigned whose order is the floats' (no NaN reaches it); -0 counts
@@ -87,9 +96,217 @@ __device__ __forceinline__ float load_logit(const void* __restrict__ l, int64_t 
   return v == v ? v : -INFINITY;
 }
 
-// One wave per token; lane i holds the experts i, i + 64, ..
+// ------------------------------------------------- lanes of one token
+// Reductions over the LANES (16: a DPP row, or 64) that hold a token; every
+// one of them gets the result.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp_f64(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, (uint64_t)dpp_u32<CTRL>((uint32_t)(u >> 32)) << 32 | dpp_u32<CTRL>((uint32_t)u));
+}
+
+template <int LANES>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+  v = max(v, dpp_u32<kDppQuadXor1>(v));
+  v = max(v, dpp_u32<kDppQuadXor2>(v));
+  v = max(v, dpp_u32<kDppRowHalfMirror>(v));
+  v = max(v, dpp_u32<kDppRowMirror>(v));
+  if constexpr (LANES == 64) {
+    const uint32_t a = __builtin_amdgcn_readlane(v, 0), b = __builtin_amdgcn_readlane(v, 16);
+    const uint32_t c = __builtin_amdgcn_readlane(v, 32), d = __builtin_amdgcn_readlane(v, 48);
+    v = max(max(a, b), max(c, d));
+  }
+  return v;
+}
+
+template <int LANES>
+__device__ __forceinline__ uint32_t lanes_min(uint32_t v) {
+  return ~lanes_max<LANES>(~v);
+}
+
+template <int LANES>
+__device__ __forceinline__ float lanes_max_f32(float v) {
+  v = row16_max(v);
+  if constexpr (LANES == 64) {
+    v = fmaxf(v, __shfl_xor(v, 16));
+    v = fmaxf(v, __shfl_xor(v, 32));
+  }
+  return v;
+}
+
+template <int LANES>
+__device__ __forceinline__ double lanes_sum_f64(double v) {
+  v += dpp_f64<kDppQuadXor1>(v);
+  v += dpp_f64<kDppQuadXor2>(v);
+  v += dpp_f64<kDppRowHalfMirror>(v);
+  v += dpp_f64<kDppRowMirror>(v);
+  if constexpr (LANES == 64) {
+    v += __shfl_xor(v, 16);
+    v += __shfl_xor(v, 32);
+  }
+  return v;
+}
+
+template <int LANES>
+__device__ __forceinline__ float lanes_sum_f32(float v) {
+  v += dpp_mov<kDppQuadXor1>(v);
+  v += dpp_mov<kDppQuadXor2>(v);
+  v += dpp_mov<kDppRowHalfMirror>(v);
+  v += dpp_mov<kDppRowMirror>(v);
+  if constexpr (LANES == 64) {
+    v += __shfl_xor(v, 16);
+    v += __shfl_xor(v, 32);
+  }
+  return v;
+}
+
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+
+// The two largest of two disjoint sets' two largest (a >= b).
+__device__ __forceinline__ void merge_top2(uint32_t& a, uint32_t& b, uint32_t oa, uint32_t ob) {
+  b = max(min(a, oa), max(b, ob));
+  a = max(a, oa);
+}
+
+// How the experts lie in a token's lanes: each group has `lanes` consecutive
+// lanes (a power of two), each of which has `slots` consecutive experts of
+// the group.  The lower expert is in the lower lane, then the lower slot.
+struct RouteLayout {
+  int groups;  // 1 where groups play no part
+  int size;    // experts per group
+  int lanes;   // log2
+  int slots;
+};
+
+// LANES lanes per token, NS >= slots experts per lane in registers.
+template <int LT, int LANES, int NS>
+__global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p, RouteLayout q) {
+  constexpr int kTokens = 64 / LANES;  // of a wave
+  extern __shared__ float lds[];       // bias, then a row of scores per token
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = lane % LANES;
+  const int E = p.experts;
+  float* rows = lds + E + wave * kTokens * E;
+  if (p.bias) {
+    for (int e = threadIdx.x; e < E; e += 64 * kRouteWaves) lds[e] = p.bias[e];
+    __syncthreads();
+  }
+  const int group = sub >> q.lanes;
+  const int in_group = (sub - (group << q.lanes)) * q.slots;
+  const int e0 = group * q.size + in_group;
+  const int n = group < q.groups ? min(q.slots, q.size - in_group) : 0;  // this lane's experts (<= 0: none)
+  float* mine = rows + (lane / LANES) * E;
+
+  for (int64_t t0 = ((int64_t)blockIdx.x * kRouteWaves + wave) * kTokens; t0 < p.rows;
+       t0 += (int64_t)gridDim.x * kRouteWaves * kTokens) {
+    // the wave's rows into LDS (any alignment, 64 consecutive logits at a time)
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i)
+      if (t0 + i < p.rows)
+        for (int e = lane; e < E; e += 64) rows[i * E + e] = load_logit<LT>(p.logits, (t0 + i) * p.ldl + e);
+    wave_fence();
+    float l[NS];
+#pragma unroll
+    for (int s = 0; s < NS; ++s) l[s] = s < n ? mine[e0 + s] : -INFINITY;
+
+    // scores
+    float sc[NS];
+    if (p.score == 0) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int s = 0; s < NS; ++s) top = fmaxf(top, l[s]);
+      top = lanes_max_f32<LANES>(top);
+      double ex[NS], sum = 0.0;
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        ex[s] = l[s] == -INFINITY ? 0.0 : l[s] == top ? 1.0 : exp_acc((double)l[s] - (double)top);
+        sum += ex[s];
+      }
+      sum = lanes_sum_f64<LANES>(sum);
+      const double inv = sum > 0.0 ? 1.0 / sum : 0.0;
+#pragma unroll
+      for (int s = 0; s < NS; ++s) sc[s] = (float)(ex[s] * inv);
+    } else {
+#pragma unroll
+      for (int s = 0; s < NS; ++s) sc[s] = sigmoid_acc(l[s]);
+    }
+    uint32_t key[NS];
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      float c = sc[s];
+      if (s < n) {
+        mine[e0 + s] = sc[s];
+        if (p.bias) c += lds[e0 + s];
+      }
+      key[s] = l[s] > -INFINITY && c > -INFINITY ? order_key(c) : 0u;  // (a NaN compares false)
+    }
+
+    if (q.groups > 1) {
+      uint32_t a = 0, b = 0;
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        b = max(b, min(a, key[s]));
+        a = max(a, key[s]);
+      }
+      if (q.lanes > 0) merge_top2(a, b, dpp_u32<kDppQuadXor1>(a), dpp_u32<kDppQuadXor1>(b));
+      if (q.lanes > 1) merge_top2(a, b, dpp_u32<kDppQuadXor2>(a), dpp_u32<kDppQuadXor2>(b));
+      if (q.lanes > 2) merge_top2(a, b, dpp_u32<kDppRowHalfMirror>(a), dpp_u32<kDppRowHalfMirror>(b));
+      if constexpr (LANES == 64) {
+        if (q.lanes > 3) merge_top2(a, b, dpp_u32<kDppRowMirror>(a), dpp_u32<kDppRowMirror>(b));
+        if (q.lanes > 4) merge_top2(a, b, __shfl_xor(a, 16), __shfl_xor(b, 16));
+      }
+      uint32_t gk = a == 0 ? 0u : p.group_top > 1 && b != 0 ? order_key(key_value(a) + key_value(b)) : a;
+      bool keep = false;
+      for (int r = 0; r < p.top_groups; ++r) {
+        const uint32_t best = lanes_max<LANES>(gk);
+        const uint32_t g = lanes_min<LANES>(gk == best ? (uint32_t)group : ~0u);
+        if ((uint32_t)group == g && best != 0) {
+          keep = true;
+          gk = 0;
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < NS; ++s) key[s] = keep ? key[s] : 0u;
+    }
+
+    int at = -1;  // lane j of the token: its j-th expert
+    for (int j = 0; j < p.k; ++j) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int s = 0; s < NS; ++s) top = max(top, key[s]);
+      const uint32_t best = lanes_max<LANES>(top);
+      int slot = NS;
+#pragma unroll
+      for (int s = NS - 1; s >= 0; --s) slot = key[s] == best ? s : slot;
+      const uint32_t win = lanes_min<LANES>(slot < NS ? (uint32_t)(e0 + slot) : ~0u);
+      if (best == 0) slot = NS;
+      slot = (uint32_t)(e0 + slot) == win ? slot : NS;
+#pragma unroll
+      for (int s = 0; s < NS; ++s) key[s] = s == slot ? 0u : key[s];
+      if (sub == j && best != 0) at = (int)win;
+    }
+    wave_fence();
+    const float s = at >= 0 ? mine[at] : 0.0f;
+    const float sum = lanes_sum_f32<LANES>(s);
+    const int64_t t = t0 + lane / LANES;
+    if (t < p.rows && sub < p.k) {
+      p.idx[t * p.ld_idx + sub] = at;
+      p.w[t * p.ldw + sub] = p.renorm ? (sum > 0.0f ? s / sum * p.scale : 0.0f) : s * p.scale;
+    }
+    wave_fence();  // the rows are free for the next tokens
+  }
+}
+
+// Any number of groups: one wave per token, lane i holds the experts i,
+// i + 64, ..; group values are formed from LDS.  For what route_kernel's
+// layout does not fit (more than 64 groups, or over 16 experts to a lane).
 template <int LT, int NE>
-__global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p) {
+__global__ __launch_bounds__(64 * kRouteWaves) void route_any_kernel(RouteArgs p) {
   __shared__ float cbuf[kRouteWaves][64 * NE];
   __shared__ float sbuf[kRouteWaves][64 * NE];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -117,7 +334,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p) {
       for (int i = 0; i < NE; ++i) s[i] = sum > 0.0 ? (float)(ex[i] / sum) : 0.0f;
     } else {
 #pragma unroll
-      for (int i = 0; i < NE; ++i) s[i] = l[i] < -700.0f ? 0.0f : (float)(1.0 / (1.0 + exp_acc(-(double)l[i])));
+      for (int i = 0; i < NE; ++i) s[i] = sigmoid_acc(l[i]);
     }
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
@@ -209,18 +426,22 @@ __device__ __forceinline__ float exp_below(float l, float top) {
   return l == -INFINITY ? 0.0f : l == top ? 1.0f : expf(l - top);
 }
 
-// One wave per token.  Lane j < k holds the j-th chosen expert.
-template <int LT>
+// One wave per token: lane j < k has the j-th chosen expert, and lane i the
+// logits (where the gradient is dense) and gradients i, i + 64, ..
+template <int LT, int NE>
 __global__ __launch_bounds__(64 * kRouteWaves) void route_grad_kernel(RouteGradArgs p) {
-  __shared__ float vbuf[kRouteWaves][kRouteMaxExperts];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int E = p.experts;
   const bool dense = p.score == 0 && !p.renorm;
   for (int64_t t = (int64_t)blockIdx.x * kRouteWaves + wave; t < p.rows; t += (int64_t)gridDim.x * kRouteWaves) {
-    float top = -INFINITY, total = 0.0f, s = 0.0f, v = 0.0f, dot = 0.0f;
+    float y[NE];
+    if (dense) {
+#pragma unroll
+      for (int i = 0; i < NE; ++i)
+        y[i] = lane + 64 * i < E ? load_logit<LT>(p.logits, t * p.ldl + lane + 64 * i) : -INFINITY;
+    }
+    float l = -INFINITY, v = 0.0f, top = -INFINITY, total = 0.0f, dot = 0.0f;
     int e = -1;
-    for (int x = lane; x < E; x += 64) vbuf[wave][x] = 0.0f;
-    float l = -INFINITY;
     if (lane < p.k) {
       e = p.idx[t * p.ld_idx + lane];
       if ((uint32_t)e < (uint32_t)E) {
@@ -232,22 +453,27 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_grad_kernel(RouteGradA
     }
     if (p.score == 0) {
       top = l;
-      if (dense)
-        for (int x = lane; x < E; x += 64) top = fmaxf(top, load_logit<LT>(p.logits, t * p.ldl + x));
+      if (dense) {
 #pragma unroll
-      for (int m = 1; m < 64; m <<= 1) top = fmaxf(top, __shfl_xor(top, m));
-      s = exp_below(l, top);
+        for (int i = 0; i < NE; ++i) top = fmaxf(top, y[i]);
+      }
+      top = lanes_max_f32<64>(top);
+      float s = exp_below(l, top);
       total = s;
       if (dense) {
         total = 0.0f;
-        for (int x = lane; x < E; x += 64) total += exp_below(load_logit<LT>(p.logits, t * p.ldl + x), top);
+#pragma unroll
+        for (int i = 0; i < NE; ++i) {
+          y[i] = exp_below(y[i], top);
+          total += y[i];
+        }
       }
       total = wave_sum(total);
       s = total > 0.0f ? s / total : 0.0f;
       dot = wave_sum(v * s);
       if (!dense) v = s * (v - dot);
     } else {
-      s = l == -INFINITY ? 0.0f : 1.0f / (1.0f + expf(-l));
+      const float s = l == -INFINITY ? 0.0f : 1.0f / (1.0f + expf(-l));
       float share = s;  // s_j / S when renormalised
       if (p.renorm) {
         total = wave_sum(s);
@@ -256,42 +482,81 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_grad_kernel(RouteGradA
       }
       v = v * share * (1.0f - s);
     }
-    wave_fence();
-    if (e >= 0) vbuf[wave][e] = v;
-    wave_fence();
-    for (int x = lane; x < E; x += 64) {
-      float d = vbuf[wave][x];
-      if (dense) {
-        const float y = exp_below(load_logit<LT>(p.logits, t * p.ldl + x), top);
-        d = total > 0.0f ? y / total * (d - dot) : 0.0f;
-      }
-      if constexpr (LT == 0)
-        reinterpret_cast<uint16_t*>(p.dl)[t * p.lddl + x] = (uint16_t)pack2_bf16(d, 0.0f);
-      else
-        reinterpret_cast<float*>(p.dl)[t * p.lddl + x] = d;
+    float d[NE];
+#pragma unroll
+    for (int i = 0; i < NE; ++i) d[i] = 0.0f;
+    for (int j = 0; j < p.k; ++j) {
+      const int ej = __builtin_amdgcn_readlane(e, j);
+      const float vj = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), j));
+#pragma unroll
+      for (int i = 0; i < NE; ++i) d[i] = lane + 64 * i == ej ? vj : d[i];
     }
-    wave_fence();
+    const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+      const int x = lane + 64 * i;
+      if (x >= E) continue;
+      if (dense) d[i] = y[i] * inv * (d[i] - dot);
+      if constexpr (LT == 0)
+        reinterpret_cast<uint16_t*>(p.dl)[t * p.lddl + x] = (uint16_t)pack2_bf16(d[i], 0.0f);
+      else
+        reinterpret_cast<float*>(p.dl)[t * p.lddl + x] = d[i];
+    }
   }
 }
 
 constexpr int64_t kMaxRouteBlocks = 1 << 20;
 
-int64_t token_blocks(int64_t rows) {
-  const int64_t n = (rows + kRouteWaves - 1) / kRouteWaves;
-  return n < kMaxRouteBlocks ? n : kMaxRouteBlocks;
+unsigned route_blocks(int64_t rows, int tokens_per_wave) {
+  const int64_t per = (int64_t)kRouteWaves * tokens_per_wave;
+  const int64_t n = (rows + per - 1) / per;
+  return (unsigned)(n < kMaxRouteBlocks ? n : kMaxRouteBlocks);
 }
+
+// The layout over `lanes` lanes; slots = 0 where there is none.
+RouteLayout route_layout(const RouteArgs& a, int lanes) {
+  RouteLayout q{a.top_groups < a.groups ? a.groups : 1, 0, 0, 0};
+  q.size = a.experts / q.groups;
+  if (q.groups > lanes) return q;
+  while ((q.groups << (q.lanes + 1)) <= lanes) ++q.lanes;
+  q.slots = (q.size + (1 << q.lanes) - 1) >> q.lanes;
+  return q;
+}
+
+template <int LT, int LANES, int NS>
+hipError_t route_as(const RouteArgs& a, const RouteLayout& q, hipStream_t st) {
+  const size_t lds = (size_t)a.experts * (1 + kRouteWaves * (64 / LANES)) * sizeof(float);
+  hipLaunchKernelGGL((route_kernel<LT, LANES, NS>), dim3(route_blocks(a.rows, 64 / LANES)), dim3(64 * kRouteWaves), lds,
+                     st, a, q);
+  return hipGetLastError();
+}
+
+// From this many tokens on, four to a wave: fewer instructions per token,
+// but a longer chain of them.
+constexpr int64_t kRouteManyRows = 4096;
 
 template <int LT>
 hipError_t route_t(const RouteArgs& a, hipStream_t st) {
-  const dim3 grid((unsigned)token_blocks(a.rows)), block(64 * kRouteWaves);
-  if (a.experts <= 64)
-    hipLaunchKernelGGL((route_kernel<LT, 1>), grid, block, 0, st, a);
-  else if (a.experts <= 128)
-    hipLaunchKernelGGL((route_kernel<LT, 2>), grid, block, 0, st, a);
-  else if (a.experts <= 256)
-    hipLaunchKernelGGL((route_kernel<LT, 4>), grid, block, 0, st, a);
+  if (a.rows >= kRouteManyRows && a.k <= 16) {
+    const RouteLayout q = route_layout(a, 16);
+    if (q.slots > 0 && q.slots <= 16) return route_as<LT, 16, 16>(a, q, st);
+  }
+  const RouteLayout q = route_layout(a, 64);
+  if (q.slots > 0 && q.slots <= 4) return route_as<LT, 64, 4>(a, q, st);
+  if (q.slots > 0 && q.slots <= 8) return route_as<LT, 64, 8>(a, q, st);
+  if (q.slots > 0 && q.slots <= 16) return route_as<LT, 64, 16>(a, q, st);
+  hipLaunchKernelGGL((route_any_kernel<LT, kRouteMaxExperts / 64>), dim3(route_blocks(a.rows, 1)),
+                     dim3(64 * kRouteWaves), 0, st, a);
+  return hipGetLastError();
+}
+
+template <int LT>
+hipError_t route_grad_t(const RouteGradArgs& a, hipStream_t st) {
+  const dim3 grid(route_blocks(a.rows, 1)), block(64 * kRouteWaves);
+  if (a.experts <= 256)
+    hipLaunchKernelGGL((route_grad_kernel<LT, 4>), grid, block, 0, st, a);
   else
-    hipLaunchKernelGGL((route_kernel<LT, 16>), grid, block, 0, st, a);
+    hipLaunchKernelGGL((route_grad_kernel<LT, kRouteMaxExperts / 64>), grid, block, 0, st, a);
   return hipGetLastError();
 }
 
@@ -302,12 +567,7 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t st) {
 }
 
 hipError_t launch_route_grad(const RouteGradArgs& a, hipStream_t st) {
-  const dim3 grid((unsigned)token_blocks(a.rows)), block(64 * kRouteWaves);
-  if (a.l_type == 0)
-    hipLaunchKernelGGL(route_grad_kernel<0>, grid, block, 0, st, a);
-  else
-    hipLaunchKernelGGL(route_grad_kernel<1>, grid, block, 0, st, a);
-  return hipGetLastError();
+  return a.l_type == 0 ? route_grad_t<0>(a, st) : route_grad_t<1>(a, st);
 }
 
 }  // namespace fp8fg

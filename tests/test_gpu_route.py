@@ -209,3 +209,35 @@ def test_gradient_against_differences_of_the_kernel(score, renorm):
         v = rng.uniform(-1, 1, (rows, E))
         diff = [(loss(l + d * v) - loss(l - d * v)) / (2 * d) for d in (2.0 ** -4, 2.0 ** -5)]
         assert abs(diff[1] - np.sum(dl * v)) <= abs(diff[0] - diff[1]) + noise / 2.0 ** -5 + 2.0 ** -20
+
+
+@pytest.mark.parametrize("E,k,groups,top_groups,group_top", [
+    (8, 2, 1, 1, 2), (64, 6, 8, 3, 1), (100, 16, 1, 1, 2), (160, 6, 8, 3, 1), (240, 8, 6, 2, 2), (252, 7, 6, 3, 2),
+    (256, 8, 8, 4, 2), (256, 8, 4, 1, 2), (256, 17, 1, 1, 2), (256, 8, 16, 5, 2), (256, 8, 32, 5, 2), (257, 8, 1, 1, 2),
+    (30, 3, 15, 4, 2)])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_many_rows_match_few(E, k, groups, top_groups, group_top, score):
+    # long calls run several tokens to a wave: the same experts as short
+    # calls choose, and the oracle's on a sample with ties, masks and extremes
+    say("route of many rows: %d experts" % E)
+    rng = np.random.default_rng(E + groups)
+    rows = 4099
+    l = (rng.standard_normal((rows, E)) * 2).astype(np.float32)
+    l[::7] = np.round(l[::7])
+    l[5::50, : E // 2] = -np.inf
+    l[6::50] = -np.inf
+    l[8::50, E - 1] = np.nan
+    l[9::50, 0] = np.inf
+    l[10::50] *= 100
+    bias = (rng.standard_normal(E) * 0.05).astype(np.float32)
+    kw = dict(score=score, groups=groups, top_groups=top_groups, group_top=group_top, scale=1.5)
+    d, b = dev(l), dev(bias)
+    idx, w = T.route(d, k, bias=b, **kw)
+    few = [T.route(d[i:i + 1000], k, bias=b, **kw) for i in range(0, rows, 1000)]
+    assert torch.equal(idx, torch.cat([f[0] for f in few]))
+    assert torch.all((w - torch.cat([f[1] for f in few])).abs() <= 140 * U * w.abs())
+    at = np.concatenate([np.arange(0, 70), np.arange(rows - 9, rows)])
+    with np.errstate(all="ignore"):
+        io, wo = moe.route(l[at], k, bias=bias, **kw)
+    assert np.array_equal(idx.cpu().numpy()[at], io)
+    assert np.all(np.abs(w.cpu().numpy()[at] - wo) <= 70 * U * np.abs(wo) + 1e-37)
