@@ -34,34 +34,53 @@ namespace {
 
 constexpr int kRouteWaves = 4;
 
-// exp(x) for x <= 709, relative error below 2^-36: exp(x) = 2^n exp(r),
+// exp(x) for -200 <= x <= 0, relative error below 2^-36: exp(x) = 2^n exp(r),
 // |r| <= ln(2)/2, with the Taylor polynomial of degree 9 (remainder
-// r^10/10! < 2^-37).
-__device__ __forceinline__ double exp_acc(double x) {
-  if (x < -745.0) return 0.0;
+// r^10/10! < 2^-37).  The coefficients come in scalar registers (as literals
+// each would be moved into vector registers before its FMA).
+struct ExpCoef {
+  double c[7];  // 1/9! .. 1/3!
+};
+
+__device__ __forceinline__ ExpCoef exp_coef() {
+  ExpCoef k = {{1.0 / 362880.0, 1.0 / 40320.0, 1.0 / 5040.0, 1.0 / 720.0, 1.0 / 120.0, 1.0 / 24.0, 1.0 / 6.0}};
+#pragma unroll
+  for (int i = 0; i < 7; ++i) asm("" : "+s"(k.c[i]));
+  return k;
+}
+
+__device__ __forceinline__ double exp_acc(double x, const ExpCoef& k) {
   const double n = __builtin_rint(x * 1.4426950408889634);
   const double r = __builtin_fma(n, -0.6931471805599453, x);
-  double p = 1.0 / 362880.0;
-  p = __builtin_fma(p, r, 1.0 / 40320.0);
-  p = __builtin_fma(p, r, 1.0 / 5040.0);
-  p = __builtin_fma(p, r, 1.0 / 720.0);
-  p = __builtin_fma(p, r, 1.0 / 120.0);
-  p = __builtin_fma(p, r, 1.0 / 24.0);
-  p = __builtin_fma(p, r, 1.0 / 6.0);
+  double p = __builtin_fma(k.c[0], r, k.c[1]);
+#pragma unroll
+  for (int i = 2; i < 7; ++i) p = __builtin_fma(p, r, k.c[i]);
   p = __builtin_fma(p, r, 0.5);
   p = __builtin_fma(p, r, 1.0);
   p = __builtin_fma(p, r, 1.0);
   return __builtin_ldexp(p, (int)n);
 }
 
-// RN32(1 / (1 + exp(-l))): the reciprocal from fp32's and one Newton step in
-// fp64 (error squared: 2^-44).  The denominator's fp32 overflow (l < -88)
-// ends in fp32's denormals, where the quotient is formed as it is.
-__device__ __forceinline__ float sigmoid_acc(float l) {
-  if (l < -80.0f) return l < -700.0f ? 0.0f : (float)(1.0 / (1.0 + exp_acc(-(double)l)));
-  const double d = 1.0 + exp_acc(-(double)l);
-  const double y = (double)__builtin_amdgcn_rcpf((float)d);
-  return (float)__builtin_fma(y, __builtin_fma(-d, y, 1.0), y);
+// What lies this far below the largest has score 0 in fp32 (exp(-200) is
+// 2^-288), without an infinity's special cases.
+constexpr float kExpFloor = -200.0f;
+
+// RN32(1 / (1 + exp(-l))), from e = exp(-|l|) <= 1 without overflow: the
+// reciprocal of 1 + e is fp32's with one Newton step in fp64 (error squared:
+// 2^-44).
+__device__ __forceinline__ float sigmoid_acc(float l, const ExpCoef& k) {
+  const double e = exp_acc((double)fmaxf(-fabsf(l), kExpFloor), k);
+  const double d = 1.0 + e;
+  double y = (double)__builtin_amdgcn_rcpf((float)d);
+  y = __builtin_fma(y, __builtin_fma(-d, y, 1.0), y);
+  return (float)(l >= 0.0f ? y : y * e);
+}
+
+// exp(l - top) to be summed and divided by the sum; masked logits end at the
+// floor (where everything is masked, at 1: no score of theirs is used).
+__device__ __forceinline__ double softmax_term(float l, float top, const ExpCoef& k) {
+  const double d = l == top ? 0.0 : (double)l - (double)top;
+  return exp_acc(__builtin_fmax(d, (double)kExpFloor), k);
 }
 
 // fp32 -> unsigned whose order is the floats' (no NaN reaches it); -0 counts
@@ -86,14 +105,24 @@ __device__ __forceinline__ double wave_sum64(double v) {
   return v;
 }
 
+// A logit as it lies in memory, and its value (NaN: masked).
+template <int LT>
+struct RawLogitOf {
+  using type = float;
+};
+template <>
+struct RawLogitOf<0> {
+  using type = uint16_t;
+};
+template <int LT>
+using RawLogit = typename RawLogitOf<LT>::type;
+
+__device__ __forceinline__ float logit_value(float v) { return v == v ? v : -INFINITY; }
+__device__ __forceinline__ float logit_value(uint16_t v) { return logit_value(bf16_lo(v)); }
+
 template <int LT>
 __device__ __forceinline__ float load_logit(const void* __restrict__ l, int64_t off) {
-  float v;
-  if constexpr (LT == 0)
-    v = bf16_lo(reinterpret_cast<const uint16_t*>(l)[off]);
-  else
-    v = reinterpret_cast<const float*>(l)[off];
-  return v == v ? v : -INFINITY;
+  return logit_value(reinterpret_cast<const RawLogit<LT>*>(l)[off]);
 }
 
 // ------------------------------------------------- lanes of one token
@@ -101,31 +130,12 @@ __device__ __forceinline__ float load_logit(const void* __restrict__ l, int64_t 
 // one of them gets the result.
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);  // (every lane has a source)
 }
 template <int CTRL>
 __device__ __forceinline__ double dpp_f64(double v) {
   const uint64_t u = __builtin_bit_cast(uint64_t, v);
   return __builtin_bit_cast(double, (uint64_t)dpp_u32<CTRL>((uint32_t)(u >> 32)) << 32 | dpp_u32<CTRL>((uint32_t)u));
-}
-
-template <int LANES>
-__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
-  v = max(v, dpp_u32<kDppQuadXor1>(v));
-  v = max(v, dpp_u32<kDppQuadXor2>(v));
-  v = max(v, dpp_u32<kDppRowHalfMirror>(v));
-  v = max(v, dpp_u32<kDppRowMirror>(v));
-  if constexpr (LANES == 64) {
-    const uint32_t a = __builtin_amdgcn_readlane(v, 0), b = __builtin_amdgcn_readlane(v, 16);
-    const uint32_t c = __builtin_amdgcn_readlane(v, 32), d = __builtin_amdgcn_readlane(v, 48);
-    v = max(max(a, b), max(c, d));
-  }
-  return v;
-}
-
-template <int LANES>
-__device__ __forceinline__ uint32_t lanes_min(uint32_t v) {
-  return ~lanes_max<LANES>(~v);
 }
 
 template <int LANES>
@@ -168,10 +178,63 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
+// A candidate as one number: its key, then 1023 - index, so that the larger
+// candidate, the lower index on equal keys, is the larger number.  As the
+// bits of a double between 2 and 4 it is compared and selected by one
+// v_max_f64 / v_min_f64, which this chip issues at the full rate.
+__device__ __forceinline__ double pack(uint32_t key, int index) {
+  const uint64_t u = (uint64_t)key << 10 | (uint32_t)(1023 - index);
+  return __builtin_bit_cast(double, u | 0x4000000000000000ull);
+}
+constexpr double kNoPack = 2.0;  // below every candidate
+__device__ __forceinline__ uint32_t pack_key(double v) {
+  return (uint32_t)(__builtin_bit_cast(uint64_t, v) >> 10);
+}
+__device__ __forceinline__ int pack_index(double v) {
+  return 1023 - (int)((uint32_t)__builtin_bit_cast(uint64_t, v) & 1023u);
+}
+
+// The lanes 16 or 32 apart exchanged, and the larger of both.
+template <int STEP>
+__device__ __forceinline__ double swap_max(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)u, hi = (uint32_t)(u >> 32);
+  if constexpr (STEP == 16) {
+    const auto a = __builtin_amdgcn_permlane16_swap(lo, lo, false, false);
+    const auto b = __builtin_amdgcn_permlane16_swap(hi, hi, false, false);
+    return __builtin_fmax(__builtin_bit_cast(double, (uint64_t)b[0] << 32 | a[0]),
+                          __builtin_bit_cast(double, (uint64_t)b[1] << 32 | a[1]));
+  } else {
+    const auto a = __builtin_amdgcn_permlane32_swap(lo, lo, false, false);
+    const auto b = __builtin_amdgcn_permlane32_swap(hi, hi, false, false);
+    return __builtin_fmax(__builtin_bit_cast(double, (uint64_t)b[0] << 32 | a[0]),
+                          __builtin_bit_cast(double, (uint64_t)b[1] << 32 | a[1]));
+  }
+}
+
+template <int LANES>
+__device__ __forceinline__ double lanes_max_pack(double v) {
+  v = __builtin_fmax(v, dpp_f64<kDppQuadXor1>(v));
+  v = __builtin_fmax(v, dpp_f64<kDppQuadXor2>(v));
+  v = __builtin_fmax(v, dpp_f64<kDppRowHalfMirror>(v));
+  v = __builtin_fmax(v, dpp_f64<kDppRowMirror>(v));
+  if constexpr (LANES == 64) {
+    v = swap_max<16>(v);
+    v = swap_max<32>(v);
+  }
+  return v;
+}
+
 // The two largest of two disjoint sets' two largest (a >= b).
-__device__ __forceinline__ void merge_top2(uint32_t& a, uint32_t& b, uint32_t oa, uint32_t ob) {
-  b = max(min(a, oa), max(b, ob));
-  a = max(a, oa);
+__device__ __forceinline__ void merge_top2(double& a, double& b, double oa, double ob) {
+  b = __builtin_fmax(__builtin_fmin(a, oa), __builtin_fmax(b, ob));
+  a = __builtin_fmax(a, oa);
+}
+
+__device__ __forceinline__ void order2(double& a, double& b) {
+  const double x = __builtin_fmax(a, b);
+  b = __builtin_fmin(a, b);
+  a = x;
 }
 
 // How the experts lie in a token's lanes: each group has `lanes` consecutive
@@ -184,37 +247,51 @@ struct RouteLayout {
   int slots;
 };
 
-// LANES lanes per token, NS >= slots experts per lane in registers.
+// LANES lanes per token, NS >= slots experts per lane in registers, as NS / 4
+// descending lists of 4: an expert that is taken only moves up the list that
+// it heads.
 template <int LT, int LANES, int NS>
 __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p, RouteLayout q) {
   constexpr int kTokens = 64 / LANES;  // of a wave
-  extern __shared__ float lds[];       // bias, then a row of scores per token
+  constexpr int NL = NS / 4;
+  extern __shared__ float lds[];       // a row of logits, then scores, per token
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = lane % LANES;
   const int E = p.experts;
-  float* rows = lds + E + wave * kTokens * E;
-  if (p.bias) {
-    for (int e = threadIdx.x; e < E; e += 64 * kRouteWaves) lds[e] = p.bias[e];
-    __syncthreads();
-  }
+  float* rows = lds + wave * kTokens * E;
+  float* mine = rows + (lane / LANES) * E;
   const int group = sub >> q.lanes;
   const int in_group = (sub - (group << q.lanes)) * q.slots;
   const int e0 = group * q.size + in_group;
   const int n = group < q.groups ? min(q.slots, q.size - in_group) : 0;  // this lane's experts (<= 0: none)
-  float* mine = rows + (lane / LANES) * E;
+  const ExpCoef coef = exp_coef();
+  float bias[NS];
+  if (p.bias) {
+#pragma unroll
+    for (int s = 0; s < NS; ++s) bias[s] = p.bias[min(e0 + s, E - 1)];
+  }
 
   for (int64_t t0 = ((int64_t)blockIdx.x * kRouteWaves + wave) * kTokens; t0 < p.rows;
        t0 += (int64_t)gridDim.x * kRouteWaves * kTokens) {
-    // the wave's rows into LDS (any alignment, 64 consecutive logits at a time)
+    // the wave's rows into LDS (any alignment, 64 consecutive logits at a
+    // time), all loads in flight before the first is stored
+    constexpr int kRuns = LANES * NS / 64;  // of 64 logits in a row
+    // (past the end the last logit again: loads without branches)
+    RawLogit<LT> in[kTokens][kRuns];
 #pragma unroll
     for (int i = 0; i < kTokens; ++i)
-      if (t0 + i < p.rows)
-        for (int e = lane; e < E; e += 64) rows[i * E + e] = load_logit<LT>(p.logits, (t0 + i) * p.ldl + e);
+#pragma unroll
+      for (int r = 0; r < kRuns; ++r)
+        in[i][r] = reinterpret_cast<const RawLogit<LT>*>(p.logits)[min(t0 + i, p.rows - 1) * p.ldl + min(lane + 64 * r, E - 1)];
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i)
+#pragma unroll
+      for (int r = 0; r < kRuns; ++r)
+        if (lane + 64 * r < E) rows[i * E + lane + 64 * r] = logit_value(in[i][r]);
     wave_fence();
     float l[NS];
 #pragma unroll
     for (int s = 0; s < NS; ++s) l[s] = s < n ? mine[e0 + s] : -INFINITY;
 
-    // scores
     float sc[NS];
     if (p.score == 0) {
       float top = -INFINITY;
@@ -224,71 +301,77 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p, Ro
       double ex[NS], sum = 0.0;
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
-        ex[s] = l[s] == -INFINITY ? 0.0 : l[s] == top ? 1.0 : exp_acc((double)l[s] - (double)top);
-        sum += ex[s];
+        ex[s] = softmax_term(l[s], top, coef);
+        sum += s < n ? ex[s] : 0.0;
       }
-      sum = lanes_sum_f64<LANES>(sum);
-      const double inv = sum > 0.0 ? 1.0 / sum : 0.0;
+      const double inv = 1.0 / lanes_sum_f64<LANES>(sum);
 #pragma unroll
       for (int s = 0; s < NS; ++s) sc[s] = (float)(ex[s] * inv);
     } else {
 #pragma unroll
-      for (int s = 0; s < NS; ++s) sc[s] = sigmoid_acc(l[s]);
+      for (int s = 0; s < NS; ++s) sc[s] = sigmoid_acc(l[s], coef);
     }
-    uint32_t key[NS];
+    double c[NL][4];
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
-      float c = sc[s];
-      if (s < n) {
-        mine[e0 + s] = sc[s];
-        if (p.bias) c += lds[e0 + s];
-      }
-      key[s] = l[s] > -INFINITY && c > -INFINITY ? order_key(c) : 0u;  // (a NaN compares false)
+      if (s < n) mine[e0 + s] = sc[s];
+      const float v = p.bias ? sc[s] + bias[s] : sc[s];
+      const bool live = l[s] > -INFINITY && v > -INFINITY;  // (a NaN compares false)
+      c[s / 4][s % 4] = live ? pack(order_key(v), e0 + s) : kNoPack;
+    }
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {  // a sorting network for 4
+      order2(c[i][0], c[i][1]);
+      order2(c[i][2], c[i][3]);
+      order2(c[i][0], c[i][2]);
+      order2(c[i][1], c[i][3]);
+      order2(c[i][1], c[i][2]);
     }
 
     if (q.groups > 1) {
-      uint32_t a = 0, b = 0;
+      double a = c[0][0], b = c[0][1];
 #pragma unroll
-      for (int s = 0; s < NS; ++s) {
-        b = max(b, min(a, key[s]));
-        a = max(a, key[s]);
-      }
-      if (q.lanes > 0) merge_top2(a, b, dpp_u32<kDppQuadXor1>(a), dpp_u32<kDppQuadXor1>(b));
-      if (q.lanes > 1) merge_top2(a, b, dpp_u32<kDppQuadXor2>(a), dpp_u32<kDppQuadXor2>(b));
-      if (q.lanes > 2) merge_top2(a, b, dpp_u32<kDppRowHalfMirror>(a), dpp_u32<kDppRowHalfMirror>(b));
+      for (int i = 1; i < NL; ++i) merge_top2(a, b, c[i][0], c[i][1]);
+      if (q.lanes > 0) merge_top2(a, b, dpp_f64<kDppQuadXor1>(a), dpp_f64<kDppQuadXor1>(b));
+      if (q.lanes > 1) merge_top2(a, b, dpp_f64<kDppQuadXor2>(a), dpp_f64<kDppQuadXor2>(b));
+      if (q.lanes > 2) merge_top2(a, b, dpp_f64<kDppRowHalfMirror>(a), dpp_f64<kDppRowHalfMirror>(b));
       if constexpr (LANES == 64) {
-        if (q.lanes > 3) merge_top2(a, b, dpp_u32<kDppRowMirror>(a), dpp_u32<kDppRowMirror>(b));
+        if (q.lanes > 3) merge_top2(a, b, dpp_f64<kDppRowMirror>(a), dpp_f64<kDppRowMirror>(b));
         if (q.lanes > 4) merge_top2(a, b, __shfl_xor(a, 16), __shfl_xor(b, 16));
       }
-      uint32_t gk = a == 0 ? 0u : p.group_top > 1 && b != 0 ? order_key(key_value(a) + key_value(b)) : a;
+      double g = kNoPack;
+      if (a != kNoPack)
+        g = pack(p.group_top > 1 && b != kNoPack ? order_key(key_value(pack_key(a)) + key_value(pack_key(b))) : pack_key(a),
+                 group);
       bool keep = false;
       for (int r = 0; r < p.top_groups; ++r) {
-        const uint32_t best = lanes_max<LANES>(gk);
-        const uint32_t g = lanes_min<LANES>(gk == best ? (uint32_t)group : ~0u);
-        if ((uint32_t)group == g && best != 0) {
+        const double best = lanes_max_pack<LANES>(g);
+        if (g == best) {  // (where nothing is left, kept lanes without candidates)
           keep = true;
-          gk = 0;
+          g = kNoPack;
         }
       }
 #pragma unroll
-      for (int s = 0; s < NS; ++s) key[s] = keep ? key[s] : 0u;
+      for (int i = 0; i < NL; ++i)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) c[i][s] = keep ? c[i][s] : kNoPack;
     }
 
     int at = -1;  // lane j of the token: its j-th expert
     for (int j = 0; j < p.k; ++j) {
-      uint32_t top = 0;
+      double head = c[0][0];
 #pragma unroll
-      for (int s = 0; s < NS; ++s) top = max(top, key[s]);
-      const uint32_t best = lanes_max<LANES>(top);
-      int slot = NS;
+      for (int i = 1; i < NL; ++i) head = __builtin_fmax(head, c[i][0]);
+      const double best = lanes_max_pack<LANES>(head);
 #pragma unroll
-      for (int s = NS - 1; s >= 0; --s) slot = key[s] == best ? s : slot;
-      const uint32_t win = lanes_min<LANES>(slot < NS ? (uint32_t)(e0 + slot) : ~0u);
-      if (best == 0) slot = NS;
-      slot = (uint32_t)(e0 + slot) == win ? slot : NS;
-#pragma unroll
-      for (int s = 0; s < NS; ++s) key[s] = s == slot ? 0u : key[s];
-      if (sub == j && best != 0) at = (int)win;
+      for (int i = 0; i < NL; ++i) {
+        const bool taken = c[i][0] == best;  // (an empty list stays empty)
+        c[i][0] = taken ? c[i][1] : c[i][0];
+        c[i][1] = taken ? c[i][2] : c[i][1];
+        c[i][2] = taken ? c[i][3] : c[i][2];
+        c[i][3] = taken ? kNoPack : c[i][3];
+      }
+      if (sub == j && best != kNoPack) at = pack_index(best);
     }
     wave_fence();
     const float s = at >= 0 ? mine[at] : 0.0f;
@@ -309,6 +392,7 @@ template <int LT, int NE>
 __global__ __launch_bounds__(64 * kRouteWaves) void route_any_kernel(RouteArgs p) {
   __shared__ float cbuf[kRouteWaves][64 * NE];
   __shared__ float sbuf[kRouteWaves][64 * NE];
+  const ExpCoef coef = exp_coef();
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int E = p.experts;
   for (int64_t t = (int64_t)blockIdx.x * kRouteWaves + wave; t < p.rows; t += (int64_t)gridDim.x * kRouteWaves) {
@@ -326,15 +410,15 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_any_kernel(RouteArgs p
       double ex[NE], sum = 0.0;
 #pragma unroll
       for (int i = 0; i < NE; ++i) {
-        ex[i] = l[i] == -INFINITY ? 0.0 : l[i] == top ? 1.0 : exp_acc((double)l[i] - (double)top);
-        sum += ex[i];
+        ex[i] = softmax_term(l[i], top, coef);
+        sum += lane + 64 * i < E ? ex[i] : 0.0;
       }
-      sum = wave_sum64(sum);
+      const double inv = 1.0 / wave_sum64(sum);
 #pragma unroll
-      for (int i = 0; i < NE; ++i) s[i] = sum > 0.0 ? (float)(ex[i] / sum) : 0.0f;
+      for (int i = 0; i < NE; ++i) s[i] = (float)(ex[i] * inv);
     } else {
 #pragma unroll
-      for (int i = 0; i < NE; ++i) s[i] = sigmoid_acc(l[i]);
+      for (int i = 0; i < NE; ++i) s[i] = sigmoid_acc(l[i], coef);
     }
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
@@ -434,11 +518,12 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_grad_kernel(RouteGradA
   const int E = p.experts;
   const bool dense = p.score == 0 && !p.renorm;
   for (int64_t t = (int64_t)blockIdx.x * kRouteWaves + wave; t < p.rows; t += (int64_t)gridDim.x * kRouteWaves) {
+    RawLogit<LT> in[NE];
     float y[NE];
     if (dense) {
 #pragma unroll
       for (int i = 0; i < NE; ++i)
-        y[i] = lane + 64 * i < E ? load_logit<LT>(p.logits, t * p.ldl + lane + 64 * i) : -INFINITY;
+        in[i] = reinterpret_cast<const RawLogit<LT>*>(p.logits)[t * p.ldl + min(lane + 64 * i, E - 1)];
     }
     float l = -INFINITY, v = 0.0f, top = -INFINITY, total = 0.0f, dot = 0.0f;
     int e = -1;
@@ -455,7 +540,10 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_grad_kernel(RouteGradA
       top = l;
       if (dense) {
 #pragma unroll
-        for (int i = 0; i < NE; ++i) top = fmaxf(top, y[i]);
+        for (int i = 0; i < NE; ++i) {
+          y[i] = lane + 64 * i < E ? logit_value(in[i]) : -INFINITY;
+          top = fmaxf(top, y[i]);
+        }
       }
       top = lanes_max_f32<64>(top);
       float s = exp_below(l, top);
@@ -525,7 +613,7 @@ RouteLayout route_layout(const RouteArgs& a, int lanes) {
 
 template <int LT, int LANES, int NS>
 hipError_t route_as(const RouteArgs& a, const RouteLayout& q, hipStream_t st) {
-  const size_t lds = (size_t)a.experts * (1 + kRouteWaves * (64 / LANES)) * sizeof(float);
+  const size_t lds = (size_t)a.experts * kRouteWaves * (64 / LANES) * sizeof(float);
   hipLaunchKernelGGL((route_kernel<LT, LANES, NS>), dim3(route_blocks(a.rows, 64 / LANES)), dim3(64 * kRouteWaves), lds,
                      st, a, q);
   return hipGetLastError();
