@@ -126,7 +126,7 @@ __device__ __forceinline__ float load_logit(const void* __restrict__ l, int64_t 
 }
 
 // ------------------------------------------------- lanes of one token
-// Reductions over the LANES (16: a DPP row, or 64) that hold a token; every
+// Reductions over the LANES (32 or 64) that hold a token; every
 // one of them gets the result.
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
@@ -141,10 +141,8 @@ __device__ __forceinline__ double dpp_f64(double v) {
 template <int LANES>
 __device__ __forceinline__ float lanes_max_f32(float v) {
   v = row16_max(v);
-  if constexpr (LANES == 64) {
-    v = fmaxf(v, __shfl_xor(v, 16));
-    v = fmaxf(v, __shfl_xor(v, 32));
-  }
+  v = fmaxf(v, __shfl_xor(v, 16));
+  if constexpr (LANES == 64) v = fmaxf(v, __shfl_xor(v, 32));
   return v;
 }
 
@@ -154,10 +152,8 @@ __device__ __forceinline__ double lanes_sum_f64(double v) {
   v += dpp_f64<kDppQuadXor2>(v);
   v += dpp_f64<kDppRowHalfMirror>(v);
   v += dpp_f64<kDppRowMirror>(v);
-  if constexpr (LANES == 64) {
-    v += __shfl_xor(v, 16);
-    v += __shfl_xor(v, 32);
-  }
+  v += __shfl_xor(v, 16);
+  if constexpr (LANES == 64) v += __shfl_xor(v, 32);
   return v;
 }
 
@@ -167,10 +163,8 @@ __device__ __forceinline__ float lanes_sum_f32(float v) {
   v += dpp_mov<kDppQuadXor2>(v);
   v += dpp_mov<kDppRowHalfMirror>(v);
   v += dpp_mov<kDppRowMirror>(v);
-  if constexpr (LANES == 64) {
-    v += __shfl_xor(v, 16);
-    v += __shfl_xor(v, 32);
-  }
+  v += __shfl_xor(v, 16);
+  if constexpr (LANES == 64) v += __shfl_xor(v, 32);
   return v;
 }
 
@@ -178,19 +172,19 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
-// A candidate as one number: its key, then 1023 - index, so that the larger
-// candidate, the lower index on equal keys, is the larger number.  As the
+// A candidate as one number: its key, then 1023 - place, so that the larger
+// candidate, the lower place on equal keys, is the larger number.  As the
 // bits of a double between 2 and 4 it is compared and selected by one
 // v_max_f64 / v_min_f64, which this chip issues at the full rate.
-__device__ __forceinline__ double pack(uint32_t key, int index) {
-  const uint64_t u = (uint64_t)key << 10 | (uint32_t)(1023 - index);
+__device__ __forceinline__ double pack(uint32_t key, int place) {
+  const uint64_t u = (uint64_t)key << 10 | (uint32_t)(1023 - place);
   return __builtin_bit_cast(double, u | 0x4000000000000000ull);
 }
 constexpr double kNoPack = 2.0;  // below every candidate
 __device__ __forceinline__ uint32_t pack_key(double v) {
   return (uint32_t)(__builtin_bit_cast(uint64_t, v) >> 10);
 }
-__device__ __forceinline__ int pack_index(double v) {
+__device__ __forceinline__ int pack_place(double v) {
   return 1023 - (int)((uint32_t)__builtin_bit_cast(uint64_t, v) & 1023u);
 }
 
@@ -212,16 +206,15 @@ __device__ __forceinline__ double swap_max(double v) {
   }
 }
 
+// (`same`: log2 of the consecutive lanes that hold equal values already.)
 template <int LANES>
-__device__ __forceinline__ double lanes_max_pack(double v) {
-  v = __builtin_fmax(v, dpp_f64<kDppQuadXor1>(v));
-  v = __builtin_fmax(v, dpp_f64<kDppQuadXor2>(v));
+__device__ __forceinline__ double lanes_max_pack(double v, int same = 0) {
+  if (same < 1) v = __builtin_fmax(v, dpp_f64<kDppQuadXor1>(v));
+  if (same < 2) v = __builtin_fmax(v, dpp_f64<kDppQuadXor2>(v));
   v = __builtin_fmax(v, dpp_f64<kDppRowHalfMirror>(v));
   v = __builtin_fmax(v, dpp_f64<kDppRowMirror>(v));
-  if constexpr (LANES == 64) {
-    v = swap_max<16>(v);
-    v = swap_max<32>(v);
-  }
+  v = swap_max<16>(v);
+  if constexpr (LANES == 64) v = swap_max<32>(v);
   return v;
 }
 
@@ -239,85 +232,85 @@ __device__ __forceinline__ void order2(double& a, double& b) {
 
 // How the experts lie in a token's lanes: each group has `lanes` consecutive
 // lanes (a power of two), each of which has `slots` consecutive experts of
-// the group.  The lower expert is in the lower lane, then the lower slot.
+// the group.  The lower expert is in the lower lane, then the lower slot:
+// place = lane * NS + slot orders candidates as their indexes do.
 struct RouteLayout {
   int groups;  // 1 where groups play no part
   int size;    // experts per group
   int lanes;   // log2
   int slots;
+  int vec;     // every lane's experts are NS whole ones, aligned: 16-byte loads
 };
+
+// The NS values from e0 on of a row of E (past its end the last ones: loads
+// without branches, all in flight).
+template <typename T, int NS>
+__device__ __forceinline__ void load_slots(const T* __restrict__ row, int e0, int E, int vec, T (&v)[NS]) {
+  if (vec && NS * sizeof(T) >= 16) {
+    struct alignas(16) Run {
+      T v[NS];
+    };
+    const Run r = *reinterpret_cast<const Run*>(row + min(e0, E - NS));
+#pragma unroll
+    for (int s = 0; s < NS; ++s) v[s] = r.v[s];
+  } else {
+#pragma unroll
+    for (int s = 0; s < NS; ++s) v[s] = row[min(e0 + s, E - 1)];
+  }
+}
 
 // LANES lanes per token, NS >= slots experts per lane in registers, as NS / 4
 // descending lists of 4: an expert that is taken only moves up the list that
 // it heads.
-template <int LT, int LANES, int NS>
+template <int LT, int LANES, int NS, int SCORE>
 __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p, RouteLayout q) {
   constexpr int kTokens = 64 / LANES;  // of a wave
   constexpr int NL = NS / 4;
-  extern __shared__ float lds[];       // a row of logits, then scores, per token
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = lane % LANES;
   const int E = p.experts;
-  float* rows = lds + wave * kTokens * E;
-  float* mine = rows + (lane / LANES) * E;
   const int group = sub >> q.lanes;
   const int in_group = (sub - (group << q.lanes)) * q.slots;
   const int e0 = group * q.size + in_group;
   const int n = group < q.groups ? min(q.slots, q.size - in_group) : 0;  // this lane's experts (<= 0: none)
   const ExpCoef coef = exp_coef();
+  __shared__ float scores[kRouteWaves][64 * NS];
+  float* mine = scores[wave] + (lane / LANES) * LANES * NS;
   float bias[NS];
-  if (p.bias) {
-#pragma unroll
-    for (int s = 0; s < NS; ++s) bias[s] = p.bias[min(e0 + s, E - 1)];
-  }
+  if (p.bias) load_slots<float, NS>(p.bias, e0, E, q.vec, bias);
 
   for (int64_t t0 = ((int64_t)blockIdx.x * kRouteWaves + wave) * kTokens; t0 < p.rows;
        t0 += (int64_t)gridDim.x * kRouteWaves * kTokens) {
-    // the wave's rows into LDS (any alignment, 64 consecutive logits at a
-    // time), all loads in flight before the first is stored
-    constexpr int kRuns = LANES * NS / 64;  // of 64 logits in a row
-    // (past the end the last logit again: loads without branches)
-    RawLogit<LT> in[kTokens][kRuns];
-#pragma unroll
-    for (int i = 0; i < kTokens; ++i)
-#pragma unroll
-      for (int r = 0; r < kRuns; ++r)
-        in[i][r] = reinterpret_cast<const RawLogit<LT>*>(p.logits)[min(t0 + i, p.rows - 1) * p.ldl + min(lane + 64 * r, E - 1)];
-#pragma unroll
-    for (int i = 0; i < kTokens; ++i)
-#pragma unroll
-      for (int r = 0; r < kRuns; ++r)
-        if (lane + 64 * r < E) rows[i * E + lane + 64 * r] = logit_value(in[i][r]);
-    wave_fence();
+    // (lanes without experts or token read the last one's)
+    const int64_t t = t0 + lane / LANES;
+    const int64_t row = min(t, p.rows - 1) * p.ldl;
+    RawLogit<LT> in[NS];
+    load_slots<RawLogit<LT>, NS>(reinterpret_cast<const RawLogit<LT>*>(p.logits) + row, e0, E, q.vec, in);
     float l[NS];
 #pragma unroll
-    for (int s = 0; s < NS; ++s) l[s] = s < n ? mine[e0 + s] : -INFINITY;
+    for (int s = 0; s < NS; ++s) l[s] = s < n ? logit_value(in[s]) : -INFINITY;
 
-    float sc[NS];
-    if (p.score == 0) {
-      float top = -INFINITY;
+    float top = -INFINITY;
+    double inv = 0.0;
+    double c[NL][4];  // softmax: the terms, until the scores replace them
+    if constexpr (SCORE == 0) {
 #pragma unroll
       for (int s = 0; s < NS; ++s) top = fmaxf(top, l[s]);
       top = lanes_max_f32<LANES>(top);
-      double ex[NS], sum = 0.0;
+      double sum = 0.0;
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
-        ex[s] = softmax_term(l[s], top, coef);
-        sum += s < n ? ex[s] : 0.0;
+        c[s / 4][s % 4] = softmax_term(l[s], top, coef);
+        sum += s < n ? c[s / 4][s % 4] : 0.0;
       }
-      const double inv = 1.0 / lanes_sum_f64<LANES>(sum);
-#pragma unroll
-      for (int s = 0; s < NS; ++s) sc[s] = (float)(ex[s] * inv);
-    } else {
-#pragma unroll
-      for (int s = 0; s < NS; ++s) sc[s] = sigmoid_acc(l[s], coef);
+      inv = 1.0 / lanes_sum_f64<LANES>(sum);
     }
-    double c[NL][4];
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
-      if (s < n) mine[e0 + s] = sc[s];
-      const float v = p.bias ? sc[s] + bias[s] : sc[s];
+      const float sc = SCORE == 0 ? (float)(c[s / 4][s % 4] * inv) : sigmoid_acc(l[s], coef);
+      const float v = p.bias ? sc + bias[s] : sc;
       const bool live = l[s] > -INFINITY && v > -INFINITY;  // (a NaN compares false)
-      c[s / 4][s % 4] = live ? pack(order_key(v), e0 + s) : kNoPack;
+      mine[sub * NS + s] = sc;
+      c[s / 4][s % 4] = live ? pack(order_key(v), sub * NS + s) : kNoPack;
     }
 #pragma unroll
     for (int i = 0; i < NL; ++i) {  // a sorting network for 4
@@ -335,8 +328,8 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p, Ro
       if (q.lanes > 0) merge_top2(a, b, dpp_f64<kDppQuadXor1>(a), dpp_f64<kDppQuadXor1>(b));
       if (q.lanes > 1) merge_top2(a, b, dpp_f64<kDppQuadXor2>(a), dpp_f64<kDppQuadXor2>(b));
       if (q.lanes > 2) merge_top2(a, b, dpp_f64<kDppRowHalfMirror>(a), dpp_f64<kDppRowHalfMirror>(b));
+      if (q.lanes > 3) merge_top2(a, b, dpp_f64<kDppRowMirror>(a), dpp_f64<kDppRowMirror>(b));
       if constexpr (LANES == 64) {
-        if (q.lanes > 3) merge_top2(a, b, dpp_f64<kDppRowMirror>(a), dpp_f64<kDppRowMirror>(b));
         if (q.lanes > 4) merge_top2(a, b, __shfl_xor(a, 16), __shfl_xor(b, 16));
       }
       double g = kNoPack;
@@ -345,19 +338,20 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p, Ro
                  group);
       bool keep = false;
       for (int r = 0; r < p.top_groups; ++r) {
-        const double best = lanes_max_pack<LANES>(g);
+        const double best = lanes_max_pack<LANES>(g, q.lanes);
         if (g == best) {  // (where nothing is left, kept lanes without candidates)
           keep = true;
           g = kNoPack;
         }
       }
+      if (!keep) {
 #pragma unroll
-      for (int i = 0; i < NL; ++i)
-#pragma unroll
-        for (int s = 0; s < 4; ++s) c[i][s] = keep ? c[i][s] : kNoPack;
+        for (int i = 0; i < NL; ++i) c[i][0] = c[i][1] = c[i][2] = c[i][3] = kNoPack;
+        asm volatile("" : "+v"(c[0][0]));
+      }
     }
 
-    int at = -1;  // lane j of the token: its j-th expert
+    int at = -1;  // lane j of the token: the place of its j-th expert
     for (int j = 0; j < p.k; ++j) {
       double head = c[0][0];
 #pragma unroll
@@ -365,23 +359,29 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p, Ro
       const double best = lanes_max_pack<LANES>(head);
 #pragma unroll
       for (int i = 0; i < NL; ++i) {
-        const bool taken = c[i][0] == best;  // (an empty list stays empty)
-        c[i][0] = taken ? c[i][1] : c[i][0];
-        c[i][1] = taken ? c[i][2] : c[i][1];
-        c[i][2] = taken ? c[i][3] : c[i][2];
-        c[i][3] = taken ? kNoPack : c[i][3];
+        if (c[i][0] == best) {  // (an empty list stays empty)
+          c[i][0] = c[i][1];
+          c[i][1] = c[i][2];
+          c[i][2] = c[i][3];
+          c[i][3] = kNoPack;
+          asm volatile("" : "+v"(c[i][0]));  // moves under the lanes' mask, no selects
+        }
       }
-      if (sub == j && best != kNoPack) at = pack_index(best);
+      if (sub == j && best != kNoPack) at = pack_place(best);
     }
     wave_fence();
-    const float s = at >= 0 ? mine[at] : 0.0f;
+    float s = 0.0f;
+    if (at >= 0) {
+      s = mine[at];
+      const int from = at / NS;
+      at = (from >> q.lanes) * q.size + (from & ((1 << q.lanes) - 1)) * q.slots + at % NS;
+    }
     const float sum = lanes_sum_f32<LANES>(s);
-    const int64_t t = t0 + lane / LANES;
     if (t < p.rows && sub < p.k) {
       p.idx[t * p.ld_idx + sub] = at;
       p.w[t * p.ldw + sub] = p.renorm ? (sum > 0.0f ? s / sum * p.scale : 0.0f) : s * p.scale;
     }
-    wave_fence();  // the rows are free for the next tokens
+    wave_fence();  // the scores' places are free for the next tokens
   }
 }
 
@@ -603,7 +603,7 @@ unsigned route_blocks(int64_t rows, int tokens_per_wave) {
 
 // The layout over `lanes` lanes; slots = 0 where there is none.
 RouteLayout route_layout(const RouteArgs& a, int lanes) {
-  RouteLayout q{a.top_groups < a.groups ? a.groups : 1, 0, 0, 0};
+  RouteLayout q{a.top_groups < a.groups ? a.groups : 1, 0, 0, 0, 0};
   q.size = a.experts / q.groups;
   if (q.groups > lanes) return q;
   while ((q.groups << (q.lanes + 1)) <= lanes) ++q.lanes;
@@ -613,21 +613,27 @@ RouteLayout route_layout(const RouteArgs& a, int lanes) {
 
 template <int LT, int LANES, int NS>
 hipError_t route_as(const RouteArgs& a, const RouteLayout& q, hipStream_t st) {
-  const size_t lds = (size_t)a.experts * kRouteWaves * (64 / LANES) * sizeof(float);
-  hipLaunchKernelGGL((route_kernel<LT, LANES, NS>), dim3(route_blocks(a.rows, 64 / LANES)), dim3(64 * kRouteWaves), lds,
-                     st, a, q);
+  RouteLayout l = q;
+  constexpr int kPer16 = LT == 0 ? 8 : 4;
+  l.vec = NS % kPer16 == 0 && q.slots == NS && q.size % NS == 0 && a.ldl % kPer16 == 0 &&
+          reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 && reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
+  const dim3 grid(route_blocks(a.rows, 64 / LANES)), block(64 * kRouteWaves);
+  if (a.score == 0)
+    hipLaunchKernelGGL((route_kernel<LT, LANES, NS, 0>), grid, block, 0, st, a, l);
+  else
+    hipLaunchKernelGGL((route_kernel<LT, LANES, NS, 1>), grid, block, 0, st, a, l);
   return hipGetLastError();
 }
 
-// From this many tokens on, four to a wave: fewer instructions per token,
-// but a longer chain of them.
+// From this many tokens on, two to a wave: fewer instructions per token, but
+// a longer chain of them.
 constexpr int64_t kRouteManyRows = 4096;
 
 template <int LT>
 hipError_t route_t(const RouteArgs& a, hipStream_t st) {
-  if (a.rows >= kRouteManyRows && a.k <= 16) {
-    const RouteLayout q = route_layout(a, 16);
-    if (q.slots > 0 && q.slots <= 16) return route_as<LT, 16, 16>(a, q, st);
+  if (a.rows >= kRouteManyRows && a.k <= 32) {
+    const RouteLayout q = route_layout(a, 32);
+    if (q.slots > 0 && q.slots <= 8) return route_as<LT, 32, 8>(a, q, st);
   }
   const RouteLayout q = route_layout(a, 64);
   if (q.slots > 0 && q.slots <= 4) return route_as<LT, 64, 4>(a, q, st);
