@@ -1,9 +1,11 @@
-"""Build libfp8fg.so (HIP, gfx950) in-tree.
+"""Build libfp8fg.so (HIP, gfx950) and _native.so in-tree.
 
     python -m fp8_fine_grained_x1_amd.build
 
-Objects go to ``_build/`` at the repository root; the shared library is
-written next to this file.  Every call recompiles.
+Objects go to ``_build/`` at the repository root; the shared libraries are
+written next to this file.  Every call recompiles.  ``_native.so`` is the
+Python module of the tensor helpers in ``csrc/native.cpp`` (host code against
+torch's headers; it loads libfp8fg.so from its own folder).
 
 ``build_host_sanitized()`` compiles the same sources with AddressSanitizer
 and UndefinedBehaviorSanitizer on the host code only (argument validation,
@@ -25,6 +27,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfp8fg.so")
+NATIVE = os.path.join(PKG, "_native.so")
 
 SOURCES = ["abi.cpp", "quant.hip", "gemm.hip", "norm.hip", "route.hip", "dispatch.hip"]
 
@@ -66,18 +69,48 @@ def _compile(src, outdir=BUILD, extra=()):
     return obj
 
 
+def _compile_native():
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    obj = os.path.join(BUILD, "native.o")
+    cmd = (["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-fvisibility=hidden",
+            "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI), "-I" + INCLUDE,
+            "-I" + sysconfig.get_paths()["include"]] +
+           ["-isystem" + p for p in cpp_extension.include_paths()] +
+           ["-c", os.path.join(CSRC, "native.cpp"), "-o", obj])
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("compile failed: %s\n%s\n%s" % (" ".join(cmd), r.stdout, r.stderr))
+    return obj, os.path.join(os.path.dirname(torch.__file__), "lib")
+
+
+def _link_native(obj, torch_lib):
+    tmp = NATIVE + ".tmp"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L" + PKG, "-l:" + os.path.basename(LIB), "-L" + torch_lib,
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("link failed: %s\n%s\n%s" % (" ".join(cmd), r.stdout, r.stderr))
+    shutil.move(tmp, NATIVE)
+
+
 def build(verbose=True):
     if not os.path.exists(HIPCC):
         raise RuntimeError("hipcc not found at %s" % HIPCC)
     os.makedirs(BUILD, exist_ok=True)
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        native = ex.submit(_compile_native)
         objs = list(ex.map(_compile, SOURCES))
+        native = native.result()
     tmp = LIB + ".tmp"
     cmd = [HIPCC, "-shared", "--offload-arch=gfx950", "-fPIC", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("link failed: %s\n%s\n%s" % (" ".join(cmd), r.stdout, r.stderr))
     shutil.move(tmp, LIB)
+    _link_native(*native)
     if verbose:
         print("built", LIB)
     return LIB

@@ -138,46 +138,50 @@ def grouped_gemm(qa, sa, offsets, qb, sb, out_dtype=torch.bfloat16, out=None, st
     return c
 
 
-def _need(ok, what):
-    if not ok:
-        raise ValueError(what)
+_native_module = None
 
 
-def _alloc(rows, cols, dtype, device):
-    # empty_strided is the cheapest of torch's allocating calls
-    return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
+def _native():
+    """The native helpers (checks, allocation, call) of the functions below."""
+    global _native_module
+    if _native_module is None:
+        try:
+            from . import _native as m
+        except ImportError as e:
+            raise RuntimeError("the _native module is not built; run `python -m fp8_fine_grained_x1_amd.build`") from e
+        m.set_error(B.Fp8fgError)
+        _native_module = m
+    return _native_module
 
 
-def _alloc1(n, dtype, device):
-    return torch.empty_strided((n,), (1,), dtype=dtype, device=device)
-
-
-def _rows2d(name, x, like=None, dtypes=None):
-    """x is a 2-d GPU tensor with contiguous rows, where `like` is given of
-    its shape, type and device."""
-    _need(x.is_cuda, "%s must be on the GPU" % name)
-    _need(x.dim() == 2 and (x.stride(1) == 1 or x.shape[1] <= 1), "%s must be 2-d with contiguous rows" % name)
-    if dtypes is not None:
-        _need(x.dtype in dtypes, "%s has type %s" % (name, x.dtype))
-    if like is not None:
-        _need(x.shape == like.shape and x.dtype == like.dtype and x.device == like.device,
-              "%s does not match in shape, type or device" % name)
-
-
-def _pitch(x):
-    """Row pitch of a 2-d tensor; a single row's stride carries no meaning."""
-    return x.stride(0) if x.shape[0] > 1 else max(x.shape[1], 1)
-
-
-def _on_stream(stream, *tensors):
-    """Tells torch's allocator that tensors of the current stream are in use
-    on `stream` (a torch stream or a raw handle)."""
+def _handle(stream, x):
+    """hipStream_t of `stream` (a torch stream or a raw handle), or of the
+    current stream of x's device."""
     if stream is None:
-        return
-    for t in tensors:
-        if t is not None and t.is_cuda:
-            st = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=t.device)
-            t.record_stream(st)
+        d = x.get_device()
+        return torch._C._cuda_getCurrentRawStream(d) if d >= 0 else 0
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _on_stream(stream, tensors):
+    """Tells torch's allocator that tensors of the current stream are in use
+    on `stream`; returns them."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None and t.is_cuda:
+                t.record_stream(stream if hasattr(stream, "cuda_stream") else
+                                torch.cuda.ExternalStream(int(stream), device=t.device))
+    return tensors
+
+
+_LAYOUT = {"group_major": True, "row_major": False}
+_SCORE = {"softmax": B.FP8FG_SCORE_SOFTMAX, "sigmoid": B.FP8FG_SCORE_SIGMOID}
+
+
+def _of(table, key, name):
+    if key not in table:
+        raise ValueError("%s must be one of %s" % (name, sorted(table)))
+    return table[key]
 
 
 def rmsnorm_quantize(x, gamma, residual=None, eps=1e-6, pow2=False, scale_layout="group_major",
@@ -185,87 +189,30 @@ def rmsnorm_quantize(x, gamma, residual=None, eps=1e-6, pow2=False, scale_layout
     """h = x + residual (x where there is none), y = h * rstd * gamma, and
     y in E4M3 with 1x128 scales.  Returns (q, s, h, y, rstd); y is None
     unless want_y."""
-    _rows2d("x", x, dtypes=_XTYPE)
-    M, C = x.shape
-    _need(gamma.dim() == 1 and gamma.shape[0] == C and gamma.is_contiguous() and gamma.dtype in _XTYPE and
-          gamma.device == x.device, "gamma must be a contiguous vector of the columns")
-    if residual is not None:
-        _rows2d("residual", residual, like=x)
-    dev = x.device
-    q = _alloc(M, C, torch.uint8, dev)
-    s = _scales(M, C // 128, scale_layout, dev)
-    h = x if residual is None else _alloc(M, C, x.dtype, dev)
-    y = _alloc(M, C, x.dtype, dev) if want_y else None
-    rstd = _alloc1(M, torch.float32, dev)
-    B.fp8_rmsnorm_quantize(x, _XTYPE[x.dtype], M, C, _pitch(x), residual,
-                           0 if residual is None else _pitch(residual), gamma, _XTYPE[gamma.dtype],
-                           eps, _rule(pow2), None if residual is None else h, C, y, C, q, C, s,
-                           s.stride(0), s.stride(1), rstd, stream)
-    _on_stream(stream, q, s, h, y, rstd)
-    return q, s, h, y, rstd
+    out = _native().rmsnorm_quantize(x, gamma, residual, eps, _rule(pow2), _of(_LAYOUT, scale_layout, "scale_layout"),
+                                     want_y, _handle(stream, x))
+    return _on_stream(stream, out)
 
 
 def rmsnorm_backward(dy, h, gamma, rstd, dh=None, stream=None):
     """Gradients of rmsnorm_quantize's y (through the quantizer as it is) and,
     with dh, of its h.  Returns (dx, dgamma); dx is residual's gradient too."""
-    _rows2d("h", h, dtypes=_XTYPE)
-    _rows2d("dy", dy, like=h)
-    if dh is not None:
-        _rows2d("dh", dh, like=h)
-    M, C = h.shape
-    _need(gamma.dim() == 1 and gamma.shape[0] == C and gamma.is_contiguous() and gamma.dtype in _XTYPE and
-          gamma.device == h.device, "gamma must be a contiguous vector of the columns")
-    _need(rstd.shape == (M,) and rstd.dtype == torch.float32 and rstd.is_contiguous() and rstd.device == h.device,
-          "rstd must be a contiguous f32 vector of the rows")
-    dx = _alloc(M, C, h.dtype, h.device)
-    dgamma = _alloc1(C, torch.float32, h.device)
-    n = B.fp8_rmsnorm_backward_workspace(M, C)
-    ws = _alloc1(max(n, 16), torch.uint8, h.device)
-    B.fp8_rmsnorm_backward(dy, _XTYPE[h.dtype], M, C, _pitch(dy), dh, 0 if dh is None else _pitch(dh), h,
-                           _pitch(h), gamma, _XTYPE[gamma.dtype], rstd, dx, C, dgamma, ws, n, stream)
-    _on_stream(stream, dx, dgamma, ws)
-    return dx, dgamma
-
-
-_SCORE = {"softmax": B.FP8FG_SCORE_SOFTMAX, "sigmoid": B.FP8FG_SCORE_SIGMOID}
+    return _on_stream(stream, _native().rmsnorm_backward(dy, h, gamma, rstd, dh, _handle(stream, h)))[:2]
 
 
 def route(logits, k, bias=None, score="softmax", groups=1, top_groups=1, group_top=2, renorm=True,
           scale=1.0, stream=None):
     """The k experts of each token and their weights; see fp8_route in
     include/fp8fg.h for the choice, masks and ties."""
-    _rows2d("logits", logits, dtypes=_XTYPE)
-    _need(score in _SCORE, "score must be 'softmax' or 'sigmoid'")
-    M, E = logits.shape
-    if bias is not None:
-        _need(bias.shape == (E,) and bias.dtype == torch.float32 and bias.is_contiguous() and
-              bias.device == logits.device, "bias must be a contiguous f32 vector of the experts")
-    idx = _alloc(M, k, torch.int32, logits.device)
-    w = _alloc(M, k, torch.float32, logits.device)
-    B.fp8_route(logits, _XTYPE[logits.dtype], M, E, _pitch(logits), bias, _SCORE[score], groups,
-                top_groups, group_top, k, int(renorm), scale, idx, k, w, k, stream)
-    _on_stream(stream, idx, w)
-    return idx, w
+    out = _native().route(logits, k, bias, _of(_SCORE, score, "score"), groups, top_groups, group_top, renorm, scale,
+                          _handle(stream, logits))
+    return _on_stream(stream, out)
 
 
 def route_backward(dw, logits, idx, score="softmax", renorm=True, scale=1.0, stream=None):
     """Gradient of route's weights with respect to the logits."""
-    _rows2d("logits", logits, dtypes=_XTYPE)
-    _need(score in _SCORE, "score must be 'softmax' or 'sigmoid'")
-    M, E = logits.shape
-    _rows2d("idx", idx, dtypes=(torch.int32,))
-    _rows2d("dw", dw, dtypes=(torch.float32,))
-    k = idx.shape[1]
-    _need(idx.shape == (M, k) and dw.shape == (M, k) and idx.device == logits.device and dw.device == logits.device,
-          "idx and dw must be [tokens][k] on the logits' device")
-    dl = _alloc(M, E, logits.dtype, logits.device)
-    B.fp8_route_backward(logits, _XTYPE[logits.dtype], M, E, _pitch(logits), _SCORE[score], k, int(renorm),
-                         scale, idx, _pitch(idx), dw, _pitch(dw), dl, E, stream)
-    _on_stream(stream, dl)
-    return dl
-
-
-_MOVE = {torch.uint8: B.FP8FG_E4M3, torch.bfloat16: B.FP8FG_BF16, torch.float32: B.FP8FG_F32}
+    out = _native().route_backward(dw, logits, idx, _of(_SCORE, score, "score"), renorm, scale, _handle(stream, logits))
+    return _on_stream(stream, out)[0]
 
 
 def dispatch(idx, experts, x, s=None, scale_layout="group_major", stream=None):
@@ -273,70 +220,17 @@ def dispatch(idx, experts, x, s=None, scale_layout="group_major", stream=None):
     into the order of their experts.  Returns (x', s', offsets, pos, token);
     s' is None for bf16 / f32.  Entries of idx outside [0, experts) come last
     with zero rows."""
-    _rows2d("idx", idx, dtypes=(torch.int32,))
-    _rows2d("x", x, dtypes=_MOVE)
-    M, k = idx.shape
-    C = x.shape[1]
-    dev = x.device
-    _need(x.shape[0] == M and idx.device == dev, "idx must be [tokens][k] on x's device")
-    e4m3 = x.dtype == torch.uint8
-    _need((s is not None) == e4m3, "E4M3 rows need their scales, others have none")
-    out_s = None
-    if e4m3:
-        _need(s.shape == (M, C // 128) and s.dtype == torch.float32 and s.device == dev,
-              "s must be the f32 [tokens][columns / 128] scales of x")
-        out_s = _scales(M * k, C // 128, scale_layout, dev)
-    out = _alloc(M * k, C, x.dtype, dev)
-    offsets = _alloc1(experts + 1, torch.int32, dev)
-    pos = _alloc(M, k, torch.int32, dev)
-    token = _alloc1(M * k, torch.int32, dev)
-    n = B.fp8_dispatch_workspace(M, k, experts)
-    ws = _alloc1(max(n, 16), torch.uint8, dev)
-    st = (s.stride(0), s.stride(1), out_s.stride(0), out_s.stride(1)) if e4m3 else (0, 0, 0, 0)
-    B.fp8_dispatch(idx, _pitch(idx), M, k, experts, x, _MOVE[x.dtype], C, _pitch(x), s, st[0], st[1],
-                   offsets, pos, token, out, C, out_s, st[2], st[3], ws, n, stream)
-    _on_stream(stream, out, out_s, offsets, pos, token, ws)
-    return out, out_s, offsets, pos, token
-
-
-def _check_places(pos, w, like):
-    _need(pos.dim() == 2 and pos.dtype == torch.int32 and pos.is_contiguous() and pos.device == like.device,
-          "pos must be contiguous int32 [tokens][k] on the rows' device")
-    if w is not None:
-        _rows2d("w", w, dtypes=(torch.float32,))
-        _need(w.shape == pos.shape and w.device == like.device, "w must be f32 [tokens][k] on the rows' device")
+    out = _native().dispatch(idx, experts, x, s, _of(_LAYOUT, scale_layout, "scale_layout"), _handle(stream, x))
+    return _on_stream(stream, out)[:5]
 
 
 def combine(z, pos, w=None, base=None, stream=None):
     """base + sum_j w[:, j] * z[pos[:, j]] (w None: ones, the gradient of
     dispatch; base None: nothing added)."""
-    _rows2d("z", z, dtypes=_XTYPE)
-    _check_places(pos, w, z)
-    M, k = pos.shape
-    R, C = z.shape
-    out = _alloc(M, C, z.dtype, z.device)
-    if base is not None:
-        _rows2d("base", base, like=out)
-    B.fp8_combine(z, _XTYPE[z.dtype], R, M, k, C, _pitch(z), pos, w, 0 if w is None else _pitch(w),
-                  base, 0 if base is None else _pitch(base), out, C, stream)
-    _on_stream(stream, out)
-    return out
+    return _on_stream(stream, _native().combine(z, pos, w, base, _handle(stream, z)))[0]
 
 
 def combine_backward(dy, z, pos, w, stream=None):
     """Gradients of combine's z and w for the places of one dispatch (every
     row of z in one place)."""
-    _rows2d("z", z, dtypes=_XTYPE)
-    _rows2d("dy", dy, dtypes=_XTYPE)
-    _check_places(pos, w, z)
-    M, k = pos.shape
-    R, C = z.shape
-    _need(dy.shape == (M, C) and dy.dtype == z.dtype and dy.device == z.device,
-          "dy must be [tokens][columns] of z's type and device")
-    _need(R == M * k, "z must have tokens * k rows")
-    dz = _alloc(R, C, z.dtype, z.device)
-    dw = _alloc(M, k, torch.float32, z.device)
-    B.fp8_combine_backward(dy, _XTYPE[z.dtype], R, M, k, C, _pitch(dy), z, _pitch(z), pos, w,
-                           0 if w is None else _pitch(w), dz, C, dw, k, stream)
-    _on_stream(stream, dz, dw)
-    return dz, dw
+    return _on_stream(stream, _native().combine_backward(dy, z, pos, w, _handle(stream, z)))
