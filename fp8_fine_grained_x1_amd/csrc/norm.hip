@@ -70,7 +70,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs p) {
         for (int e = 0; e < 8; ++e) a[e] += b[e];
         raw[i] = encode8<XT>(a);
       }
-      if (p.h) store_raw8<XT, true>(p.h, row * p.ldh + v * 8, raw[i]);
+      if (p.h) store_raw8<XT, false>(p.h, row * p.ldh + v * 8, raw[i]);
       float f[8];
       decode8<XT>(raw[i], f);
 #pragma unroll
@@ -89,7 +89,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs p) {
       load_gamma8(p.gamma, p.g_type, (int64_t)v * 8, g);
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] = f[e] * rstd * g[e];
-      if (p.y) store_raw8<XT, true>(p.y, row * p.ldy + v * 8, encode8<XT>(f));
+      if (p.y) store_raw8<XT, false>(p.y, row * p.ldy + v * 8, encode8<XT>(f));
       if (p.q) {
         float m = 0.0f;
 #pragma unroll
@@ -130,7 +130,7 @@ __device__ __forceinline__ void load_grad_row(const NormGradArgs& p, int64_t row
   for (int i = 0; i < NV; ++i) {
     const int v = threadIdx.x + i * blockDim.x;
     if (v >= nvec) continue;
-    r.d[i] = load_raw8<XT, true>(p.dy, row * p.lddy + v * 8);
+    r.d[i] = load_raw8<XT, false>(p.dy, row * p.lddy + v * 8);
     r.h[i] = load_raw8<XT, true>(p.h, row * p.ldh + v * 8);
     if (p.dh) r.b[i] = load_raw8<XT, true>(p.dh, row * p.lddh + v * 8);
   }
@@ -188,7 +188,7 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(NormGradArgs p) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] += b[e];
       }
-      store_raw8<XT, true>(p.dx, row * p.lddx + v * 8, encode8<XT>(o));
+      store_raw8<XT, false>(p.dx, row * p.lddx + v * 8, encode8<XT>(o));
     }
     if (PREFETCH) r = next;
   }
