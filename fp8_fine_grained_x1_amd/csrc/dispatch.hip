@@ -50,10 +50,15 @@ struct Plan {
   int32_t* token;
 };
 
-__device__ __forceinline__ int bucket_of(const Plan& p, int i) {
-  const int t = i / p.k;
-  const int e = p.idx[p.ld_idx == p.k ? (int64_t)i : t * p.ld_idx + (i - t * p.k)];
+__device__ __forceinline__ int bucket_at(const Plan& p, int64_t at) {
+  const int e = p.idx[at];
   return (uint32_t)e < (uint32_t)p.experts ? e : p.experts;
+}
+
+__device__ __forceinline__ int bucket_of(const Plan& p, int i) {
+  if (p.ld_idx == p.k) return bucket_at(p, i);
+  const int t = i / p.k;
+  return bucket_at(p, t * p.ld_idx + (i - t * p.k));
 }
 
 // counts[e][chunk]: a bucket's counts lie side by side for place_kernel.
@@ -200,9 +205,14 @@ struct Move {
 // an ordinary one, since the quantizer that wrote the row has just left it in
 // the caches; the writes are non-temporal (ordinary ones measured 12% more
 // time over 8192 x 8 rows of 7168 bytes).
-__device__ __forceinline__ void move_row(const Move& p, int64_t t, const int32_t* pos) {
+__device__ __forceinline__ uint4 row_vec(const Move& p, int64_t t, int v) {
+  return *reinterpret_cast<const uint4*>(p.x + t * p.pitch + (int64_t)v * 16);
+}
+
+// `first`: this thread's first vector, loaded ahead.
+__device__ __forceinline__ void move_row(const Move& p, int64_t t, const int32_t* pos, uint4 first) {
   for (int v = threadIdx.x; v < p.vecs; v += blockDim.x) {
-    const uint4 w = *reinterpret_cast<const uint4*>(p.x + t * p.pitch + (int64_t)v * 16);
+    const uint4 w = v == (int)threadIdx.x ? first : row_vec(p, t, v);
     for (int j = 0; j < p.k; ++j) {
       const int32_t r = pos[j];
       const int64_t row = r >= 0 ? r : -2 - r;
@@ -240,7 +250,7 @@ __global__ __launch_bounds__(kMoveThreads) void move_kernel(Move p) {
   }
   const int64_t step = gridDim.x - p.scale_blocks;
   for (int64_t t = (int64_t)blockIdx.x - p.scale_blocks; t < p.tokens; t += step) {
-    move_row(p, t, p.pos + t * p.k);
+    move_row(p, t, p.pos + t * p.k, (int)threadIdx.x < p.vecs ? row_vec(p, t, threadIdx.x) : uint4{});
     if (p.scale_blocks == 0) move_scales_of(p, t, p.pos + t * p.k);
   }
 }
@@ -272,8 +282,9 @@ __global__ __launch_bounds__(512) void dispatch_small_kernel(Plan p, Move m) {
 #pragma unroll
   for (int j = 0; j < kSmallK; ++j) {
     before[j] = 0;
-    mine[j] = j < p.k ? bucket_of(p, t * p.k + j) : 0;
+    mine[j] = j < p.k ? bucket_at(p, t * p.ld_idx + j) : 0;
   }
+  const uint4 first = m.x && tid < m.vecs ? row_vec(m, t, tid) : uint4{};
   for (int i0 = wave * 64; i0 < p.entries; i0 += kPlanThreads) {
     const int i = i0 + lane;
     const int b = i < p.entries ? bucket_of(p, i) : kMaxBuckets;
@@ -289,14 +300,14 @@ __global__ __launch_bounds__(512) void dispatch_small_kernel(Plan p, Move m) {
     int32_t r = 0;
 #pragma unroll
     for (int w = 0; w < kPlanWaves; ++w) r += part[w][tid];
-    const bool here = bucket_of(p, t * p.k + tid) < p.experts;
+    const bool here = bucket_at(p, t * p.ld_idx + tid) < p.experts;
     place[tid] = here ? r : -2 - r;
     p.pos[t * p.k + tid] = place[tid];
     p.token[r] = here ? t : -1;
   }
   __syncthreads();
   if (!m.x) return;
-  move_row(m, t, place);
+  move_row(m, t, place, first);
   move_scales_of(m, t, place);
 }
 

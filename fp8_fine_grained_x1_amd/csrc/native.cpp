@@ -265,13 +265,12 @@ PyObject* dispatch(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor token = make1(M * k, at::kInt, x);
   const Tensor os = s ? make_scales(M * k, C / 128, truth(a[4]), x) : Tensor();
   const int64_t bytes = fp8_dispatch_workspace(M, k, E);
-  const Tensor ws = bytes > 0 ? make1(bytes, at::kByte, x) : Tensor();
+  const Tensor ws = make1(bytes + 16, at::kByte, x);  // (0 bytes: the call below says why)
   check(fp8_dispatch(ptr<int32_t>(idx), pitch(idx), M, k, E, ptr(x), type, C, pitch(x), ptr<float>(s), s ? s->stride(0) : 0,
                      s ? s->stride(1) : 0, ptr<int32_t>(offsets), ptr<int32_t>(pos), ptr<int32_t>(token), ptr(out), C,
-                     s ? ptr<float>(os) : nullptr, s ? os.stride(0) : 0, s ? os.stride(1) : 0, bytes > 0 ? ptr(ws) : nullptr,
-                     bytes, handle(a[5])),
+                     s ? ptr<float>(os) : nullptr, s ? os.stride(0) : 0, s ? os.stride(1) : 0, ptr(ws), bytes, handle(a[5])),
         "fp8_dispatch");
-  return give({&out, s ? &os : nullptr, &offsets, &pos, &token, bytes > 0 ? &ws : nullptr});
+  return give({&out, s ? &os : nullptr, &offsets, &pos, &token, &ws});
   END_HANDLE_TH_ERRORS
 }
 

@@ -26,42 +26,67 @@ namespace {
 
 constexpr int kMaxWaves = 16;
 
-// Sum over the workgroup's waves; every thread gets the result.  `part` has
-// kMaxWaves slots and is free again after the call's second barrier of the
-// next use: callers alternate between two of them.
+// Sum over the workgroup's waves (at most 16); every thread gets the result,
+// the waves' sums added by a row of 16 lanes.  `part` may be written again
+// after the next call's barrier: callers alternate between two of them.
 __device__ __forceinline__ float block_sum(float v, float* part) {
   v = wave_sum(v);
   const int waves = blockDim.x >> 6;
   if (waves == 1) return v;
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
   __syncthreads();
-  float t = part[0];
-  for (int i = 1; i < waves; ++i) t += part[i];
+  const int i = threadIdx.x & 15;
+  float t = i < waves ? part[i] : 0.0f;
+  t += dpp_mov<kDppQuadXor1>(t);
+  t += dpp_mov<kDppQuadXor2>(t);
+  t += dpp_mov<kDppRowHalfMirror>(t);
+  t += dpp_mov<kDppRowMirror>(t);
   return t;
 }
 
-__device__ __forceinline__ void load_gamma8(const void* __restrict__ g, int g_type, int64_t off, float v[8]) {
+// 8 elements of gamma, undecoded: loaded ahead of the row's reduction.
+struct RawGamma {
+  uint4 a, b;
+};
+
+__device__ __forceinline__ RawGamma load_gamma8(const void* __restrict__ g, int g_type, int v) {
+  RawGamma r = {};
+  if (g_type == 0) {
+    r.a = reinterpret_cast<const uint4*>(g)[v];
+  } else {
+    r.a = reinterpret_cast<const uint4*>(g)[2 * v];
+    r.b = reinterpret_cast<const uint4*>(g)[2 * v + 1];
+  }
+  return r;
+}
+
+__device__ __forceinline__ void decode_gamma8(const RawGamma& r, int g_type, float v[8]) {
   if (g_type == 0)
-    decode8<0>(load_raw8<0, false>(g, off), v);
+    decode8<0>(Raw8<0>{r.a}, v);
   else
-    decode8<1>(load_raw8<1, false>(g, off), v);
+    decode8<1>(Raw8<1>{r.a, r.b}, v);
 }
 
 // One row per workgroup iteration; thread t holds the 8-element vectors
 // t, t + blockDim, ..: 16 consecutive lanes hold one 1x128 tile.
-template <int XT, int NV>
+// AHEAD: gamma is loaded before the reduction too, which shortens the chain of
+// a call on few rows; on many it costs registers that the streams want
+// (8192 x 7168 bf16: 98 us instead of 93).
+template <int XT, int NV, bool AHEAD>
 __global__ __launch_bounds__(1024) void norm_kernel(NormArgs p) {
   __shared__ float part[2][kMaxWaves];
   const int nvec = (int)(p.cols >> 3);
   int flip = 0;
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, flip ^= 1) {
     Raw8<XT> raw[NV];
+    RawGamma gamma[NV];
     float ss = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
       if (v >= nvec) continue;
       raw[i] = load_raw8<XT, true>(p.x, row * p.ldx + v * 8);
+      if (AHEAD) gamma[i] = load_gamma8(p.gamma, p.g_type, v);
       if (p.r) {
         float a[8], b[8];
         decode8<XT>(raw[i], a);
@@ -86,7 +111,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs p) {
       if (v >= nvec) continue;
       float f[8], g[8];
       decode8<XT>(raw[i], f);
-      load_gamma8(p.gamma, p.g_type, (int64_t)v * 8, g);
+      decode_gamma8(AHEAD ? gamma[i] : load_gamma8(p.gamma, p.g_type, v), p.g_type, g);
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] = f[e] * rstd * g[e];
       if (p.y) store_raw8<XT, false>(p.y, row * p.ldy + v * 8, encode8<XT>(f));
@@ -147,7 +172,7 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(NormGradArgs p) {
     const int v = threadIdx.x + i * blockDim.x;
 #pragma unroll
     for (int e = 0; e < 8; ++e) g[i][e] = acc[i][e] = 0.0f;
-    if (v < nvec) load_gamma8(p.gamma, p.g_type, (int64_t)v * 8, g[i]);
+    if (v < nvec) decode_gamma8(load_gamma8(p.gamma, p.g_type, v), p.g_type, g[i]);
   }
   int flip = 0;
   GradRow<XT, NV> r;
@@ -237,34 +262,39 @@ __global__ __launch_bounds__(kSumThreads) void norm_grad_sum_kernel(const float*
 }
 
 constexpr int64_t kMaxRowBlocks = 1 << 20;
+constexpr int64_t kFewRows = 256;  // a workgroup per CU
 
 // Vectors per thread and threads per workgroup for rows of `nvec` vectors:
 // at most 512 threads, whose register budget holds a row of up to 2048
-// vectors, and 1024 beyond.
+// vectors, and 1024 beyond.  `few` rows leave most of the chip idle: one
+// vector per thread then, for the shorter chain.
 struct RowShape {
   int nv, threads;
 };
-RowShape row_shape(int64_t nvec) {
-  const int nv = nvec <= 512 ? 1 : nvec <= 1024 ? 2 : 4;
+RowShape row_shape(int64_t nvec, bool few) {
+  const int nv = nvec <= (few ? 1024 : 512) ? 1 : nvec <= 1024 ? 2 : 4;
   const int64_t t = (nvec + nv - 1) / nv;
   return {nv, (int)((t + 63) / 64 * 64)};
 }
 
 template <int XT>
 hipError_t norm_t(const NormArgs& a, hipStream_t st) {
-  const RowShape sh = row_shape(a.cols / 8);
+  const RowShape sh = row_shape(a.cols / 8, a.rows <= kFewRows);
   const dim3 grid((unsigned)(a.rows < kMaxRowBlocks ? a.rows : kMaxRowBlocks)), block(sh.threads);
-  switch (sh.nv) {
-    case 1: hipLaunchKernelGGL((norm_kernel<XT, 1>), grid, block, 0, st, a); break;
-    case 2: hipLaunchKernelGGL((norm_kernel<XT, 2>), grid, block, 0, st, a); break;
-    default: hipLaunchKernelGGL((norm_kernel<XT, 4>), grid, block, 0, st, a); break;
-  }
+  if (sh.nv == 1 && a.rows <= kFewRows)
+    hipLaunchKernelGGL((norm_kernel<XT, 1, true>), grid, block, 0, st, a);
+  else if (sh.nv == 1)
+    hipLaunchKernelGGL((norm_kernel<XT, 1, false>), grid, block, 0, st, a);
+  else if (sh.nv == 2)
+    hipLaunchKernelGGL((norm_kernel<XT, 2, false>), grid, block, 0, st, a);
+  else
+    hipLaunchKernelGGL((norm_kernel<XT, 4, false>), grid, block, 0, st, a);
   return hipGetLastError();
 }
 
 template <int XT>
 hipError_t norm_grad_t(const NormGradArgs& a, hipStream_t st) {
-  const RowShape sh = row_shape(a.cols / 8);
+  const RowShape sh = row_shape(a.cols / 8, false);
   const dim3 grid((unsigned)norm_grad_strips(a.rows, a.cols)), block(sh.threads);
   if (sh.nv == 1)
     hipLaunchKernelGGL((norm_grad_kernel<XT, 1, 512, true>), grid, block, 0, st, a);
