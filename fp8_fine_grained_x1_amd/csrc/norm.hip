@@ -266,23 +266,26 @@ constexpr int64_t kFewRows = 256;  // a workgroup per CU
 
 // Vectors per thread and threads per workgroup for rows of `nvec` vectors:
 // at most 512 threads, whose register budget holds a row of up to 2048
-// vectors, and 1024 beyond.  `few` rows leave most of the chip idle: one
-// vector per thread then, for the shorter chain.
+// vectors, and 1024 beyond.  The columns alone decide, and with them the
+// order of a row's additions: its results do not depend on the other rows.
 struct RowShape {
   int nv, threads;
 };
-RowShape row_shape(int64_t nvec, bool few) {
-  const int nv = nvec <= (few ? 1024 : 512) ? 1 : nvec <= 1024 ? 2 : 4;
+RowShape row_shape(int64_t nvec) {
+  const int nv = nvec <= 512 ? 1 : nvec <= 1024 ? 2 : 4;
   const int64_t t = (nvec + nv - 1) / nv;
   return {nv, (int)((t + 63) / 64 * 64)};
 }
 
 template <int XT>
 hipError_t norm_t(const NormArgs& a, hipStream_t st) {
-  const RowShape sh = row_shape(a.cols / 8, a.rows <= kFewRows);
+  const RowShape sh = row_shape(a.cols / 8);
   const dim3 grid((unsigned)(a.rows < kMaxRowBlocks ? a.rows : kMaxRowBlocks)), block(sh.threads);
-  if (sh.nv == 1 && a.rows <= kFewRows)
+  const bool ahead = a.rows <= kFewRows;
+  if (sh.nv == 1 && ahead)
     hipLaunchKernelGGL((norm_kernel<XT, 1, true>), grid, block, 0, st, a);
+  else if (sh.nv == 2 && ahead)
+    hipLaunchKernelGGL((norm_kernel<XT, 2, true>), grid, block, 0, st, a);
   else if (sh.nv == 1)
     hipLaunchKernelGGL((norm_kernel<XT, 1, false>), grid, block, 0, st, a);
   else if (sh.nv == 2)
@@ -294,7 +297,7 @@ hipError_t norm_t(const NormArgs& a, hipStream_t st) {
 
 template <int XT>
 hipError_t norm_grad_t(const NormGradArgs& a, hipStream_t st) {
-  const RowShape sh = row_shape(a.cols / 8, false);
+  const RowShape sh = row_shape(a.cols / 8);
   const dim3 grid((unsigned)norm_grad_strips(a.rows, a.cols)), block(sh.threads);
   if (sh.nv == 1)
     hipLaunchKernelGGL((norm_grad_kernel<XT, 1, 512, true>), grid, block, 0, st, a);

@@ -272,6 +272,7 @@ FP8FG_API int fp8_grouped_gemm_blockscaled(int64_t G, const int32_t* offsets,
  *            so may y (the norm rounded to x_type), q with s (no quantized
  *            output) and rstd.
  *   gamma    : [cols], g_type BF16 or F32.  eps >= 0, finite.
+ *   A row's results do not depend on the other rows or their number.
  *   Requires cols % 128 == 0.  rows == 0 or cols == 0 is a valid no-op.
  *   Alignment: x, r, h, y, gamma, q 16-byte aligned, their pitches multiples
  *   of 16 bytes; s and rstd 4-byte aligned.
