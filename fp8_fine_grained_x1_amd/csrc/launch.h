@@ -86,6 +86,10 @@ struct ColumnPlan {
 };
 ColumnPlan plan_columns(int64_t tiles_m, int64_t N, int cus);
 
+// Inputs of more bytes than this are read past the caches: less of them is
+// likely to lie in the 256 MB Infinity Cache, where their producer left them.
+constexpr int64_t kStreamBytes = (int64_t)128 << 20;
+
 // ------------------------------------------------- norm (norm.hip)
 struct NormArgs {
   const void* x;

@@ -75,11 +75,17 @@ __device__ __forceinline__ void decode_gamma8(const RawGamma& r, int g_type, flo
 
 // One row per workgroup iteration; thread t holds the 8-element vectors
 // t, t + blockDim, ..: 16 consecutive lanes hold one 1x128 tile.
-// AHEAD: gamma is loaded before the reduction too, which shortens the chain of
+// kFew: gamma is loaded before the reduction too, which shortens the chain of
 // a call on few rows; on many it costs registers that the streams want
-// (8192 x 7168 bf16: 98 us instead of 93).
-template <int XT, int NV, bool AHEAD, bool WITH_Y>
+// (8192 x 7168 bf16: 98 us instead of 93).  kStream: x and r pass the caches
+// by, which on inputs that fit in them costs (1111 x 5120 f32: 9.1 us, 8.6
+// with ordinary reads) and on larger ones gains (8192 x 7168 bf16 with r: 91.5
+// us, 98.7).
+enum NormMode { kFew, kMid, kStream };
+
+template <int XT, int NV, NormMode MODE, bool WITH_Y>
 __global__ __launch_bounds__(1024) void norm_kernel(NormArgs p) {
+  constexpr bool AHEAD = MODE == kFew, NT = MODE == kStream;
   __shared__ float part[2][kMaxWaves];
   const int nvec = (int)(p.cols >> 3);
   int flip = 0;
@@ -91,17 +97,17 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs p) {
     for (int i = 0; i < NV; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
       if (v >= nvec) continue;
-      raw[i] = load_raw8<XT, true>(p.x, row * p.ldx + v * 8);
+      raw[i] = load_raw8<XT, NT>(p.x, row * p.ldx + v * 8);
       if (AHEAD) gamma[i] = load_gamma8(p.gamma, p.g_type, v);
       if (p.r) {
         float a[8], b[8];
         decode8<XT>(raw[i], a);
-        load8<XT>(p.r, row * p.ldr + v * 8, b);
+        decode8<XT>(load_raw8<XT, NT>(p.r, row * p.ldr + v * 8), b);
 #pragma unroll
         for (int e = 0; e < 8; ++e) a[e] += b[e];
         raw[i] = encode8<XT>(a);
       }
-      if (p.h) store_raw8<XT, WITH_Y>(p.h, row * p.ldh + v * 8, raw[i]);
+      if (p.h) store_raw8<XT, WITH_Y && NT>(p.h, row * p.ldh + v * 8, raw[i]);
       float f[8];
       decode8<XT>(raw[i], f);
 #pragma unroll
@@ -154,20 +160,20 @@ struct GradRow {
   float rstd;
 };
 
-template <int XT, int NV>
+template <int XT, int NV, bool NT>
 __device__ __forceinline__ void load_grad_row(const NormGradArgs& p, int64_t row, int nvec, GradRow<XT, NV>& r) {
   r.rstd = p.rstd[row];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int v = threadIdx.x + i * blockDim.x;
     if (v >= nvec) continue;
-    r.d[i] = load_raw8<XT, true>(p.dy, row * p.lddy + v * 8);
-    r.h[i] = load_raw8<XT, true>(p.h, row * p.ldh + v * 8);
-    if (p.dh) r.b[i] = load_raw8<XT, true>(p.dh, row * p.lddh + v * 8);
+    r.d[i] = load_raw8<XT, NT>(p.dy, row * p.lddy + v * 8);
+    r.h[i] = load_raw8<XT, NT>(p.h, row * p.ldh + v * 8);
+    if (p.dh) r.b[i] = load_raw8<XT, NT>(p.dh, row * p.lddh + v * 8);
   }
 }
 
-template <int XT, int NV, int THREADS, bool PREFETCH>
+template <int XT, int NV, int THREADS, bool PREFETCH, bool NT>
 __global__ __launch_bounds__(THREADS) void norm_grad_kernel(NormGradArgs p) {
   __shared__ float part[2][kMaxWaves];
   const int nvec = (int)(p.cols >> 3);
@@ -183,9 +189,9 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(NormGradArgs p) {
   int flip = 0;
   GradRow<XT, NV> r;
   int64_t row = blockIdx.x;
-  if (PREFETCH && row < p.rows) load_grad_row(p, row, nvec, r);
+  if (PREFETCH && row < p.rows) load_grad_row<XT, NV, NT>(p, row, nvec, r);
   for (; row < p.rows; row += gridDim.x, flip ^= 1) {
-    if (!PREFETCH) load_grad_row(p, row, nvec, r);
+    if (!PREFETCH) load_grad_row<XT, NV, NT>(p, row, nvec, r);
     float c = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -202,7 +208,7 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(NormGradArgs p) {
       }
     }
     GradRow<XT, NV> next;
-    if (PREFETCH && row + gridDim.x < p.rows) load_grad_row(p, row + gridDim.x, nvec, next);
+    if (PREFETCH && row + gridDim.x < p.rows) load_grad_row<XT, NV, NT>(p, row + gridDim.x, nvec, next);
     c = block_sum(c, part[flip]) * inv_cols * r.rstd;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -287,17 +293,27 @@ template <int XT, bool WITH_Y>
 hipError_t norm_as(const NormArgs& a, hipStream_t st) {
   const RowShape sh = row_shape(a.cols / 8);
   const dim3 grid((unsigned)(a.rows < kMaxRowBlocks ? a.rows : kMaxRowBlocks)), block(sh.threads);
-  const bool ahead = a.rows <= kFewRows;
-  if (sh.nv == 1 && ahead)
-    hipLaunchKernelGGL((norm_kernel<XT, 1, true, WITH_Y>), grid, block, 0, st, a);
-  else if (sh.nv == 2 && ahead)
-    hipLaunchKernelGGL((norm_kernel<XT, 2, true, WITH_Y>), grid, block, 0, st, a);
-  else if (sh.nv == 1)
-    hipLaunchKernelGGL((norm_kernel<XT, 1, false, WITH_Y>), grid, block, 0, st, a);
-  else if (sh.nv == 2)
-    hipLaunchKernelGGL((norm_kernel<XT, 2, false, WITH_Y>), grid, block, 0, st, a);
-  else
-    hipLaunchKernelGGL((norm_kernel<XT, 4, false, WITH_Y>), grid, block, 0, st, a);
+  const int64_t bytes = a.rows * a.cols * (XT == 0 ? 2 : 4) * (a.r ? 2 : 1);
+  if (a.rows <= kFewRows && sh.nv <= 2) {
+    if (sh.nv == 1)
+      hipLaunchKernelGGL((norm_kernel<XT, 1, kFew, WITH_Y>), grid, block, 0, st, a);
+    else
+      hipLaunchKernelGGL((norm_kernel<XT, 2, kFew, WITH_Y>), grid, block, 0, st, a);
+  } else if (bytes <= kStreamBytes) {
+    if (sh.nv == 1)
+      hipLaunchKernelGGL((norm_kernel<XT, 1, kMid, WITH_Y>), grid, block, 0, st, a);
+    else if (sh.nv == 2)
+      hipLaunchKernelGGL((norm_kernel<XT, 2, kMid, WITH_Y>), grid, block, 0, st, a);
+    else
+      hipLaunchKernelGGL((norm_kernel<XT, 4, kMid, WITH_Y>), grid, block, 0, st, a);
+  } else {
+    if (sh.nv == 1)
+      hipLaunchKernelGGL((norm_kernel<XT, 1, kStream, WITH_Y>), grid, block, 0, st, a);
+    else if (sh.nv == 2)
+      hipLaunchKernelGGL((norm_kernel<XT, 2, kStream, WITH_Y>), grid, block, 0, st, a);
+    else
+      hipLaunchKernelGGL((norm_kernel<XT, 4, kStream, WITH_Y>), grid, block, 0, st, a);
+  }
   return hipGetLastError();
 }
 
@@ -306,19 +322,25 @@ hipError_t norm_t(const NormArgs& a, hipStream_t st) {
   return a.y ? norm_as<XT, true>(a, st) : norm_as<XT, false>(a, st);
 }
 
-template <int XT>
-hipError_t norm_grad_t(const NormGradArgs& a, hipStream_t st) {
+template <int XT, bool NT>
+hipError_t norm_grad_as(const NormGradArgs& a, hipStream_t st) {
   const RowShape sh = row_shape(a.cols / 8);
   const dim3 grid((unsigned)norm_grad_strips(a.rows, a.cols)), block(sh.threads);
   if (sh.nv == 1)
-    hipLaunchKernelGGL((norm_grad_kernel<XT, 1, 512, true>), grid, block, 0, st, a);
+    hipLaunchKernelGGL((norm_grad_kernel<XT, 1, 512, true, NT>), grid, block, 0, st, a);
   else if (sh.nv == 2)
-    hipLaunchKernelGGL((norm_grad_kernel<XT, 2, 512, true>), grid, block, 0, st, a);
+    hipLaunchKernelGGL((norm_grad_kernel<XT, 2, 512, true, NT>), grid, block, 0, st, a);
   else if (sh.threads <= 512)
-    hipLaunchKernelGGL((norm_grad_kernel<XT, 4, 512, false>), grid, block, 0, st, a);
+    hipLaunchKernelGGL((norm_grad_kernel<XT, 4, 512, false, NT>), grid, block, 0, st, a);
   else
-    hipLaunchKernelGGL((norm_grad_kernel<XT, 4, 1024, false>), grid, block, 0, st, a);
+    hipLaunchKernelGGL((norm_grad_kernel<XT, 4, 1024, false, NT>), grid, block, 0, st, a);
   return hipGetLastError();
+}
+
+template <int XT>
+hipError_t norm_grad_t(const NormGradArgs& a, hipStream_t st) {
+  const int64_t bytes = a.rows * a.cols * (XT == 0 ? 2 : 4) * (a.dh ? 3 : 2);
+  return bytes > kStreamBytes ? norm_grad_as<XT, true>(a, st) : norm_grad_as<XT, false>(a, st);
 }
 
 }  // namespace
