@@ -266,16 +266,43 @@ __device__ __forceinline__ void wave_fence() {
   __builtin_amdgcn_wave_barrier();
 }
 
-// Sum over the 64 lanes of a wave; every lane gets the result.  The order of
-// additions is fixed.
-__device__ __forceinline__ float wave_sum(float v) {
+// A value and its counterpart 16 or 32 lanes away, in either order (the swap
+// of a register with itself leaves the lower half's in one result and the
+// upper half's in the other).
+struct LanePair {
+  uint32_t a, b;
+};
+template <int STEP>
+__device__ __forceinline__ LanePair lane_pair(uint32_t v) {
+  static_assert(STEP == 16 || STEP == 32, "rows or halves");
+  if constexpr (STEP == 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return {r[0], r[1]};
+  } else {
+    const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return {r[0], r[1]};
+  }
+}
+template <int STEP>
+__device__ __forceinline__ float pair_sum(float v) {
+  const LanePair p = lane_pair<STEP>(__float_as_uint(v));
+  return __uint_as_float(p.a) + __uint_as_float(p.b);
+}
+template <int STEP>
+__device__ __forceinline__ float pair_max(float v) {
+  const LanePair p = lane_pair<STEP>(__float_as_uint(v));
+  return fmaxf(__uint_as_float(p.a), __uint_as_float(p.b));
+}
+
+// Sum over the 16 lanes of a DPP row, over 32 or over all 64 lanes of a
+// wave; every lane gets the result.  The order of additions is fixed.
+__device__ __forceinline__ float row16_sum(float v) {
   v += dpp_mov<kDppQuadXor1>(v);
   v += dpp_mov<kDppQuadXor2>(v);
   v += dpp_mov<kDppRowHalfMirror>(v);
   v += dpp_mov<kDppRowMirror>(v);
-  v += __shfl_xor(v, 16);
-  v += __shfl_xor(v, 32);
   return v;
 }
+__device__ __forceinline__ float wave_sum(float v) { return pair_sum<32>(pair_sum<16>(row16_sum(v))); }
 
 }  // namespace fp8fg

@@ -42,12 +42,7 @@ __device__ __forceinline__ float block_sum(float v, float* part) {
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
   __syncthreads();
   const int i = threadIdx.x & 15;
-  float t = i < waves ? part[i] : 0.0f;
-  t += dpp_mov<kDppQuadXor1>(t);
-  t += dpp_mov<kDppQuadXor2>(t);
-  t += dpp_mov<kDppRowHalfMirror>(t);
-  t += dpp_mov<kDppRowMirror>(t);
-  return t;
+  return row16_sum(i < waves ? part[i] : 0.0f);
 }
 
 // 8 elements of gamma, undecoded: loaded ahead of the row's reduction.

@@ -99,12 +99,6 @@ __device__ __forceinline__ uint64_t wave_max64(uint64_t v) {
   return v;
 }
 
-__device__ __forceinline__ double wave_sum64(double v) {
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
-  return v;
-}
-
 // A logit as it lies in memory, and its value (NaN: masked).
 template <int LT>
 struct RawLogitOf {
@@ -140,10 +134,21 @@ __device__ __forceinline__ double dpp_f64(double v) {
 
 template <int LANES>
 __device__ __forceinline__ float lanes_max_f32(float v) {
-  v = row16_max(v);
-  v = fmaxf(v, __shfl_xor(v, 16));
-  if constexpr (LANES == 64) v = fmaxf(v, __shfl_xor(v, 32));
-  return v;
+  v = pair_max<16>(row16_max(v));
+  return LANES == 64 ? pair_max<32>(v) : v;
+}
+
+template <int LANES>
+__device__ __forceinline__ float lanes_sum_f32(float v) {
+  v = pair_sum<16>(row16_sum(v));
+  return LANES == 64 ? pair_sum<32>(v) : v;
+}
+
+template <int STEP>
+__device__ __forceinline__ double pair_sum_f64(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const LanePair lo = lane_pair<STEP>((uint32_t)u), hi = lane_pair<STEP>((uint32_t)(u >> 32));
+  return __builtin_bit_cast(double, (uint64_t)hi.a << 32 | lo.a) + __builtin_bit_cast(double, (uint64_t)hi.b << 32 | lo.b);
 }
 
 template <int LANES>
@@ -152,20 +157,33 @@ __device__ __forceinline__ double lanes_sum_f64(double v) {
   v += dpp_f64<kDppQuadXor2>(v);
   v += dpp_f64<kDppRowHalfMirror>(v);
   v += dpp_f64<kDppRowMirror>(v);
-  v += __shfl_xor(v, 16);
-  if constexpr (LANES == 64) v += __shfl_xor(v, 32);
+  v = pair_sum_f64<16>(v);
+  return LANES == 64 ? pair_sum_f64<32>(v) : v;
+}
+
+// (`same`: log2 of the consecutive lanes that hold equal values already.)
+template <int LANES>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v, int same = 0) {
+  if (same < 1) v = max(v, dpp_u32<kDppQuadXor1>(v));
+  if (same < 2) v = max(v, dpp_u32<kDppQuadXor2>(v));
+  v = max(v, dpp_u32<kDppRowHalfMirror>(v));
+  v = max(v, dpp_u32<kDppRowMirror>(v));
+  LanePair p = lane_pair<16>(v);
+  v = max(p.a, p.b);
+  if constexpr (LANES == 64) {
+    p = lane_pair<32>(v);
+    v = max(p.a, p.b);
+  }
   return v;
 }
 
+// The first `n` lanes from the lowest set one on, of every token's part of a
+// lane mask (scalar arithmetic; n at most LANES / 2).
 template <int LANES>
-__device__ __forceinline__ float lanes_sum_f32(float v) {
-  v += dpp_mov<kDppQuadXor1>(v);
-  v += dpp_mov<kDppQuadXor2>(v);
-  v += dpp_mov<kDppRowHalfMirror>(v);
-  v += dpp_mov<kDppRowMirror>(v);
-  v += __shfl_xor(v, 16);
-  if constexpr (LANES == 64) v += __shfl_xor(v, 32);
-  return v;
+__device__ __forceinline__ uint64_t first_lanes(uint64_t m, int n) {
+  if constexpr (LANES == 64) return m ? ((1ull << n) - 1) << __builtin_ctzll(m) : 0;
+  const uint32_t lo = (uint32_t)m, hi = (uint32_t)(m >> 32), span = (1u << n) - 1;
+  return (uint64_t)((hi & (0u - hi)) * span) << 32 | (lo & (0u - lo)) * span;
 }
 
 __device__ __forceinline__ float key_value(uint32_t k) {
@@ -180,42 +198,12 @@ __device__ __forceinline__ double pack(uint32_t key, int place) {
   const uint64_t u = (uint64_t)key << 10 | (uint32_t)(1023 - place);
   return __builtin_bit_cast(double, u | 0x4000000000000000ull);
 }
-constexpr double kNoPack = 2.0;  // below every candidate
-__device__ __forceinline__ uint32_t pack_key(double v) {
-  return (uint32_t)(__builtin_bit_cast(uint64_t, v) >> 10);
-}
+constexpr double kNoPack = 2.0;  // below every candidate; its key is 0
 __device__ __forceinline__ int pack_place(double v) {
   return 1023 - (int)((uint32_t)__builtin_bit_cast(uint64_t, v) & 1023u);
 }
-
-// The lanes 16 or 32 apart exchanged, and the larger of both.
-template <int STEP>
-__device__ __forceinline__ double swap_max(double v) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = (uint32_t)u, hi = (uint32_t)(u >> 32);
-  if constexpr (STEP == 16) {
-    const auto a = __builtin_amdgcn_permlane16_swap(lo, lo, false, false);
-    const auto b = __builtin_amdgcn_permlane16_swap(hi, hi, false, false);
-    return __builtin_fmax(__builtin_bit_cast(double, (uint64_t)b[0] << 32 | a[0]),
-                          __builtin_bit_cast(double, (uint64_t)b[1] << 32 | a[1]));
-  } else {
-    const auto a = __builtin_amdgcn_permlane32_swap(lo, lo, false, false);
-    const auto b = __builtin_amdgcn_permlane32_swap(hi, hi, false, false);
-    return __builtin_fmax(__builtin_bit_cast(double, (uint64_t)b[0] << 32 | a[0]),
-                          __builtin_bit_cast(double, (uint64_t)b[1] << 32 | a[1]));
-  }
-}
-
-// (`same`: log2 of the consecutive lanes that hold equal values already.)
-template <int LANES>
-__device__ __forceinline__ double lanes_max_pack(double v, int same = 0) {
-  if (same < 1) v = __builtin_fmax(v, dpp_f64<kDppQuadXor1>(v));
-  if (same < 2) v = __builtin_fmax(v, dpp_f64<kDppQuadXor2>(v));
-  v = __builtin_fmax(v, dpp_f64<kDppRowHalfMirror>(v));
-  v = __builtin_fmax(v, dpp_f64<kDppRowMirror>(v));
-  v = swap_max<16>(v);
-  if constexpr (LANES == 64) v = swap_max<32>(v);
-  return v;
+__device__ __forceinline__ uint32_t pack_key(double v) {
+  return (uint32_t)(__builtin_bit_cast(uint64_t, v) >> 10);
 }
 
 // The two largest of two disjoint sets' two largest (a >= b).
@@ -261,7 +249,15 @@ __device__ __forceinline__ void load_slots(const T* __restrict__ row, int e0, in
 
 // LANES lanes per token, NS >= slots experts per lane in registers, as NS / 4
 // descending lists of 4: an expert that is taken only moves up the list that
-// it heads.
+// it heads.  A step of the selection is a maximum over the lists' heads and
+// the lanes (32-bit keys, by DPP and row swaps), a ballot, and scalar
+// arithmetic for the lowest lane that has it.
+//
+// Bound by instruction issue: about 900 vector instructions a wave, 430 of
+// them the scores.  16384 x 256, 8 of 256 in 4 of 8 groups, f32: 13.3 us with
+// two tokens to a wave (the logits' bytes at a device copy's rate: 3.5); 25.7
+// with one (850 instructions for it alone), 22 with four (16 experts to a
+// lane: too few waves to hide the loads).  5 x 256: 3.8 us.
 template <int LT, int LANES, int NS, int SCORE>
 __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p, RouteLayout q) {
   constexpr int kTokens = 64 / LANES;  // of a wave
@@ -274,6 +270,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p, Ro
   const int n = group < q.groups ? min(q.slots, q.size - in_group) : 0;  // this lane's experts (<= 0: none)
   const ExpCoef coef = exp_coef();
   __shared__ float scores[kRouteWaves][64 * NS];
+  __shared__ int picks[kRouteWaves][64];
   float* mine = scores[wave] + (lane / LANES) * LANES * NS;
   float bias[NS];
   if (p.bias) load_slots<float, NS>(p.bias, e0, E, q.vec, bias);
@@ -332,44 +329,47 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p, Ro
       if constexpr (LANES == 64) {
         if (q.lanes > 4) merge_top2(a, b, __shfl_xor(a, 16), __shfl_xor(b, 16));
       }
-      double g = kNoPack;
-      if (a != kNoPack)
-        g = pack(p.group_top > 1 && b != kNoPack ? order_key(key_value(pack_key(a)) + key_value(pack_key(b))) : pack_key(a),
-                 group);
-      bool keep = false;
+      // (0: no candidate; where nothing else is left, such groups are kept)
+      uint32_t g = p.group_top > 1 && b != kNoPack ? order_key(key_value(pack_key(a)) + key_value(pack_key(b))) : pack_key(a);
+      uint64_t keep = 0;
       for (int r = 0; r < p.top_groups; ++r) {
-        const double best = lanes_max_pack<LANES>(g, q.lanes);
-        if (g == best) {  // (where nothing is left, kept lanes without candidates)
-          keep = true;
-          g = kNoPack;
-        }
+        const uint32_t best = lanes_max<LANES>(g, q.lanes);
+        const uint64_t won = first_lanes<LANES>(__builtin_amdgcn_ballot_w64(g == best), 1 << q.lanes);
+        keep |= won;
+        g = __builtin_amdgcn_inverse_ballot_w64(won) ? 0u : g;
       }
-      if (!keep) {
+      if (!__builtin_amdgcn_inverse_ballot_w64(keep)) {
 #pragma unroll
         for (int i = 0; i < NL; ++i) c[i][0] = c[i][1] = c[i][2] = c[i][3] = kNoPack;
         asm volatile("" : "+v"(c[0][0]));
       }
     }
 
-    int at = -1;  // lane j of the token: the place of its j-th expert
+    picks[wave][lane] = -1;
+    wave_fence();
     for (int j = 0; j < p.k; ++j) {
-      double head = c[0][0];
+      uint32_t head = pack_key(c[0][0]);
 #pragma unroll
-      for (int i = 1; i < NL; ++i) head = __builtin_fmax(head, c[i][0]);
-      const double best = lanes_max_pack<LANES>(head);
+      for (int i = 1; i < NL; ++i) head = max(head, pack_key(c[i][0]));
+      const uint32_t best = lanes_max<LANES>(head);
+      // the lowest lane that has it, and there the first list (lower places)
+      bool mine_now = __builtin_amdgcn_inverse_ballot_w64(first_lanes<LANES>(__builtin_amdgcn_ballot_w64(head == best), 1));
+      mine_now = mine_now && best != 0;
 #pragma unroll
       for (int i = 0; i < NL; ++i) {
-        if (c[i][0] == best) {  // (an empty list stays empty)
+        if (mine_now && pack_key(c[i][0]) == best) {
+          picks[wave][(lane & ~(LANES - 1)) + j] = pack_place(c[i][0]);
           c[i][0] = c[i][1];
           c[i][1] = c[i][2];
           c[i][2] = c[i][3];
           c[i][3] = kNoPack;
+          mine_now = false;
           asm volatile("" : "+v"(c[i][0]));  // moves under the lanes' mask, no selects
         }
       }
-      if (sub == j && best != kNoPack) at = pack_place(best);
     }
     wave_fence();
+    int at = sub < p.k ? picks[wave][lane] : -1;  // lane j of the token: the place of its j-th expert
     float s = 0.0f;
     if (at >= 0) {
       s = mine[at];
@@ -413,7 +413,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_any_kernel(RouteArgs p
         ex[i] = softmax_term(l[i], top, coef);
         sum += lane + 64 * i < E ? ex[i] : 0.0;
       }
-      const double inv = 1.0 / wave_sum64(sum);
+      const double inv = 1.0 / lanes_sum_f64<64>(sum);
 #pragma unroll
       for (int i = 0; i < NE; ++i) s[i] = (float)(ex[i] * inv);
     } else {
@@ -504,14 +504,28 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_any_kernel(RouteArgs p
   }
 }
 
+// exp(x) for x <= 0 by the hardware's 2^t, t = x log2(e) with the product's
+// rounding error and the constant's made good to first order: within 2 ulp
+// down to 2^-126, 0 below.
+__device__ __forceinline__ float exp_neg(float x) {
+  x = fmaxf(x, -120.0f);
+  const float t = x * 1.44269502f;                                    // RN32(log2 e)
+  const float e = __builtin_fmaf(x, 1.44269502f, -t) + x * 1.92596299e-8f;  // log2 e - RN32(log2 e)
+  const float p = __builtin_amdgcn_exp2f(t);
+  return __builtin_fmaf(p, e * 0.693147181f, p);
+}
+
 // exp(l - top), 0 for a masked logit, 1 at the top (also where both are
 // +inf).
 __device__ __forceinline__ float exp_below(float l, float top) {
-  return l == -INFINITY ? 0.0f : l == top ? 1.0f : expf(l - top);
+  const float e = exp_neg(l == top ? 0.0f : l - top);
+  return l == -INFINITY ? 0.0f : e;
 }
 
 // One wave per token: lane j < k has the j-th chosen expert, and lane i the
-// logits (where the gradient is dense) and gradients i, i + 64, ..
+// logits (where the gradient is dense) and gradients i, i + 64, ..  Only the
+// dense form reads a whole row.  Bound by instruction issue: 8191 x 160 bf16,
+// dense: 6.0 us (its bytes at a device copy's rate: 1.1).
 template <int LT, int NE>
 __global__ __launch_bounds__(64 * kRouteWaves) void route_grad_kernel(RouteGradArgs p) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -561,14 +575,15 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_grad_kernel(RouteGradA
       dot = wave_sum(v * s);
       if (!dense) v = s * (v - dot);
     } else {
-      const float s = l == -INFINITY ? 0.0f : 1.0f / (1.0f + expf(-l));
+      const float e1 = expf(-fabsf(l));  // (a masked logit: 0; denormals count, shares are quotients)
+      const float s = (l >= 0.0f ? 1.0f : e1) / (1.0f + e1);
       float share = s;  // s_j / S when renormalised
       if (p.renorm) {
         total = wave_sum(s);
         share = total > 0.0f ? s / total : 0.0f;
         v -= wave_sum(v * share);
       }
-      v = v * share * (1.0f - s);
+      v = v * share * ((l >= 0.0f ? e1 : 1.0f) / (1.0f + e1));  // 1 - s without cancellation
     }
     float d[NE];
 #pragma unroll
@@ -625,9 +640,9 @@ hipError_t route_as(const RouteArgs& a, const RouteLayout& q, hipStream_t st) {
   return hipGetLastError();
 }
 
-// From this many tokens on, two to a wave: fewer instructions per token, but
-// a longer chain of them.
-constexpr int64_t kRouteManyRows = 4096;
+// From this many tokens on, two to a wave: fewer instructions per token.
+// (Below, a wave per token leaves no SIMD with more than two.)
+constexpr int64_t kRouteManyRows = 2048;
 
 template <int LT>
 hipError_t route_t(const RouteArgs& a, hipStream_t st) {
