@@ -432,7 +432,7 @@ __global__ __launch_bounds__(512) void combine_grad_kernel(CombineGradArgs p) {
 }
 
 constexpr int64_t kMaxTokenBlocks = 1 << 20;
-constexpr int64_t kMaxCombineBlocks = 1 << 24;
+constexpr int64_t kMaxCombineBlocks = 1 << 22;  // (x 256 threads: below 2^32 work-items)
 
 unsigned token_blocks(int64_t tokens) { return (unsigned)(tokens < kMaxTokenBlocks ? tokens : kMaxTokenBlocks); }
 

@@ -147,15 +147,16 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs p) {
 
 // A workgroup takes the rows blockIdx.x, blockIdx.x + gridDim.x, ..; its
 // threads keep their columns' part of dgamma in registers and write it once.
-// The next row is loaded before the reduction of this one (PREFETCH: where
-// the registers hold both).
+// The next row is loaded before the reduction of this one where the registers
+// hold both (PREFETCH); the widest rows (1024 threads) leave gamma and dh in
+// memory until their use, too.
 template <int XT, int NV>
 struct GradRow {
   Raw8<XT> d[NV], h[NV], b[NV];
   float rstd;
 };
 
-template <int XT, int NV, bool NT>
+template <int XT, int NV, bool NT, bool WITH_B>
 __device__ __forceinline__ void load_grad_row(const NormGradArgs& p, int64_t row, int nvec, GradRow<XT, NV>& r) {
   r.rstd = p.rstd[row];
 #pragma unroll
@@ -164,12 +165,13 @@ __device__ __forceinline__ void load_grad_row(const NormGradArgs& p, int64_t row
     if (v >= nvec) continue;
     r.d[i] = load_raw8<XT, NT>(p.dy, row * p.lddy + v * 8);
     r.h[i] = load_raw8<XT, NT>(p.h, row * p.ldh + v * 8);
-    if (p.dh) r.b[i] = load_raw8<XT, NT>(p.dh, row * p.lddh + v * 8);
+    if (WITH_B && p.dh) r.b[i] = load_raw8<XT, NT>(p.dh, row * p.lddh + v * 8);
   }
 }
 
 template <int XT, int NV, int THREADS, bool PREFETCH, bool NT>
 __global__ __launch_bounds__(THREADS) void norm_grad_kernel(NormGradArgs p) {
+  constexpr bool kKeepGamma = THREADS <= 512;
   __shared__ float part[2][kMaxWaves];
   const int nvec = (int)(p.cols >> 3);
   const float inv_cols = 1.0f / (float)p.cols;
@@ -179,14 +181,14 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(NormGradArgs p) {
     const int v = threadIdx.x + i * blockDim.x;
 #pragma unroll
     for (int e = 0; e < 8; ++e) g[i][e] = acc[i][e] = 0.0f;
-    if (v < nvec) decode_gamma8(load_gamma8(p.gamma, p.g_type, v), p.g_type, g[i]);
+    if (kKeepGamma && v < nvec) decode_gamma8(load_gamma8(p.gamma, p.g_type, v), p.g_type, g[i]);
   }
   int flip = 0;
   GradRow<XT, NV> r;
   int64_t row = blockIdx.x;
-  if (PREFETCH && row < p.rows) load_grad_row<XT, NV, NT>(p, row, nvec, r);
+  if (PREFETCH && row < p.rows) load_grad_row<XT, NV, NT, PREFETCH>(p, row, nvec, r);
   for (; row < p.rows; row += gridDim.x, flip ^= 1) {
-    if (!PREFETCH) load_grad_row<XT, NV, NT>(p, row, nvec, r);
+    if (!PREFETCH) load_grad_row<XT, NV, NT, PREFETCH>(p, row, nvec, r);
     float c = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -195,6 +197,7 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(NormGradArgs p) {
       float d[8], h[8];
       decode8<XT>(r.d[i], d);
       decode8<XT>(r.h[i], h);
+      if (!kKeepGamma) decode_gamma8(load_gamma8(p.gamma, p.g_type, v), p.g_type, g[i]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float dx = d[e] * (h[e] * r.rstd);
@@ -203,7 +206,7 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(NormGradArgs p) {
       }
     }
     GradRow<XT, NV> next;
-    if (PREFETCH && row + gridDim.x < p.rows) load_grad_row<XT, NV, NT>(p, row + gridDim.x, nvec, next);
+    if (PREFETCH && row + gridDim.x < p.rows) load_grad_row<XT, NV, NT, PREFETCH>(p, row + gridDim.x, nvec, next);
     c = block_sum(c, part[flip]) * inv_cols * r.rstd;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -212,11 +215,12 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(NormGradArgs p) {
       float d[8], h[8], o[8];
       decode8<XT>(r.d[i], d);
       decode8<XT>(r.h[i], h);
+      if (!kKeepGamma) decode_gamma8(load_gamma8(p.gamma, p.g_type, v), p.g_type, g[i]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) o[e] = r.rstd * __builtin_fmaf(-h[e], c, d[e] * g[i][e]);
       if (p.dh) {
         float b[8];
-        decode8<XT>(r.b[i], b);
+        decode8<XT>(PREFETCH ? r.b[i] : load_raw8<XT, NT>(p.dh, row * p.lddh + v * 8), b);
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] += b[e];
       }
