@@ -473,12 +473,16 @@ hipError_t launch_dispatch(const DispatchArgs& a, hipStream_t st) {
     return hipGetLastError();
   }
   hipLaunchKernelGGL(count_kernel, dim3((unsigned)chunks), dim3(kPlanThreads), 0, st, p);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
   hipLaunchKernelGGL(place_kernel, dim3((unsigned)chunks), dim3(kPlanThreads), 0, st, p);
-  if (a.x) {
+  e = hipGetLastError();
+  if (e == hipSuccess && a.x) {
     if (m.tiles > 0 && a.os_rs == 1) m.scale_blocks = (int)token_blocks((entries + 63) / 64);
     hipLaunchKernelGGL(move_kernel, dim3(m.scale_blocks + token_blocks(a.tokens)), dim3(kMoveThreads), 0, st, m);
+    e = hipGetLastError();
   }
-  return hipGetLastError();
+  return e;
 }
 
 template <int XT>

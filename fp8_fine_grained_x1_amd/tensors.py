@@ -28,7 +28,7 @@ A mixture-of-experts layer around them:
 These check the shapes, types, devices and row layouts that the C interface
 cannot see and raise ValueError.  They allocate on the current stream; with
 ``stream`` they run on that one (the caller orders it after the producers of
-the inputs) and mark what they allocated as in use there.
+the inputs) and mark their tensors as in use there.
 """
 
 import torch
@@ -163,15 +163,15 @@ def _handle(stream, x):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _on_stream(stream, tensors):
-    """Tells torch's allocator that tensors of the current stream are in use
-    on `stream`; returns them."""
+def _on_stream(stream, out, *inputs):
+    """Tells torch's allocator that a call's tensors are in use on `stream`
+    (its inputs may be another stream's); returns its outputs."""
     if stream is not None:
-        for t in tensors:
+        for t in (*out, *inputs):
             if t is not None and t.is_cuda:
                 t.record_stream(stream if hasattr(stream, "cuda_stream") else
                                 torch.cuda.ExternalStream(int(stream), device=t.device))
-    return tensors
+    return out
 
 
 _LAYOUT = {"group_major": True, "row_major": False}
@@ -191,13 +191,14 @@ def rmsnorm_quantize(x, gamma, residual=None, eps=1e-6, pow2=False, scale_layout
     unless want_y."""
     out = _native().rmsnorm_quantize(x, gamma, residual, eps, _rule(pow2), _of(_LAYOUT, scale_layout, "scale_layout"),
                                      want_y, _handle(stream, x))
-    return _on_stream(stream, out)
+    return _on_stream(stream, out, x, gamma, residual)
 
 
 def rmsnorm_backward(dy, h, gamma, rstd, dh=None, stream=None):
     """Gradients of rmsnorm_quantize's y (through the quantizer as it is) and,
     with dh, of its h.  Returns (dx, dgamma); dx is residual's gradient too."""
-    return _on_stream(stream, _native().rmsnorm_backward(dy, h, gamma, rstd, dh, _handle(stream, h)))[:2]
+    out = _native().rmsnorm_backward(dy, h, gamma, rstd, dh, _handle(stream, h))
+    return _on_stream(stream, out, dy, h, gamma, rstd, dh)[:2]
 
 
 def route(logits, k, bias=None, score="softmax", groups=1, top_groups=1, group_top=2, renorm=True,
@@ -206,13 +207,13 @@ def route(logits, k, bias=None, score="softmax", groups=1, top_groups=1, group_t
     include/fp8fg.h for the choice, masks and ties."""
     out = _native().route(logits, k, bias, _of(_SCORE, score, "score"), groups, top_groups, group_top, renorm, scale,
                           _handle(stream, logits))
-    return _on_stream(stream, out)
+    return _on_stream(stream, out, logits, bias)
 
 
 def route_backward(dw, logits, idx, score="softmax", renorm=True, scale=1.0, stream=None):
     """Gradient of route's weights with respect to the logits."""
     out = _native().route_backward(dw, logits, idx, _of(_SCORE, score, "score"), renorm, scale, _handle(stream, logits))
-    return _on_stream(stream, out)[0]
+    return _on_stream(stream, out, dw, logits, idx)[0]
 
 
 def dispatch(idx, experts, x, s=None, scale_layout="group_major", stream=None):
@@ -221,16 +222,16 @@ def dispatch(idx, experts, x, s=None, scale_layout="group_major", stream=None):
     s' is None for bf16 / f32.  Entries of idx outside [0, experts) come last
     with zero rows."""
     out = _native().dispatch(idx, experts, x, s, _of(_LAYOUT, scale_layout, "scale_layout"), _handle(stream, x))
-    return _on_stream(stream, out)[:5]
+    return _on_stream(stream, out, idx, x, s)[:5]
 
 
 def combine(z, pos, w=None, base=None, stream=None):
     """base + sum_j w[:, j] * z[pos[:, j]] (w None: ones, the gradient of
     dispatch; base None: nothing added)."""
-    return _on_stream(stream, _native().combine(z, pos, w, base, _handle(stream, z)))[0]
+    return _on_stream(stream, _native().combine(z, pos, w, base, _handle(stream, z)), z, pos, w, base)[0]
 
 
 def combine_backward(dy, z, pos, w, stream=None):
     """Gradients of combine's z and w for the places of one dispatch (every
     row of z in one place)."""
-    return _on_stream(stream, _native().combine_backward(dy, z, pos, w, _handle(stream, z)))
+    return _on_stream(stream, _native().combine_backward(dy, z, pos, w, _handle(stream, z)), dy, z, pos, w)

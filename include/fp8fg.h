@@ -277,7 +277,9 @@ FP8FG_API int fp8_grouped_gemm_blockscaled(int64_t G, const int32_t* offsets,
  *   Alignment: x, r, h, y, gamma, q 16-byte aligned, their pitches multiples
  *   of 16 bytes; s and rstd 4-byte aligned.
  *   Limits (FP8FG_EUNSUPPORTED): cols <= 32768 (a row stays in one
- *   workgroup's registers).
+ *   workgroup's registers); here and below rows <= 2^31 - 1, row pitches and
+ *   s_rs <= 2^29 elements, s_ts <= 2^31 - 1 (64-bit offsets hold their
+ *   products).
  */
 FP8FG_API int fp8_rmsnorm_quantize(const void* x, int x_type, int64_t rows, int64_t cols,
                          int64_t ldx, const void* r, int64_t ldr, const void* gamma,
@@ -331,7 +333,8 @@ FP8FG_API int fp8_rmsnorm_backward(const void* dy, int x_type, int64_t rows, int
  *   slots are idx = -1, w = 0.
  *   Requires 1 <= k <= experts, groups dividing experts, 1 <= top_groups <=
  *   groups, scale finite.  No alignment beyond the element's.
- *   Limits (FP8FG_EUNSUPPORTED): experts <= 1024, k <= 64.
+ *   Limits (FP8FG_EUNSUPPORTED): experts <= 1024, k <= 64; rows and pitches as
+ *   above.
  */
 FP8FG_API int fp8_route(const void* logits, int l_type, int64_t rows, int64_t experts,
               int64_t ldl, const float* bias, int score, int64_t groups,
@@ -377,7 +380,7 @@ FP8FG_API int fp8_route_backward(const void* logits, int l_type, int64_t rows, i
  *   Alignment: x, out 16-byte aligned, pitches multiples of 16 bytes; idx,
  *   offsets, pos, token, xs, os 4-byte aligned.
  *   Limits (FP8FG_EUNSUPPORTED): tokens * k <= 2^31 - 3 (the rows are int32),
- *   experts <= 1024, cols <= 2^28.
+ *   experts <= 1024, cols <= 2^28; pitches and scale strides as above.
  */
 FP8FG_API int64_t fp8_dispatch_workspace(int64_t tokens, int64_t k, int64_t experts);
 FP8FG_API int fp8_dispatch(const int32_t* idx, int64_t ld_idx, int64_t tokens, int64_t k,
@@ -398,7 +401,8 @@ FP8FG_API int fp8_dispatch(const int32_t* idx, int64_t ld_idx, int64_t tokens, i
  *   pos    : int32 [tokens][k], contiguous.
  *   Requires k >= 1, cols % 8 == 0.  Alignment: z, base, out 16-byte aligned,
  *   pitches multiples of 16 bytes; pos and w 4-byte aligned.
- *   Limits (FP8FG_EUNSUPPORTED): z_rows, tokens, k <= 2^31 - 1, cols <= 2^28.
+ *   Limits (FP8FG_EUNSUPPORTED): z_rows, tokens, k <= 2^31 - 1, cols <= 2^28;
+ *   pitches as above.
  */
 FP8FG_API int fp8_combine(const void* z, int type, int64_t z_rows, int64_t tokens, int64_t k,
                 int64_t cols, int64_t ldz, const int32_t* pos, const float* w,
