@@ -70,17 +70,16 @@ __device__ __forceinline__ void decode_gamma8(const RawGamma& r, int g_type, flo
 
 // One row per workgroup iteration; thread t holds the 8-element vectors
 // t, t + blockDim, ..: 16 consecutive lanes hold one 1x128 tile.
-// kFew: gamma is loaded before the reduction too, which shortens the chain of
-// a call on few rows; on many it costs registers that the streams want
-// (8192 x 7168 bf16: 98 us instead of 93).  kStream: x and r pass the caches
-// by, which on inputs that fit in them costs (1111 x 5120 f32: 9.1 us, 8.6
-// with ordinary reads) and on larger ones gains (8192 x 7168 bf16 with r: 91.5
-// us, 98.7).
-enum NormMode { kFew, kMid, kStream };
-
-template <int XT, int NV, NormMode MODE, bool WITH_Y>
+// STREAM: x and r pass the caches by.  On inputs that fit the caches, where
+// their producer left them, that costs (bf16 of 7168 columns with r, 117 MB of
+// inputs: 51.3 us; 44.6 with ordinary reads), on larger ones it gains (143 MB:
+// 60.3; 66.3).  The ordinary form also loads gamma before the reduction, which
+// shortens its chain (2048 rows: 24.2 -> 23.1 us, one row 4.2 -> 3.8); the
+// streams want those registers (8192 rows: 98 us instead of 93), as do the
+// widest rows.
+template <int XT, int NV, bool STREAM, bool WITH_Y>
 __global__ __launch_bounds__(1024) void norm_kernel(NormArgs p) {
-  constexpr bool AHEAD = MODE == kFew, NT = MODE == kStream;
+  constexpr bool AHEAD = !STREAM && NV <= 2;
   __shared__ float part[2][kMaxWaves];
   const int nvec = (int)(p.cols >> 3);
   int flip = 0;
@@ -92,17 +91,17 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs p) {
     for (int i = 0; i < NV; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
       if (v >= nvec) continue;
-      raw[i] = load_raw8<XT, NT>(p.x, row * p.ldx + v * 8);
+      raw[i] = load_raw8<XT, STREAM>(p.x, row * p.ldx + v * 8);
       if (AHEAD) gamma[i] = load_gamma8(p.gamma, p.g_type, v);
       if (p.r) {
         float a[8], b[8];
         decode8<XT>(raw[i], a);
-        decode8<XT>(load_raw8<XT, NT>(p.r, row * p.ldr + v * 8), b);
+        decode8<XT>(load_raw8<XT, STREAM>(p.r, row * p.ldr + v * 8), b);
 #pragma unroll
         for (int e = 0; e < 8; ++e) a[e] += b[e];
         raw[i] = encode8<XT>(a);
       }
-      if (p.h) store_raw8<XT, WITH_Y && NT>(p.h, row * p.ldh + v * 8, raw[i]);
+      if (p.h) store_raw8<XT, WITH_Y && STREAM>(p.h, row * p.ldh + v * 8, raw[i]);
       float f[8];
       decode8<XT>(raw[i], f);
 #pragma unroll
@@ -273,7 +272,6 @@ __global__ __launch_bounds__(kSumThreads) void norm_grad_sum_kernel(const float*
 }
 
 constexpr int64_t kMaxRowBlocks = 1 << 20;
-constexpr int64_t kFewRows = 256;  // a workgroup per CU
 
 // Vectors per thread and threads per workgroup for rows of `nvec` vectors:
 // at most 512 threads, whose register budget holds a row of up to 2048
@@ -288,37 +286,24 @@ RowShape row_shape(int64_t nvec) {
   return {nv, (int)((t + 63) / 64 * 64)};
 }
 
-template <int XT, bool WITH_Y>
+template <int XT, bool STREAM, bool WITH_Y>
 hipError_t norm_as(const NormArgs& a, hipStream_t st) {
   const RowShape sh = row_shape(a.cols / 8);
   const dim3 grid((unsigned)(a.rows < kMaxRowBlocks ? a.rows : kMaxRowBlocks)), block(sh.threads);
-  const int64_t bytes = a.rows * a.cols * (XT == 0 ? 2 : 4) * (a.r ? 2 : 1);
-  if (a.rows <= kFewRows && sh.nv <= 2) {
-    if (sh.nv == 1)
-      hipLaunchKernelGGL((norm_kernel<XT, 1, kFew, WITH_Y>), grid, block, 0, st, a);
-    else
-      hipLaunchKernelGGL((norm_kernel<XT, 2, kFew, WITH_Y>), grid, block, 0, st, a);
-  } else if (bytes <= kStreamBytes) {
-    if (sh.nv == 1)
-      hipLaunchKernelGGL((norm_kernel<XT, 1, kMid, WITH_Y>), grid, block, 0, st, a);
-    else if (sh.nv == 2)
-      hipLaunchKernelGGL((norm_kernel<XT, 2, kMid, WITH_Y>), grid, block, 0, st, a);
-    else
-      hipLaunchKernelGGL((norm_kernel<XT, 4, kMid, WITH_Y>), grid, block, 0, st, a);
-  } else {
-    if (sh.nv == 1)
-      hipLaunchKernelGGL((norm_kernel<XT, 1, kStream, WITH_Y>), grid, block, 0, st, a);
-    else if (sh.nv == 2)
-      hipLaunchKernelGGL((norm_kernel<XT, 2, kStream, WITH_Y>), grid, block, 0, st, a);
-    else
-      hipLaunchKernelGGL((norm_kernel<XT, 4, kStream, WITH_Y>), grid, block, 0, st, a);
-  }
+  if (sh.nv == 1)
+    hipLaunchKernelGGL((norm_kernel<XT, 1, STREAM, WITH_Y>), grid, block, 0, st, a);
+  else if (sh.nv == 2)
+    hipLaunchKernelGGL((norm_kernel<XT, 2, STREAM, WITH_Y>), grid, block, 0, st, a);
+  else
+    hipLaunchKernelGGL((norm_kernel<XT, 4, STREAM, WITH_Y>), grid, block, 0, st, a);
   return hipGetLastError();
 }
 
 template <int XT>
 hipError_t norm_t(const NormArgs& a, hipStream_t st) {
-  return a.y ? norm_as<XT, true>(a, st) : norm_as<XT, false>(a, st);
+  const int64_t bytes = a.rows * a.cols * (XT == 0 ? 2 : 4) * (a.r ? 2 : 1);
+  if (bytes > kStreamBytes) return a.y ? norm_as<XT, true, true>(a, st) : norm_as<XT, true, false>(a, st);
+  return a.y ? norm_as<XT, false, true>(a, st) : norm_as<XT, false, false>(a, st);
 }
 
 template <int XT, bool NT>
@@ -344,10 +329,15 @@ hipError_t norm_grad_t(const NormGradArgs& a, hipStream_t st) {
 
 }  // namespace
 
-// Two to eight workgroups per CU, more of them where rows are short.
+// Up to 64 rows each their own strip, then four rows to a strip (a strip's
+// partial sums are written and read again: 512 rows of 7168 bf16 take 13.2 us
+// in 128 strips, 19.6 in 512, 14.9 in 256), two strips per CU at most and four
+// where rows are short (16384 x 1024: 23 us in 1024 strips, 27 in 512, 26 in
+// 2048; 8192 x 7168 in 768 strips 92 us, in 512 90).
 int64_t norm_grad_strips(int64_t rows, int64_t cols) {
-  const int64_t most = cols <= 2048 ? 2048 : cols <= 4096 ? 1024 : 512;
-  return rows < most ? rows : most;
+  const int64_t most = cols <= 1024 ? 1024 : 512;
+  const int64_t n = rows < 64 ? rows : rows < 256 ? 64 : (rows + 3) / 4;
+  return n < most ? n : most;
 }
 
 hipError_t launch_norm(const NormArgs& a, hipStream_t st) {

@@ -640,9 +640,10 @@ hipError_t route_as(const RouteArgs& a, const RouteLayout& q, hipStream_t st) {
   return hipGetLastError();
 }
 
-// From this many tokens on, two to a wave: fewer instructions per token.
-// (Below, a wave per token leaves no SIMD with more than two.)
-constexpr int64_t kRouteManyRows = 2048;
+// From this many tokens on, two to a wave: fewer instructions per token, but
+// a longer chain of them (8 of 256 experts, 2048 tokens: 5.1 us, one to a wave
+// 4.8; 4096: 6.0 and 6.5; 8192: 8.4 and 9.8).
+constexpr int64_t kRouteManyRows = 2560;
 
 template <int LT>
 hipError_t route_t(const RouteArgs& a, hipStream_t st) {

@@ -180,3 +180,22 @@ def test_dispatch_gradient_is_combine_without_weights():
     a = np.sum(out.cpu().numpy().astype(np.float64) * g)
     b = np.sum(x.astype(np.float64) * back.cpu().numpy())
     assert abs(a - b) <= 16 * U * np.sum(np.abs(out.cpu().numpy() * g))
+
+
+def test_combine_gradient_against_differences_of_the_kernel():
+    # combine is linear in z and in w, so a difference with any step is the
+    # derivative, up to the rounding of both sides' fp32 results
+    rng = np.random.default_rng(12)
+    _, pos, _ = moe.dispatch(draw_idx(rng, 20, 3, 7, True), 7)
+    p = torch.from_numpy(pos).to(DEV)
+    z, dz_dir = (rng.standard_normal((60, 136)).astype(np.float32) for _ in range(2))
+    w, dw_dir = (rng.standard_normal((20, 3)).astype(np.float32) for _ in range(2))
+    dy = rng.standard_normal((20, 136)).astype(np.float32)
+    dz, dw = (t.cpu().numpy().astype(np.float64) for t in T.combine_backward(dev(dy), dev(z), p, dev(w)))
+
+    def loss(a, b):
+        return np.sum(dy * T.combine(dev(a), p, dev(b)).cpu().numpy().astype(np.float64))
+
+    for a, b, grad in (((z + dz_dir, w), (z - dz_dir, w), np.sum(dz * dz_dir)), ((z, w + dw_dir), (z, w - dw_dir), np.sum(dw * dw_dir))):
+        size = sum(np.sum(np.abs(dy) * moe.combine(np.abs(x), pos, np.abs(y))) for x, y in (a, b))
+        assert abs((loss(*a) - loss(*b)) / 2 - grad) <= 32 * U * size
