@@ -97,23 +97,27 @@ __device__ __forceinline__ float quotient(float x, const TileScale& t) {
   }
 }
 
-// x / s for 8 values with one scale per lane.  Under the amax rule the
+// x / s for N values with one scale per lane.  Under the amax rule the
 // pre-scaling multiply is skipped when no active lane of the wave has a tiny
 // scale (a wave-uniform branch; there it is a multiply by 1).
-template <int RULE>
-__device__ __forceinline__ void quotient8(float (&v)[8], const TileScale& t) {
+template <int RULE, int N>
+__device__ __forceinline__ void quotients(float (&v)[N], const TileScale& t) {
   if constexpr (RULE == 0) {
     if (__builtin_amdgcn_ballot_w64(t.pre != 1.0f) == 0) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = div_by_scale(v[i], t.d, t.y);
+      for (int i = 0; i < N; ++i) v[i] = div_by_scale(v[i], t.d, t.y);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = div_by_scale(v[i] * t.pre, t.d, t.y);
+      for (int i = 0; i < N; ++i) v[i] = div_by_scale(v[i] * t.pre, t.d, t.y);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = v[i] * t.y;
+    for (int i = 0; i < N; ++i) v[i] = v[i] * t.y;
   }
+}
+template <int RULE>
+__device__ __forceinline__ void quotient8(float (&v)[8], const TileScale& t) {
+  quotients<RULE, 8>(v, t);
 }
 
 // Four fp32 values -> four E4M3 bytes (first value in the lowest byte),
@@ -264,6 +268,43 @@ __device__ __forceinline__ void store_raw8(void* __restrict__ p, int64_t off, co
 __device__ __forceinline__ void wave_fence() {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
+}
+
+// 16 bytes of elements (XT 0: 8 bf16, 1: 4 f32): what one lane reads or writes
+// with one instruction, so that a wave's accesses are contiguous.
+template <int XT>
+constexpr int kPer16 = XT == 0 ? 8 : 4;
+
+template <int XT, bool NT>
+__device__ __forceinline__ uint4 load16(const void* __restrict__ p, int64_t off) {
+  const char* q = reinterpret_cast<const char*>(p) + off * (XT == 0 ? 2 : 4);
+  return NT ? ld_nt16(q) : *reinterpret_cast<const uint4*>(q);
+}
+template <int XT, bool NT>
+__device__ __forceinline__ void store16(void* __restrict__ p, int64_t off, uint4 w) {
+  char* q = reinterpret_cast<char*>(p) + off * (XT == 0 ? 2 : 4);
+  if constexpr (NT)
+    st_nt16(q, w);
+  else
+    *reinterpret_cast<uint4*>(q) = w;
+}
+template <int XT>
+__device__ __forceinline__ void decode16(uint4 w, float (&v)[kPer16<XT>]) {
+  if constexpr (XT == 0) {
+    decode8<0>(Raw8<0>{w}, v);
+  } else {
+    v[0] = __uint_as_float(w.x);
+    v[1] = __uint_as_float(w.y);
+    v[2] = __uint_as_float(w.z);
+    v[3] = __uint_as_float(w.w);
+  }
+}
+template <int XT>
+__device__ __forceinline__ uint4 encode16(const float (&v)[kPer16<XT>]) {
+  if constexpr (XT == 0)
+    return encode8<0>(v).w;
+  else
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
 }
 
 // A value and its counterpart 16 or 32 lanes away, in either order (the swap

@@ -317,28 +317,32 @@ __global__ __launch_bounds__(512) void dispatch_small_kernel(Plan p, Move m) {
   move_scales_of(m, t, place);
 }
 
-// A thread sums one 8-element vector over the token's places, the loads of
-// kAhead of them in flight together: a decode batch has few tokens, so the
-// columns are spread over workgroups too.  Reads of z are ordinary (the GEMM
-// has just written it), the result's stores non-temporal: 116 us over
-// 4096 x 8 rows of 4096 f32; non-temporal reads 124, ordinary stores 131.
+// A lane sums 16 bytes of the row over the token's places, the loads of
+// kAhead of them in flight together; the columns are spread over workgroups
+// of one wave, which suits a decode batch's few tokens and the many of a long
+// one alike.  Large z is read past the caches, base ordinarily (its producer
+// has just left it), the result stored past them.  4096 x 8 rows of 4096 f32
+// with base: 101 us (6.6 TB/s); workgroups of two waves 103, of four 105; 32
+// bytes a lane, in two loads, 117; z ordinarily +7, base past the caches +5,
+// the result ordinarily +3.
 constexpr int kAhead = 8;
-constexpr int kCombineThreads = 256;
+constexpr int kCombineThreads = 64;
 
-template <int XT>
+template <int XT, bool NT>
 __global__ __launch_bounds__(kCombineThreads) void combine_kernel(CombineArgs p, int64_t units, int blocks) {
-  const int nvec = (int)(p.cols >> 3);
+  constexpr int N = kPer16<XT>;
+  const int nvec = (int)(p.cols / N);
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
     const int64_t t = u / blocks;
     const int v = (int)(u - t * blocks) * kCombineThreads + threadIdx.x;
     if (v >= nvec) continue;
-    float acc[8];
+    float acc[N];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
-    Raw8<XT> base = {};
-    if (p.base) base = load_raw8<XT, true>(p.base, t * p.ldb + (int64_t)v * 8);
+    for (int e = 0; e < N; ++e) acc[e] = 0.0f;
+    uint4 base = {};
+    if (p.base) base = load16<XT, false>(p.base, t * p.ldb + (int64_t)v * N);
     for (int j0 = 0; j0 < p.k; j0 += kAhead) {
-      Raw8<XT> z[kAhead];
+      uint4 z[kAhead];
       float w[kAhead];
       bool here[kAhead];
 #pragma unroll
@@ -348,26 +352,26 @@ __global__ __launch_bounds__(kCombineThreads) void combine_kernel(CombineArgs p,
         z[j] = {};
         w[j] = 1.0f;
         if (here[j]) {
-          z[j] = load_raw8<XT, false>(p.z, r * p.ldz + (int64_t)v * 8);
+          z[j] = load16<XT, NT>(p.z, r * p.ldz + (int64_t)v * N);
           if (p.w) w[j] = p.w[t * p.ldw + j0 + j];
         }
       }
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
         if (!here[j]) continue;
-        float f[8];
-        decode8<XT>(z[j], f);
+        float f[N];
+        decode16<XT>(z[j], f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] = __builtin_fmaf(w[j], f[e], acc[e]);
+        for (int e = 0; e < N; ++e) acc[e] = __builtin_fmaf(w[j], f[e], acc[e]);
       }
     }
     if (p.base) {
-      float f[8];
-      decode8<XT>(base, f);
+      float f[N];
+      decode16<XT>(base, f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] += f[e];
+      for (int e = 0; e < N; ++e) acc[e] += f[e];
     }
-    store_raw8<XT, true>(p.out, t * p.ldo + (int64_t)v * 8, encode8<XT>(acc));
+    store16<XT, true>(p.out, t * p.ldo + (int64_t)v * N, encode16<XT>(acc));
   }
 }
 
@@ -379,7 +383,8 @@ __global__ __launch_bounds__(kCombineThreads) void combine_kernel(CombineArgs p,
 template <int XT, bool NT>
 __global__ __launch_bounds__(512) void combine_grad_kernel(CombineGradArgs p) {
   __shared__ float part[8][kAhead];
-  const int nvec = (int)(p.cols >> 3);
+  constexpr int N = kPer16<XT>;
+  const int nvec = (int)(p.cols / N);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
   for (int64_t t = blockIdx.x; t < p.tokens; t += gridDim.x) {
     for (int j0 = 0; j0 < p.k; j0 += kAhead) {
@@ -396,27 +401,27 @@ __global__ __launch_bounds__(512) void combine_grad_kernel(CombineGradArgs p) {
         dot[j] = 0.0f;
       }
       for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
-        float d[8];
-        const Raw8<XT> dy = load_raw8<XT, false>(p.dy, t * p.lddy + (int64_t)v * 8);
-        Raw8<XT> z[kAhead];
+        float d[N];
+        const uint4 dy = load16<XT, false>(p.dy, t * p.lddy + (int64_t)v * N);
+        uint4 z[kAhead];
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
           z[j] = {};
-          if (here[j] && p.dw) z[j] = load_raw8<XT, NT>(p.z, row[j] * p.ldz + (int64_t)v * 8);
+          if (here[j] && p.dw) z[j] = load16<XT, NT>(p.z, row[j] * p.ldz + (int64_t)v * N);
         }
-        decode8<XT>(dy, d);
+        decode16<XT>(dy, d);
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
           if (row[j] < 0) continue;
-          float f[8];
+          float f[N];
           if (here[j]) {
-            decode8<XT>(z[j], f);
+            decode16<XT>(z[j], f);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dot[j] = __builtin_fmaf(d[e], f[e], dot[j]);
+            for (int e = 0; e < N; ++e) dot[j] = __builtin_fmaf(d[e], f[e], dot[j]);
           }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = here[j] ? w[j] * d[e] : 0.0f;
-          store_raw8<XT, true>(p.dz, row[j] * p.lddz + (int64_t)v * 8, encode8<XT>(f));
+          for (int e = 0; e < N; ++e) f[e] = here[j] ? w[j] * d[e] : 0.0f;
+          store16<XT, true>(p.dz, row[j] * p.lddz + (int64_t)v * N, encode16<XT>(f));
         }
       }
       if (p.dw) {
@@ -438,7 +443,7 @@ __global__ __launch_bounds__(512) void combine_grad_kernel(CombineGradArgs p) {
 }
 
 constexpr int64_t kMaxTokenBlocks = 1 << 20;
-constexpr int64_t kMaxCombineBlocks = 1 << 22;  // (x 256 threads: below 2^32 work-items)
+constexpr int64_t kMaxCombineBlocks = 1 << 24;  // (x 64 threads: below 2^32 work-items)
 
 unsigned token_blocks(int64_t tokens) { return (unsigned)(tokens < kMaxTokenBlocks ? tokens : kMaxTokenBlocks); }
 
@@ -493,10 +498,13 @@ hipError_t launch_dispatch(const DispatchArgs& a, hipStream_t st) {
 
 template <int XT>
 static void combine_t(const CombineArgs& a, hipStream_t st) {
-  const int64_t blocks = (a.cols / 8 + kCombineThreads - 1) / kCombineThreads;
+  const int64_t blocks = (a.cols / kPer16<XT> + kCombineThreads - 1) / kCombineThreads;
   const int64_t units = a.tokens * blocks;
   const unsigned grid = (unsigned)(units < kMaxCombineBlocks ? units : kMaxCombineBlocks);
-  hipLaunchKernelGGL(combine_kernel<XT>, dim3(grid), dim3(kCombineThreads), 0, st, a, units, (int)blocks);
+  if (a.tokens * a.k * a.cols * (XT == 0 ? 2 : 4) > kStreamBytes)
+    hipLaunchKernelGGL((combine_kernel<XT, true>), dim3(grid), dim3(kCombineThreads), 0, st, a, units, (int)blocks);
+  else
+    hipLaunchKernelGGL((combine_kernel<XT, false>), dim3(grid), dim3(kCombineThreads), 0, st, a, units, (int)blocks);
 }
 
 hipError_t launch_combine(const CombineArgs& a, hipStream_t st) {
@@ -508,7 +516,7 @@ hipError_t launch_combine(const CombineArgs& a, hipStream_t st) {
 }
 
 hipError_t launch_combine_grad(const CombineGradArgs& a, hipStream_t st) {
-  const dim3 grid(token_blocks(a.tokens)), block(row_threads(a.cols / 8));
+  const dim3 grid(token_blocks(a.tokens)), block(row_threads(a.cols / (a.type == 0 ? kPer16<0> : kPer16<1>)));
   const bool stream = a.tokens * a.k * a.cols * (a.type == 0 ? 2 : 4) > kStreamBytes;
   if (a.type == 0 && stream)
     hipLaunchKernelGGL((combine_grad_kernel<0, true>), grid, block, 0, st, a);

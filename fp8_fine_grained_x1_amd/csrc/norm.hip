@@ -45,31 +45,54 @@ __device__ __forceinline__ float block_sum(float v, float* part) {
   return row16_sum(i < waves ? part[i] : 0.0f);
 }
 
-// 8 elements of gamma, undecoded: loaded ahead of the row's reduction.
+// gamma's elements N v .. N v + N - 1, undecoded.
+template <int N>
 struct RawGamma {
   uint4 a, b;
 };
 
-__device__ __forceinline__ RawGamma load_gamma8(const void* __restrict__ g, int g_type, int v) {
-  RawGamma r = {};
+template <int N>
+__device__ __forceinline__ RawGamma<N> load_gamma(const void* __restrict__ g, int g_type, int v) {
+  RawGamma<N> r = {};
   if (g_type == 0) {
-    r.a = reinterpret_cast<const uint4*>(g)[v];
+    if constexpr (N == 8) {
+      r.a = reinterpret_cast<const uint4*>(g)[v];
+    } else {
+      const uint2 h = reinterpret_cast<const uint2*>(g)[v];
+      r.a.x = h.x;
+      r.a.y = h.y;
+    }
   } else {
-    r.a = reinterpret_cast<const uint4*>(g)[2 * v];
-    r.b = reinterpret_cast<const uint4*>(g)[2 * v + 1];
+    r.a = reinterpret_cast<const uint4*>(g)[N / 4 * v];
+    if constexpr (N == 8) r.b = reinterpret_cast<const uint4*>(g)[2 * v + 1];
   }
   return r;
 }
 
-__device__ __forceinline__ void decode_gamma8(const RawGamma& r, int g_type, float v[8]) {
-  if (g_type == 0)
-    decode8<0>(Raw8<0>{r.a}, v);
-  else
-    decode8<1>(Raw8<1>{r.a, r.b}, v);
+template <int N>
+__device__ __forceinline__ void decode_gamma(const RawGamma<N>& r, int g_type, float (&v)[N]) {
+  if (g_type == 0) {
+    v[0] = bf16_lo(r.a.x); v[1] = bf16_hi(r.a.x);
+    v[2] = bf16_lo(r.a.y); v[3] = bf16_hi(r.a.y);
+    if constexpr (N == 8) {
+      v[4] = bf16_lo(r.a.z); v[5] = bf16_hi(r.a.z);
+      v[6] = bf16_lo(r.a.w); v[7] = bf16_hi(r.a.w);
+    }
+  } else {
+    v[0] = __uint_as_float(r.a.x); v[1] = __uint_as_float(r.a.y);
+    v[2] = __uint_as_float(r.a.z); v[3] = __uint_as_float(r.a.w);
+    if constexpr (N == 8) {
+      v[4] = __uint_as_float(r.b.x); v[5] = __uint_as_float(r.b.y);
+      v[6] = __uint_as_float(r.b.z); v[7] = __uint_as_float(r.b.w);
+    }
+  }
 }
 
 // One row per workgroup iteration; thread t holds the 8-element vectors
-// t, t + blockDim, ..: 16 consecutive lanes hold one 1x128 tile.
+// t, t + blockDim, ..: 16 consecutive lanes hold one 1x128 tile.  (For f32, 16
+// bytes a lane and tiles of 32 lanes form every scale in twice the lanes and
+// take more registers: 1111 x 5120 11.4 us instead of 8.6.)
+//
 // STREAM: x and r pass the caches by.  On inputs that fit the caches, where
 // their producer left them, that costs (bf16 of 7168 columns with r, 117 MB of
 // inputs: 51.3 us; 44.6 with ordinary reads), on larger ones it gains (143 MB:
@@ -85,14 +108,14 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs p) {
   int flip = 0;
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, flip ^= 1) {
     Raw8<XT> raw[NV];
-    RawGamma gamma[NV];
+    RawGamma<8> gamma[NV];
     float ss = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
       if (v >= nvec) continue;
       raw[i] = load_raw8<XT, STREAM>(p.x, row * p.ldx + v * 8);
-      if (AHEAD) gamma[i] = load_gamma8(p.gamma, p.g_type, v);
+      if (AHEAD) gamma[i] = load_gamma<8>(p.gamma, p.g_type, v);
       if (p.r) {
         float a[8], b[8];
         decode8<XT>(raw[i], a);
@@ -117,7 +140,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs p) {
       if (v >= nvec) continue;
       float f[8], g[8];
       decode8<XT>(raw[i], f);
-      decode_gamma8(AHEAD ? gamma[i] : load_gamma8(p.gamma, p.g_type, v), p.g_type, g);
+      decode_gamma<8>(AHEAD ? gamma[i] : load_gamma<8>(p.gamma, p.g_type, v), p.g_type, g);
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] = f[e] * rstd * g[e];
       if constexpr (WITH_Y) store_raw8<XT, false>(p.y, row * p.ldy + v * 8, encode8<XT>(f));
@@ -148,42 +171,46 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs p) {
 // threads keep their columns' part of dgamma in registers and write it once.
 // The next row is loaded before the reduction of this one where the registers
 // hold both (PREFETCH); the widest rows (1024 threads) leave gamma and dh in
-// memory until their use, too.
-template <int XT, int NV>
+// memory until their use, too.  A lane holds units of 16 bytes, so that a
+// wave's accesses are contiguous (f32 4096 x 7168 with dh: 94 us; 32 bytes a
+// lane, in two accesses, 101).
+template <int NV>
 struct GradRow {
-  Raw8<XT> d[NV], h[NV], b[NV];
+  uint4 d[NV], h[NV], b[NV];
   float rstd;
 };
 
 template <int XT, int NV, bool NT, bool WITH_B>
-__device__ __forceinline__ void load_grad_row(const NormGradArgs& p, int64_t row, int nvec, GradRow<XT, NV>& r) {
+__device__ __forceinline__ void load_grad_row(const NormGradArgs& p, int64_t row, int nvec, GradRow<NV>& r) {
+  constexpr int N = kPer16<XT>;
   r.rstd = p.rstd[row];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int v = threadIdx.x + i * blockDim.x;
     if (v >= nvec) continue;
-    r.d[i] = load_raw8<XT, NT>(p.dy, row * p.lddy + v * 8);
-    r.h[i] = load_raw8<XT, NT>(p.h, row * p.ldh + v * 8);
-    if (WITH_B && p.dh) r.b[i] = load_raw8<XT, NT>(p.dh, row * p.lddh + v * 8);
+    r.d[i] = load16<XT, NT>(p.dy, row * p.lddy + v * N);
+    r.h[i] = load16<XT, NT>(p.h, row * p.ldh + v * N);
+    if (WITH_B && p.dh) r.b[i] = load16<XT, NT>(p.dh, row * p.lddh + v * N);
   }
 }
 
 template <int XT, int NV, int THREADS, bool PREFETCH, bool NT>
 __global__ __launch_bounds__(THREADS) void norm_grad_kernel(NormGradArgs p) {
+  constexpr int N = kPer16<XT>;
   constexpr bool kKeepGamma = THREADS <= 512;
   __shared__ float part[2][kMaxWaves];
-  const int nvec = (int)(p.cols >> 3);
+  const int nvec = (int)(p.cols / N);
   const float inv_cols = 1.0f / (float)p.cols;
-  float g[NV][8], acc[NV][8];
+  float g[NV][N], acc[NV][N];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int v = threadIdx.x + i * blockDim.x;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) g[i][e] = acc[i][e] = 0.0f;
-    if (kKeepGamma && v < nvec) decode_gamma8(load_gamma8(p.gamma, p.g_type, v), p.g_type, g[i]);
+    for (int e = 0; e < N; ++e) g[i][e] = acc[i][e] = 0.0f;
+    if (kKeepGamma && v < nvec) decode_gamma<N>(load_gamma<N>(p.gamma, p.g_type, v), p.g_type, g[i]);
   }
   int flip = 0;
-  GradRow<XT, NV> r;
+  GradRow<NV> r;
   int64_t row = blockIdx.x;
   if (PREFETCH && row < p.rows) load_grad_row<XT, NV, NT, PREFETCH>(p, row, nvec, r);
   for (; row < p.rows; row += gridDim.x, flip ^= 1) {
@@ -193,44 +220,48 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(NormGradArgs p) {
     for (int i = 0; i < NV; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
       if (v >= nvec) continue;
-      float d[8], h[8];
-      decode8<XT>(r.d[i], d);
-      decode8<XT>(r.h[i], h);
-      if (!kKeepGamma) decode_gamma8(load_gamma8(p.gamma, p.g_type, v), p.g_type, g[i]);
+      float d[N], h[N];
+      decode16<XT>(r.d[i], d);
+      decode16<XT>(r.h[i], h);
+      if (!kKeepGamma) decode_gamma<N>(load_gamma<N>(p.gamma, p.g_type, v), p.g_type, g[i]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
+      for (int e = 0; e < N; ++e) {
         const float dx = d[e] * (h[e] * r.rstd);
         c = __builtin_fmaf(dx, g[i][e], c);
         acc[i][e] += dx;
       }
     }
-    GradRow<XT, NV> next;
+    GradRow<NV> next;
     if (PREFETCH && row + gridDim.x < p.rows) load_grad_row<XT, NV, NT, PREFETCH>(p, row + gridDim.x, nvec, next);
     c = block_sum(c, part[flip]) * inv_cols * r.rstd;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
       if (v >= nvec) continue;
-      float d[8], h[8], o[8];
-      decode8<XT>(r.d[i], d);
-      decode8<XT>(r.h[i], h);
-      if (!kKeepGamma) decode_gamma8(load_gamma8(p.gamma, p.g_type, v), p.g_type, g[i]);
+      float d[N], h[N], o[N];
+      decode16<XT>(r.d[i], d);
+      decode16<XT>(r.h[i], h);
+      if (!kKeepGamma) decode_gamma<N>(load_gamma<N>(p.gamma, p.g_type, v), p.g_type, g[i]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = r.rstd * __builtin_fmaf(-h[e], c, d[e] * g[i][e]);
+      for (int e = 0; e < N; ++e) o[e] = r.rstd * __builtin_fmaf(-h[e], c, d[e] * g[i][e]);
       if (p.dh) {
-        float b[8];
-        decode8<XT>(PREFETCH ? r.b[i] : load_raw8<XT, NT>(p.dh, row * p.lddh + v * 8), b);
+        float b[N];
+        decode16<XT>(PREFETCH ? r.b[i] : load16<XT, NT>(p.dh, row * p.lddh + v * N), b);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] += b[e];
+        for (int e = 0; e < N; ++e) o[e] += b[e];
       }
-      store_raw8<XT, false>(p.dx, row * p.lddx + v * 8, encode8<XT>(o));
+      store16<XT, false>(p.dx, row * p.lddx + v * N, encode16<XT>(o));
     }
     if (PREFETCH) r = next;
   }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int v = threadIdx.x + i * blockDim.x;
-    if (v < nvec) store_raw8<1, false>(p.partial, blockIdx.x * p.cols + v * 8, encode8<1>(acc[i]));
+    if (v >= nvec) continue;
+    float* out = p.partial + blockIdx.x * p.cols + v * N;
+#pragma unroll
+    for (int e = 0; e < N; e += 4)
+      *reinterpret_cast<float4*>(out + e) = make_float4(acc[i][e], acc[i][e + 1], acc[i][e + 2], acc[i][e + 3]);
   }
 }
 
@@ -273,26 +304,27 @@ __global__ __launch_bounds__(kSumThreads) void norm_grad_sum_kernel(const float*
 
 constexpr int64_t kMaxRowBlocks = 1 << 20;
 
-// Vectors per thread and threads per workgroup for rows of `nvec` vectors:
-// at most 512 threads, whose register budget holds a row of up to 2048
-// vectors, and 1024 beyond.  The columns alone decide, and with them the
-// order of a row's additions: its results do not depend on the other rows.
+// Elements (8 `per` thread) and threads of a workgroup for a row: at most 512
+// threads, whose register budget holds a row of up to 16384 elements, and
+// 1024 beyond.  The columns alone decide, and with them the order of a row's
+// additions: its results do not depend on the other rows.
 struct RowShape {
-  int nv, threads;
+  int per, threads;
 };
-RowShape row_shape(int64_t nvec) {
-  const int nv = nvec <= 512 ? 1 : nvec <= 1024 ? 2 : 4;
-  const int64_t t = (nvec + nv - 1) / nv;
-  return {nv, (int)((t + 63) / 64 * 64)};
+RowShape row_shape(int64_t cols) {
+  const int64_t groups = cols / 8;
+  const int per = groups <= 512 ? 1 : groups <= 1024 ? 2 : 4;
+  const int64_t t = (groups + per - 1) / per;
+  return {per, (int)((t + 63) / 64 * 64)};
 }
 
 template <int XT, bool STREAM, bool WITH_Y>
 hipError_t norm_as(const NormArgs& a, hipStream_t st) {
-  const RowShape sh = row_shape(a.cols / 8);
+  const RowShape sh = row_shape(a.cols);
   const dim3 grid((unsigned)(a.rows < kMaxRowBlocks ? a.rows : kMaxRowBlocks)), block(sh.threads);
-  if (sh.nv == 1)
+  if (sh.per == 1)
     hipLaunchKernelGGL((norm_kernel<XT, 1, STREAM, WITH_Y>), grid, block, 0, st, a);
-  else if (sh.nv == 2)
+  else if (sh.per == 2)
     hipLaunchKernelGGL((norm_kernel<XT, 2, STREAM, WITH_Y>), grid, block, 0, st, a);
   else
     hipLaunchKernelGGL((norm_kernel<XT, 4, STREAM, WITH_Y>), grid, block, 0, st, a);
@@ -308,16 +340,17 @@ hipError_t norm_t(const NormArgs& a, hipStream_t st) {
 
 template <int XT, bool NT>
 hipError_t norm_grad_as(const NormGradArgs& a, hipStream_t st) {
-  const RowShape sh = row_shape(a.cols / 8);
+  constexpr int U = 8 / kPer16<XT>;  // units of 8 elements
+  const RowShape sh = row_shape(a.cols);
   const dim3 grid((unsigned)norm_grad_strips(a.rows, a.cols)), block(sh.threads);
-  if (sh.nv == 1)
-    hipLaunchKernelGGL((norm_grad_kernel<XT, 1, 512, true, NT>), grid, block, 0, st, a);
-  else if (sh.nv == 2)
-    hipLaunchKernelGGL((norm_grad_kernel<XT, 2, 512, true, NT>), grid, block, 0, st, a);
+  if (sh.per == 1)
+    hipLaunchKernelGGL((norm_grad_kernel<XT, U, 512, true, NT>), grid, block, 0, st, a);
+  else if (sh.per == 2)
+    hipLaunchKernelGGL((norm_grad_kernel<XT, 2 * U, 512, true, NT>), grid, block, 0, st, a);
   else if (sh.threads <= 512)
-    hipLaunchKernelGGL((norm_grad_kernel<XT, 4, 512, false, NT>), grid, block, 0, st, a);
+    hipLaunchKernelGGL((norm_grad_kernel<XT, 4 * U, 512, false, NT>), grid, block, 0, st, a);
   else
-    hipLaunchKernelGGL((norm_grad_kernel<XT, 4, 1024, false, NT>), grid, block, 0, st, a);
+    hipLaunchKernelGGL((norm_grad_kernel<XT, 4 * U, 1024, false, NT>), grid, block, 0, st, a);
   return hipGetLastError();
 }
 
