@@ -164,7 +164,7 @@ const char* fp8fg_status_string(int status) {
   switch (status) {
     case FP8FG_OK: return "ok";
     case FP8FG_EINVAL: return "invalid argument (null pointer, negative size or stride, bad enum)";
-    case FP8FG_ESHAPE: return "bad shape (size not a required multiple of 128, or leading dimension too small)";
+    case FP8FG_ESHAPE: return "bad shape (size not a required multiple, or leading dimension or workspace too small)";
     case FP8FG_EALIGN: return "misaligned pointer or row pitch (16-byte alignment required)";
     case FP8FG_EUNSUPPORTED: return "valid but unsupported combination";
     case FP8FG_ELAUNCH: return "HIP kernel launch failed";

@@ -55,7 +55,8 @@ extern "C" {
 enum fp8fg_status {
   FP8FG_OK = 0,
   FP8FG_EINVAL = 1,       /* null pointer, negative size, bad enum value     */
-  FP8FG_ESHAPE = 2,       /* size not a required multiple; stride too small  */
+  FP8FG_ESHAPE = 2,       /* size not a required multiple; stride or workspace
+                             too small                                      */
   FP8FG_EALIGN = 3,       /* pointer or row pitch misaligned                  */
   FP8FG_EUNSUPPORTED = 4, /* valid combination that is not implemented        */
   FP8FG_ELAUNCH = 5       /* HIP reported an error at launch                  */
@@ -312,9 +313,9 @@ FP8FG_API int fp8_rmsnorm_backward(const void* dy, int x_type, int64_t rows, int
                          void* workspace, int64_t workspace_bytes, void* stream);
 
 /*
- * fp8_route -- the experts of each token and their weights: [thedaegu]
- * passages on the gating of routed experts and on the bias that balances
- * their load without an auxiliary loss.
+ * fp8_route -- the experts of each token and their weights, with choices
+ * restricted to groups of experts and a bias that balances their load
+ * without an auxiliary loss.
  *
  *   logits : [rows][experts], l_type BF16 or F32, row pitch ldl.  A logit of
  *            -inf or NaN masks its expert.
