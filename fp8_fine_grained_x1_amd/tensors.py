@@ -26,9 +26,10 @@ A mixture-of-experts layer around them:
   combine(z [R][C], pos, w, base)  -> [M][C]
   combine_backward(dy, z, pos, w)  -> dz [R][C], dw [M][k]
 These check the shapes, types, devices and row layouts that the C interface
-cannot see and raise ValueError.  They allocate on the current stream; with
-``stream`` they run on that one (the caller orders it after the producers of
-the inputs) and mark their tensors as in use there.
+cannot see and raise ValueError.  With ``stream`` they allocate and run on
+that one (the caller orders it after the producers of the inputs, and the
+current stream after it before the outputs are used); the inputs are marked
+as in use there, the outputs as in use on the current stream too.
 """
 
 import torch
@@ -154,23 +155,31 @@ def _native():
     return _native_module
 
 
-def _handle(stream, x):
-    """hipStream_t of `stream` (a torch stream or a raw handle), or of the
-    current stream of x's device."""
+def _call(name, stream, x, inputs, args):
+    """The native helper `name` with `args` and a stream's handle, on `stream`
+    (a torch stream or a raw handle) or the current one of x's device.
+
+    On another stream than the current one the outputs and workspaces come
+    from that stream's memory: a block that the current stream has freed may
+    still be in use there."""
+    f = getattr(_native(), name)
     if stream is None:
         d = x.get_device()
-        return torch._C._cuda_getCurrentRawStream(d) if d >= 0 else 0
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-
-
-def _on_stream(stream, out, *inputs):
-    """Tells torch's allocator that a call's tensors are in use on `stream`
-    (its inputs may be another stream's); returns its outputs."""
-    if stream is not None:
-        for t in (*out, *inputs):
-            if t is not None and t.is_cuda:
-                t.record_stream(stream if hasattr(stream, "cuda_stream") else
-                                torch.cuda.ExternalStream(int(stream), device=t.device))
+        return f(*args, torch._C._cuda_getCurrentRawStream(d) if d >= 0 else 0)
+    if not x.is_cuda:
+        return f(*args, 0)  # refuses
+    if not hasattr(stream, "cuda_stream"):
+        stream = (torch.cuda.ExternalStream(int(stream), device=x.device) if int(stream) else
+                  torch.cuda.default_stream(x.device))
+    current = torch.cuda.current_stream(x.device)
+    with torch.cuda.stream(stream):
+        out = f(*args, stream.cuda_stream)
+    for t in inputs:
+        if t is not None:
+            t.record_stream(stream)
+    for t in out:
+        if t is not None:
+            t.record_stream(current)
     return out
 
 
@@ -189,31 +198,29 @@ def rmsnorm_quantize(x, gamma, residual=None, eps=1e-6, pow2=False, scale_layout
     """h = x + residual (x where there is none), y = h * rstd * gamma, and
     y in E4M3 with 1x128 scales.  Returns (q, s, h, y, rstd); y is None
     unless want_y."""
-    out = _native().rmsnorm_quantize(x, gamma, residual, eps, _rule(pow2), _of(_LAYOUT, scale_layout, "scale_layout"),
-                                     want_y, _handle(stream, x))
-    return _on_stream(stream, out, x, gamma, residual)
+    return _call("rmsnorm_quantize", stream, x, (x, gamma, residual),
+                 (x, gamma, residual, eps, _rule(pow2), _of(_LAYOUT, scale_layout, "scale_layout"), want_y))
 
 
 def rmsnorm_backward(dy, h, gamma, rstd, dh=None, stream=None):
     """Gradients of rmsnorm_quantize's y (through the quantizer as it is) and,
     with dh, of its h.  Returns (dx, dgamma); dx is residual's gradient too."""
-    out = _native().rmsnorm_backward(dy, h, gamma, rstd, dh, _handle(stream, h))
-    return _on_stream(stream, out, dy, h, gamma, rstd, dh)[:2]
+    args = (dy, h, gamma, rstd, dh)
+    return _call("rmsnorm_backward", stream, h, args, args)[:2]
 
 
 def route(logits, k, bias=None, score="softmax", groups=1, top_groups=1, group_top=2, renorm=True,
           scale=1.0, stream=None):
     """The k experts of each token and their weights; see fp8_route in
     include/fp8fg.h for the choice, masks and ties."""
-    out = _native().route(logits, k, bias, _of(_SCORE, score, "score"), groups, top_groups, group_top, renorm, scale,
-                          _handle(stream, logits))
-    return _on_stream(stream, out, logits, bias)
+    return _call("route", stream, logits, (logits, bias),
+                 (logits, k, bias, _of(_SCORE, score, "score"), groups, top_groups, group_top, renorm, scale))
 
 
 def route_backward(dw, logits, idx, score="softmax", renorm=True, scale=1.0, stream=None):
     """Gradient of route's weights with respect to the logits."""
-    out = _native().route_backward(dw, logits, idx, _of(_SCORE, score, "score"), renorm, scale, _handle(stream, logits))
-    return _on_stream(stream, out, dw, logits, idx)[0]
+    return _call("route_backward", stream, logits, (dw, logits, idx),
+                 (dw, logits, idx, _of(_SCORE, score, "score"), renorm, scale))[0]
 
 
 def dispatch(idx, experts, x, s=None, scale_layout="group_major", stream=None):
@@ -221,17 +228,19 @@ def dispatch(idx, experts, x, s=None, scale_layout="group_major", stream=None):
     into the order of their experts.  Returns (x', s', offsets, pos, token);
     s' is None for bf16 / f32.  Entries of idx outside [0, experts) come last
     with zero rows."""
-    out = _native().dispatch(idx, experts, x, s, _of(_LAYOUT, scale_layout, "scale_layout"), _handle(stream, x))
-    return _on_stream(stream, out, idx, x, s)[:5]
+    return _call("dispatch", stream, x, (idx, x, s),
+                 (idx, experts, x, s, _of(_LAYOUT, scale_layout, "scale_layout")))[:5]
 
 
 def combine(z, pos, w=None, base=None, stream=None):
     """base + sum_j w[:, j] * z[pos[:, j]] (w None: ones, the gradient of
     dispatch; base None: nothing added)."""
-    return _on_stream(stream, _native().combine(z, pos, w, base, _handle(stream, z)), z, pos, w, base)[0]
+    args = (z, pos, w, base)
+    return _call("combine", stream, z, args, args)[0]
 
 
 def combine_backward(dy, z, pos, w, stream=None):
     """Gradients of combine's z and w for the places of one dispatch (every
     row of z in one place)."""
-    return _on_stream(stream, _native().combine_backward(dy, z, pos, w, _handle(stream, z)), dy, z, pos, w)
+    args = (dy, z, pos, w)
+    return _call("combine_backward", stream, z, args, args)

@@ -395,8 +395,8 @@ FP8FG_API int fp8_dispatch(const int32_t* idx, int64_t ld_idx, int64_t tokens, i
  * fp8_combine -- the experts' rows back in token order.
  *
  *   out[t][c] = base[t][c] + sum_j w[t][j] * z[pos[t][j]][c], in fp32 in the
- *   order of j, rounded once to `type`; places outside [0, z_rows) have no
- *   part (their rows are not read).
+ *   order of j, base last, rounded once to `type`; places outside [0, z_rows)
+ *   have no part (their rows are not read).
  *   z, base, out: type BF16 or F32; base may be null (nothing is added), w
  *            too (ones: the gradient of fp8_dispatch).
  *   pos    : int32 [tokens][k], contiguous.

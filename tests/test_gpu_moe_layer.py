@@ -187,6 +187,32 @@ def test_another_stream():
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("raw", [False, True])
+def test_outputs_on_another_stream_are_that_streams_memory(raw):
+    # a block that the current stream has freed may have work pending there: the other stream must not write it
+    x = torch.randn((2048, 1024), device=DEV)
+    pos = torch.zeros((2048, 1), dtype=torch.int32, device=DEV)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    freed = torch.empty_like(x)
+    at = freed.data_ptr()
+    del freed
+    out = T.combine(x, pos, stream=side.cuda_stream if raw else side)
+    again = torch.empty_like(x)  # the current stream's: the freed block
+    torch.cuda.synchronize()
+    assert again.data_ptr() == at and out.data_ptr() != at
+    assert torch.equal(out, x[:1].expand_as(x))
+
+
+def test_the_default_stream_by_its_null_handle():
+    x = torch.randn((5, 256), device=DEV)
+    pos = torch.tensor([[3], [-1], [0]], dtype=torch.int32, device=DEV)
+    torch.cuda.synchronize()
+    out = T.combine(x, pos, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(out, torch.stack([x[3], torch.zeros_like(x[0]), x[0]]))
+
+
 def test_grouped_gemm_leaves_rows_past_the_experts_alone():
     # dispatch puts dropped entries behind offsets[E]: the grouped GEMM's every tile shape leaves those rows of c as they are
     rng = np.random.default_rng(0)
