@@ -8,7 +8,10 @@
 //           of its `group_top` best choices; the experts of all but the
 //           `top_groups` best groups are out
 //   top-k   by c, the lower index on equal values (groups likewise)
-//   weight  w = scale * s, or scale * s / (sum of the chosen s)
+//   weight  w = scale * s, or scale * s / (sum of the chosen s); the latter for
+//           softmax is scale * softmax over the chosen logits alone and is
+//           formed from them: where the bias keeps the largest logits out,
+//           the chosen scores may have underflowed, their shares have not
 // Slots that find no expert get index -1 and weight 0.
 //
 // The choice is discrete, so the scores' last bits matter: they are formed
@@ -81,6 +84,18 @@ __device__ __forceinline__ float sigmoid_acc(float l, const ExpCoef& k) {
 __device__ __forceinline__ double softmax_term(float l, float top, const ExpCoef& k) {
   const double d = l == top ? 0.0 : (double)l - (double)top;
   return exp_acc(__builtin_fmax(d, (double)kExpFloor), k);
+}
+
+// exp(l - top), a lane's part of the softmax over the chosen logits with the
+// largest at `top`; 0 for a lane without one.  Within 2 units of fp32 at every
+// distance: 2^t by the hardware's 2^f, f = t - rint(t), with t formed in fp64.
+// (No choice hangs on it, so it needs no more bits than that.)
+__device__ __forceinline__ float chosen_term(float l, bool chosen, float top) {
+  const double d = l == top ? 0.0 : (double)l - (double)top;
+  const double t = __builtin_fmax(d * 1.4426950408889634, (double)kExpFloor);  // (2^-200: 0 in fp32)
+  const double n = __builtin_rint(t);
+  const float e = __builtin_ldexpf(__builtin_amdgcn_exp2f((float)(t - n)), (int)n);
+  return chosen ? e : 0.0f;
 }
 
 // fp32 -> unsigned whose order is the floats' (no NaN reaches it); -0 counts
@@ -269,7 +284,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p, Ro
   const int e0 = group * q.size + in_group;
   const int n = group < q.groups ? min(q.slots, q.size - in_group) : 0;  // this lane's experts (<= 0: none)
   const ExpCoef coef = exp_coef();
-  __shared__ float scores[kRouteWaves][64 * NS];
+  __shared__ float scores[kRouteWaves][64 * NS];  // softmax: the logits
   __shared__ int picks[kRouteWaves][64];
   float* mine = scores[wave] + (lane / LANES) * LANES * NS;
   float bias[NS];
@@ -291,7 +306,10 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p, Ro
     double c[NL][4];  // softmax: the terms, until the scores replace them
     if constexpr (SCORE == 0) {
 #pragma unroll
-      for (int s = 0; s < NS; ++s) top = fmaxf(top, l[s]);
+      for (int s = 0; s < NS; ++s) {
+        mine[sub * NS + s] = l[s];
+        top = fmaxf(top, l[s]);
+      }
       top = lanes_max_f32<LANES>(top);
       double sum = 0.0;
 #pragma unroll
@@ -306,7 +324,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p, Ro
       const float sc = SCORE == 0 ? (float)(c[s / 4][s % 4] * inv) : sigmoid_acc(l[s], coef);
       const float v = p.bias ? sc + bias[s] : sc;
       const bool live = l[s] > -INFINITY && v > -INFINITY;  // (a NaN compares false)
-      mine[sub * NS + s] = sc;
+      if constexpr (SCORE == 1) mine[sub * NS + s] = sc;
       c[s / 4][s % 4] = live ? pack(order_key(v), sub * NS + s) : kNoPack;
     }
 #pragma unroll
@@ -376,6 +394,12 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p, Ro
       const int from = at / NS;
       at = (from >> q.lanes) * q.size + (from & ((1 << q.lanes) - 1)) * q.slots + at % NS;
     }
+    if constexpr (SCORE == 0) {  // from the chosen logits; unnormalised, the score once more
+      if (p.renorm)
+        s = chosen_term(s, at >= 0, lanes_max_f32<LANES>(at >= 0 ? s : -INFINITY));
+      else
+        s = at >= 0 ? (float)(softmax_term(s, top, coef) * inv) : 0.0f;
+    }
     const float sum = lanes_sum_f32<LANES>(s);
     if (t < p.rows && sub < p.k) {
       p.idx[t * p.ld_idx + sub] = at;
@@ -427,7 +451,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_any_kernel(RouteArgs p
       if (p.bias && e < E) c[i] += p.bias[e];
       if (!(l[i] > -INFINITY) || !(c[i] == c[i])) c[i] = -INFINITY;
       cbuf[wave][e] = c[i];
-      sbuf[wave][e] = s[i];
+      sbuf[wave][e] = p.score == 0 && p.renorm ? l[i] : s[i];  // what the weights are formed from
     }
     wave_fence();
 
@@ -495,6 +519,10 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_any_kernel(RouteArgs p
         at = e;
         mine = v;
       }
+    }
+    if (p.score == 0 && p.renorm) {
+      mine = chosen_term(mine, at >= 0, lanes_max_f32<64>(at >= 0 ? mine : -INFINITY));
+      sum = lanes_sum_f32<64>(mine);
     }
     if (lane < p.k) {
       p.idx[t * p.ld_idx + lane] = at;

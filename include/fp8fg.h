@@ -329,7 +329,9 @@ FP8FG_API int fp8_rmsnorm_backward(const void* dy, int x_type, int64_t rows, int
  *            descending order.  On equal values the lower index comes first,
  *            of groups as of experts.
  *   w      : scale * s, divided by the sum of the chosen s if renorm is 1
- *            (0 where that sum is 0).
+ *            (sigmoid: 0 where that sum is 0 in fp32; softmax: formed as the
+ *            softmax over the chosen logits, which the bias may have chosen
+ *            far below the largest, where s itself underflows).
  *   A masked expert is never chosen: with fewer candidates than k the last
  *   slots are idx = -1, w = 0.
  *   Requires 1 <= k <= experts, groups dividing experts, 1 <= top_groups <=

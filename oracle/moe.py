@@ -90,7 +90,12 @@ def route_token(logits, k, bias=None, score="softmax", groups=1, top_groups=1, g
     idx = np.full(k, -1, np.int32)
     w = np.zeros(k)
     idx[:len(chosen)] = chosen
-    w[:len(chosen)] = s[chosen].astype(np.float64) if chosen else 0.0
+    if chosen and renorm and score == "softmax":
+        # the shares of the chosen in the softmax over all experts are the
+        # softmax over the chosen alone, also where those scores underflow
+        w[:len(chosen)] = scores(l[chosen], score)
+    elif chosen:
+        w[:len(chosen)] = s[chosen].astype(np.float64)
     total = w.sum()
     if renorm:
         w = w / total if total > 0 else np.zeros(k)

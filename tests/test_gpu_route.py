@@ -241,3 +241,48 @@ def test_many_rows_match_few(E, k, groups, top_groups, group_top, score):
         io, wo = moe.route(l[at], k, bias=bias, **kw)
     assert np.array_equal(idx.cpu().numpy()[at], io)
     assert np.all(np.abs(w.cpu().numpy()[at] - wo) <= 70 * U * np.abs(wo) + 1e-37)
+
+
+@pytest.mark.parametrize("E,groups,top_groups,rows", [(4, 1, 1, 3), (96, 8, 3, 5), (256, 1, 1, 7), (256, 8, 4, 2600),
+                                                      (300, 100, 9, 5), (1024, 4, 2, 3)])
+@pytest.mark.parametrize("gap", [5.0, 100.0, 200.0, 1e4])
+def test_renormalised_softmax_of_experts_far_below_the_top(E, groups, top_groups, rows, gap):
+    # the bias keeps the first expert out, whose logit is `gap` above the
+    # rest: the others' scores underflow, their shares do not.  The choice is
+    # the bias's, so the differences of the kernel's weights are its gradient.
+    say("route below the top: %d experts, gap %g" % (E, gap))
+    rng = np.random.default_rng(E + rows)
+    k = min(3, E - 1)
+    l = rng.uniform(-1, 1, (rows, E)).astype(np.float32)
+    l[:, 0] = gap
+    bias = np.zeros(E, np.float32)
+    size = E // groups
+    picked = rng.permutation(np.arange(1, size))[:k] if size > k else np.arange(1, 1 + k)
+    bias[picked] = 4 + 2.0 * np.arange(picked.size)
+    bias[0] = -4.0
+    kw = dict(groups=groups, top_groups=top_groups, scale=1.5)
+    idx, w = T.route(dev(l), k, bias=dev(bias), **kw)
+    got = idx.cpu().numpy()
+    with np.errstate(all="ignore"):
+        io, wo = moe.route(l[:8], k, bias=bias, **kw)
+    assert np.array_equal(got[:8], io) and np.all(got > 0)
+    e = np.exp(np.take_along_axis(l, got, 1).astype(np.float64))
+    share = 1.5 * e / e.sum(1, keepdims=True)
+    assert np.all(np.abs(w.cpu().numpy() - share) <= 70 * U * share)
+    assert np.all(np.abs(w.cpu().numpy()[:8] - wo) <= 70 * U * np.abs(wo) + 1e-37)
+
+    dw = rng.standard_normal((rows, k)).astype(np.float32)
+    dl = T.route_backward(dev(dw), dev(l), idx, scale=1.5).cpu().numpy().astype(np.float64)
+
+    def loss(a):
+        i, v = T.route(dev(a), k, bias=dev(bias), **kw)
+        assert torch.equal(i, idx)
+        return np.sum(v.cpu().numpy().astype(np.float64) * dw, axis=1)
+
+    # a central difference is off by its truncation, which twice the step has
+    # four times of, by the weights' rounding (2^-20 of their size, over the
+    # step) and the gradient's own (128 u of it), 2^-15 of it together
+    v = rng.uniform(-1, 1, (rows, E))
+    diff = [(loss(l + d * v) - loss(l - d * v)) / (2 * d) for d in (2.0 ** -3, 2.0 ** -4)]
+    bound = np.abs(diff[0] - diff[1]) + 2.0 ** -15 * np.sum(np.abs(dw * w.cpu().numpy()), axis=1)
+    assert np.all(np.abs(diff[1] - np.sum(dl * v, axis=1)) <= bound)

@@ -151,3 +151,21 @@ def test_combine_gradient_against_differences():
         assert abs((loss(z + D * u, w) - loss(z - D * u, w)) / (2 * D) - np.sum(dz * u)) < TOL * 10
         assert abs((loss(z, w + D * v) - loss(z, w - D * v)) / (2 * D) - np.sum(dw * v)) < TOL * 10
     assert np.all(dz[5] == 0) and dw[1, 1] == 0
+
+
+@pytest.mark.parametrize("gap", [5.0, 100.0, 200.0, 1e4])
+def test_weights_of_experts_far_below_the_top(gap):
+    # the bias keeps the largest logit out: the weights are the others' shares, and the gradient is theirs
+    l = np.array([gap, 0.0, 1.0, -1.0], np.float32)
+    bias = np.array([-2.0, 0.5, 0.75, 0.0], np.float32)  # experts 2, 1 by it at every gap
+    idx, w = moe.route_token(l, 2, bias=bias, scale=1.5)
+    e = np.exp(1.0)
+    assert list(idx) == [2, 1] and np.allclose(w, [1.5 * e / (1 + e), 1.5 / (1 + e)], rtol=1e-12)
+    dw = np.array([1.0, -0.5])
+    got = moe.route_grad(dw[None], l[None], idx[None], scale=1.5)[0]
+    for n in range(4):
+        v = np.zeros(4, np.float32)
+        v[n] = 2.0 ** -6
+        diff = (np.sum(dw * moe.route_token(l + v, 2, bias=bias, scale=1.5)[1]) -
+                np.sum(dw * moe.route_token(l - v, 2, bias=bias, scale=1.5)[1])) / 2.0 ** -5
+        assert abs(diff - got[n]) < 2.0 ** -12
