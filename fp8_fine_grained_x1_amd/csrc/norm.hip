@@ -1,7 +1,8 @@
 // Root-mean-square norm with the residual's addition and an E4M3 output with
 // 1x128 scales, and its gradient, for gfx950.
 //
-// Forward, per row:  h = RN(x + r) in x's type,  rstd = 1 / sqrt(mean(h^2) + eps),
+// Forward, per row:  h = RN(x + r) in x's type,  rstd = 1 / sqrt(mean(h^2) + eps)
+//   (0 for a row of zeros with eps 0, at most the largest fp32 number),
 //   y = (h * rstd) * gamma in fp32;  per 1x128 tile the quantizers' scale
 //   s = max(amax |y| / 448, 2^-126) (or its power of two) and
 //   q = E4M3(RN32(y / s)).  y is rounded once into each output: q comes from
@@ -20,6 +21,7 @@
 // non-temporal 95.5; the gradient 85 + 7 us for dgamma's strips (5.5 TB/s),
 // dx non-temporal 90, dy read ordinarily 93.  A large device copy moves
 // 5.1 TB/s on this card.
+#include <float.h>
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -88,6 +90,39 @@ __device__ __forceinline__ void decode_gamma(const RawGamma<N>& r, int g_type, f
   }
 }
 
+// Means of squares (with eps) from here to the largest fp32 number come from
+// fp32 sums: below it squares that fp32 rounds to subnormal numbers (each off
+// by 2^-150 at most, 2^15 of them) could count, above it the sum overflows
+// (elements of 2e17 in 7168 columns).
+constexpr float kLeastMean = 0x1p-100f;
+
+// rstd of a row beyond that range, whose squares are summed in fp64 (2^-298
+// to 2^256 hold those of every number): rare, and never with ordinary eps
+// and values.  A row of zeros with eps 0 gets 0: its y is 0 and no gradient
+// passes.  Every thread of the workgroup takes part.
+template <int XT, int NV>
+__device__ __forceinline__ float wide_range_rstd(const Raw8<XT> (&raw)[NV], int nvec, int64_t cols, float eps, double* part) {
+  double sum = 0.0;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    if ((int)(threadIdx.x + i * blockDim.x) >= nvec) continue;
+    float f[8];
+    decode8<XT>(raw[i], f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum += (double)f[e] * (double)f[e];
+  }
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) sum += __shfl_xor(sum, m);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = sum;
+  __syncthreads();
+  sum = 0.0;
+  for (int w = 0; w < (int)(blockDim.x >> 6); ++w) sum += part[w];
+  __syncthreads();  // (the next such row writes them again)
+  const double m = sum / (double)cols + (double)eps;
+  const double r = m == 0.0 ? 0.0 : 1.0 / sqrt(m);
+  return (float)(r > (double)FLT_MAX ? (double)FLT_MAX : r);
+}
+
 // One row per workgroup iteration; thread t holds the 8-element vectors
 // t, t + blockDim, ..: 16 consecutive lanes hold one 1x128 tile.  (For f32, 16
 // bytes a lane and tiles of 32 lanes form every scale in twice the lanes and
@@ -104,6 +139,7 @@ template <int XT, int NV, bool STREAM, bool WITH_Y>
 __global__ __launch_bounds__(1024) void norm_kernel(NormArgs p) {
   constexpr bool AHEAD = !STREAM && NV <= 2;
   __shared__ float part[2][kMaxWaves];
+  __shared__ double wide[kMaxWaves];
   const int nvec = (int)(p.cols >> 3);
   int flip = 0;
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, flip ^= 1) {
@@ -131,7 +167,10 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs p) {
       for (int e = 0; e < 8; ++e) ss += f[e] * f[e];
     }
     ss = block_sum(ss, part[flip]);
-    const float rstd = 1.0f / sqrtf(ss / (float)p.cols + p.eps);
+    const float mean = ss / (float)p.cols + p.eps;
+    float rstd = 1.0f / sqrtf(mean);
+    if (__builtin_expect(!(mean >= kLeastMean && mean <= FLT_MAX), 0))
+      rstd = wide_range_rstd<XT, NV>(raw, nvec, p.cols, p.eps, wide);
     if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
     if (!p.q && !WITH_Y) continue;
 #pragma unroll
@@ -233,7 +272,12 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(NormGradArgs p) {
     }
     GradRow<NV> next;
     if (PREFETCH && row + gridDim.x < p.rows) load_grad_row<XT, NV, NT, PREFETCH>(p, row + gridDim.x, nvec, next);
-    c = block_sum(c, part[flip]) * inv_cols * r.rstd;
+    c = block_sum(c, part[flip]) * inv_cols;
+    // xh = h * rstd once more (rstd * c could leave fp32's range, xh does
+    // not).  Formed from a copy that the compiler takes for another value: kept
+    // from the loop above instead, f32 rows of 12288 take 64 us, not 54.
+    float rstd = r.rstd;
+    asm("" : "+v"(rstd));
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
@@ -243,7 +287,7 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(NormGradArgs p) {
       decode16<XT>(r.h[i], h);
       if (!kKeepGamma) decode_gamma<N>(load_gamma<N>(p.gamma, p.g_type, v), p.g_type, g[i]);
 #pragma unroll
-      for (int e = 0; e < N; ++e) o[e] = r.rstd * __builtin_fmaf(-h[e], c, d[e] * g[i][e]);
+      for (int e = 0; e < N; ++e) o[e] = rstd * __builtin_fmaf(-(h[e] * rstd), c, d[e] * g[i][e]);
       if (p.dh) {
         float b[N];
         decode16<XT>(PREFETCH ? r.b[i] : load16<XT, NT>(p.dh, row * p.lddh + v * N), b);

@@ -263,7 +263,9 @@ FP8FG_API int fp8_grouped_gemm_blockscaled(int64_t G, const int32_t* offsets,
  * 1x128 tile), without the bf16 tensor in between.
  *
  *   h[m][c]  = RN(x[m][c] + r[m][c]) in x_type (h = x where r is null)
- *   rstd[m]  = 1 / sqrt(sum_c h^2 / cols + eps)
+ *   rstd[m]  = 1 / sqrt(sum_c h^2 / cols + eps), at most FLT_MAX; 0 for a row
+ *              of zeros with eps 0 (y is then 0, and the gradient below has
+ *              no part of the norm)
  *   y[m][c]  = (h * rstd) * gamma[c], in fp32
  *   s, q     = the 1x128 scale and E4M3 bytes of the fp32 y, by the rules of
  *              fp8_quantize_rowtile
@@ -274,6 +276,8 @@ FP8FG_API int fp8_grouped_gemm_blockscaled(int64_t G, const int32_t* offsets,
  *            output) and rstd.
  *   gamma    : [cols], g_type BF16 or F32.  eps >= 0, finite.
  *   A row's results do not depend on the other rows or their number.
+ *   Any finite h, also one whose squares leave fp32's range: the statistics
+ *   of such a row are formed in fp64.
  *   Requires cols % 128 == 0.  rows == 0 or cols == 0 is a valid no-op.
  *   Alignment: x, r, h, y, gamma, q 16-byte aligned, their pitches multiples
  *   of 16 bytes; s and rstd 4-byte aligned.

@@ -29,11 +29,13 @@ def round_to(v, bf16):
 
 
 def rmsnorm(x, gamma, eps, residual=None, bf16=False):
-    """(h float32, rstd float64, y float64) of fp32-held inputs."""
+    """(h float32, rstd float64, y float64) of fp32-held inputs; rstd is at
+    most the largest fp32 number and 0 where the mean square and eps are."""
     x = np.asarray(x, np.float32)
     h = x if residual is None else round_to(x + np.asarray(residual, np.float32), bf16)
     d = h.astype(np.float64)
-    rstd = 1.0 / np.sqrt(np.mean(d * d, axis=1) + eps)
+    m = np.mean(d * d, axis=1) + eps
+    rstd = np.where(m > 0, np.minimum(1.0 / np.sqrt(np.where(m > 0, m, 1.0)), np.finfo(np.float32).max), 0.0)
     return h, rstd, d * rstd[:, None] * np.asarray(gamma, np.float64)
 
 

@@ -201,3 +201,62 @@ def test_gradient_against_differences_of_the_kernel():
                 else:
                     diff.append((loss(x, gamma + d * u) - loss(x, gamma - d * u)) / (2 * d))
             assert abs(diff[1] - grad) <= abs(diff[0] - diff[1]) + noise / 2.0 ** -5, (which, diff, grad)
+
+
+FLT_MAX = float(np.finfo(np.float32).max)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("cols", [256, 7168, 16512])
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+def test_rows_of_every_magnitude(cols, dtype, eps):
+    # squares that overflow fp32 or vanish in it, rows of zeros, one large
+    # element among tiny ones, ordinary rows between them
+    say("norm of every magnitude: %d %s eps %g" % (cols, dtype, eps))
+    rng = np.random.default_rng(cols)
+    mags = [1e-44, 1e-38, 1e-30, 1e-20, 1e-16, 1e-15, 1.0, 1e10, 1e17, 2.2e17, 1e19, 1e25, 5e37, 0.0]
+    x = rng.standard_normal((len(mags) + 2, cols))
+    x /= np.abs(x).max(axis=1, keepdims=True)
+    x[:len(mags)] *= 2.0 * np.array(mags)[:, None]
+    x[-2] = 1e-30 * np.sign(x[-2])
+    x[-2, 3] = 3e38
+    x[-1] = np.sign(x[-1]) * 3.3e38
+    x = moe.round_to(x, dtype == "bf16")
+    gamma = moe.round_to(1 + 0.2 * rng.uniform(-1, 1, cols), False)
+    xd, gd = dev(x, TYPES[dtype]), dev(gamma, torch.float32)
+    for residual in (None, np.zeros_like(x)):
+        q, s, h, y, rstd = T.rmsnorm_quantize(xd, gd, None if residual is None else dev(residual, TYPES[dtype]), eps=eps,
+                                              want_y=True)
+        ho, ro, yo = moe.rmsnorm(x, gamma, eps, residual, dtype == "bf16")
+        assert np.array_equal(host(h), ho)
+        # half a subnormal step where rstd is that small, and what it makes of y
+        assert np.all(np.abs(host(rstd) - ro) <= RSTD * ro + 2.0 ** -150)
+        ty = RSTD + 2 * U + (UB if dtype == "bf16" else U)
+        lost = 2.0 ** -150 * np.abs(ho).astype(np.float64) * np.abs(gamma)
+        assert np.all(np.abs(host(y) - yo) <= ty * np.abs(yo) + lost * (1 + ty) + 1e-40)
+        zero = ~np.any(x, axis=1)
+        assert np.any(zero) and np.all(host(rstd)[zero] == (0.0 if eps == 0 else np.float32(1 / np.sqrt(np.float32(eps)))))
+        z = torch.from_numpy(zero).to(DEV)
+        assert torch.all((q[z] & 0x7F) == 0) and torch.all(s[z] == 2.0 ** -126)  # (-0 keeps its sign)
+        if dtype == "f32":
+            qo, so = oracle.quantize_1x128(host(y))
+            assert np.array_equal(s.cpu().numpy(), so) and np.array_equal(q.cpu().numpy(), qo)
+    # a row's result is its own
+    alone = T.rmsnorm_quantize(xd[9:10], gd, eps=eps, want_y=True)
+    assert torch.equal(alone[0], q[9:10]) and torch.equal(alone[3], y[9:10]) and torch.equal(alone[4], rstd[9:10])
+
+    # the gradient, where rstd keeps it inside fp32
+    dy, dh = (moe.round_to(0.1 * rng.standard_normal(x.shape), dtype == "bf16") for _ in range(2))
+    r = host(rstd)
+    keep = (r < 1e30) & np.isfinite(r)
+    at = torch.from_numpy(np.flatnonzero(keep)).to(DEV)
+    dt = TYPES[dtype]
+    dx, dgamma = T.rmsnorm_backward(dev(dy[keep], dt), xd[at], gd, rstd[at], dh=dev(dh[keep], dt))
+    dxo, dgo = moe.rmsnorm_grad(dy[keep], x[keep], gamma, r[keep], dh[keep])
+    xh, a = x[keep].astype(np.float64) * r[keep, None].astype(np.float64), dy[keep].astype(np.float64) * gamma
+    size = r[keep, None] * (np.abs(a) + np.abs(xh) * np.mean(np.abs(a * xh), axis=1, keepdims=True)) + np.abs(dh[keep])
+    assert np.all(np.abs(host(dx) - dxo) <= 80 * U * size + (UB * np.abs(dxo) if dtype == "bf16" else 0))
+    assert np.all(np.abs(host(dgamma) - dgo) <= 97 * U * np.sum(np.abs(dy[keep] * xh), axis=0))
+    if eps == 0:
+        z = np.flatnonzero(zero[keep])
+        assert np.array_equal(host(dx)[z], dh[keep][z])
