@@ -17,7 +17,8 @@
 // The choice is discrete, so the scores' last bits matter: they are formed
 // in fp64 to about 2^-36 and rounded once, which gives the correctly rounded
 // fp32 value for all but one in some thousand logits; the others are one step off,
-// and choices that lie so close to another are rarer still.  (gfx950 issues fp64
+// and choices that lie so close to another are rarer still.  A token's results
+// depend neither on the other tokens nor on their number.  (gfx950 issues fp64
 // FMAs at the fp32 rate.)
 //
 // Gradient of w with respect to l, from the logits and the indexes alone:
@@ -84,6 +85,15 @@ __device__ __forceinline__ float sigmoid_acc(float l, const ExpCoef& k) {
 __device__ __forceinline__ double softmax_term(float l, float top, const ExpCoef& k) {
   const double d = l == top ? 0.0 : (double)l - (double)top;
   return exp_acc(__builtin_fmax(d, (double)kExpFloor), k);
+}
+
+// A term as it enters the sum: rounded to a multiple of 2^-42, so that the
+// sum of up to 1024 of them is exact in any order and the scores do not depend
+// on how many lanes hold a token (which goes by the number of tokens).  The
+// sum, at least 1, is off by 2^-33 at most and usually by far less.
+__device__ __forceinline__ double on_grid(double term) {
+  constexpr double kShift = 1536.0;  // (1.5 * 2^10: units of 2^-42 in its last place)
+  return (term + kShift) - kShift;
 }
 
 // exp(l - top), a lane's part of the softmax over the chosen logits with the
@@ -315,7 +325,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p, Ro
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
         c[s / 4][s % 4] = softmax_term(l[s], top, coef);
-        sum += s < n ? c[s / 4][s % 4] : 0.0;
+        sum += s < n ? on_grid(c[s / 4][s % 4]) : 0.0;
       }
       inv = 1.0 / lanes_sum_f64<LANES>(sum);
     }
@@ -435,7 +445,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_any_kernel(RouteArgs p
 #pragma unroll
       for (int i = 0; i < NE; ++i) {
         ex[i] = softmax_term(l[i], top, coef);
-        sum += lane + 64 * i < E ? ex[i] : 0.0;
+        sum += lane + 64 * i < E ? on_grid(ex[i]) : 0.0;
       }
       const double inv = 1.0 / lanes_sum_f64<64>(sum);
 #pragma unroll

@@ -336,6 +336,7 @@ FP8FG_API int fp8_rmsnorm_backward(const void* dy, int x_type, int64_t rows, int
  *            (sigmoid: 0 where that sum is 0 in fp32; softmax: formed as the
  *            softmax over the chosen logits, which the bias may have chosen
  *            far below the largest, where s itself underflows).
+ *   A token's results do not depend on the other tokens or their number.
  *   A masked expert is never chosen: with fewer candidates than k the last
  *   slots are idx = -1, w = 0.
  *   Requires 1 <= k <= experts, groups dividing experts, 1 <= top_groups <=

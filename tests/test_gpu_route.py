@@ -286,3 +286,46 @@ def test_renormalised_softmax_of_experts_far_below_the_top(E, groups, top_groups
     diff = [(loss(l + d * v) - loss(l - d * v)) / (2 * d) for d in (2.0 ** -3, 2.0 ** -4)]
     bound = np.abs(diff[0] - diff[1]) + 2.0 ** -15 * np.sum(np.abs(dw * w.cpu().numpy()), axis=1)
     assert np.all(np.abs(diff[1] - np.sum(dl * v, axis=1)) <= bound)
+
+
+# Rows of 96 float32 logits (bytes in hex) with a score so near the middle of
+# two fp32 numbers that the order of the softmax's fp64 sum decides it.
+NEAR = [
+    ("234471c0f0d279bfd16625c0663cfebe0fdb93bd453b59c0b87280bfe59b57c09ae35f404cf70fc0823438bfac64bbbf72e506c0a06f933f"
+     "86650bbf3f77573ed59e39402fb1974066e74f3cf741be3ed98922bebadf2940dc94da3f88cf304088e5a0bf719e4f40c3d82a3f0dad263f"
+     "18430ec04efc11c099cd774096eff23e8a0cbebdce7f96401bdf4ec0431cfcbebc9f22bf8d2aa93fa077034000c3dcbf24445bc0991492be"
+     "04fbe13fac161e4088142240b4e7b7bf01c337bf7cce99c0123f983f06af9a3ffd385fc0d8c3b23fa561fcbf61cd06401a9e823ee33433c0"
+     "7d5f373f0a3e2c401bb0573e6fdb1940b7df1e404cdbaf3ff88012c07d3f7c404a62be3fbff7833f5b25ce3fd101ff3fcf75a43f2202cabf"
+     "819cdcbf2eb7f6befa62f43eb8f05140869f983eb3dd543dbc6850bf228ab23fc919a2be92b4b9bf1dcb05bf2da264bf5d98503e330e78be"
+     "ec9c98c08efb1b406f9be9bf1719c93f9e0723bec6b31e401ae81dc02abbcb3fdc0d23406f568cbeed1b833fc29d3f40"),
+    ("cb9cf43f0e569e3f6ab7c23e0b14d33fbff18e3f343303c0f8a20bc088d307c0b969bfbfe9840940eb3d9e3fa0a061c0e1bf25bf804bccbf"
+     "ebc50e3fc16e58c0d7b1f6be55092fbb4787e1bf95bbd1beb452cabfe64005bfef52693fca9f3240146f96bf4596d73fce0a3ac022cc6340"
+     "46ed1cbf252b08c0794eefbf318c14be50631440e68af3bfde738440364c9f3fe250963f62f76cbd3d6c923ed05b3040da04ba3f366d9abf"
+     "0a049d40dca6d43fdf63543f5630a7bf886e053f0479174009dd1440164a22bfa9b0483f6aac133fc4b2ce3fea4ccd3ee8a4c83e4a7e3bc0"
+     "0beccb3f5d05c13ff9275340ef79bebfa19794c02b0f0040ff84554061059bbf9533aebff4c53dc00d4ca73f51a28ebf37071840dfc7843f"
+     "ee2c05c0dbffc53ebce41e40457d173e3755a3bc1fafc9bff4cc7740b6dbd63edd1d903f35bc39c081316f3d77cb8e3fd80cc2bff7160bbf"
+     "06341ebececbde3e6a64c4bf0dd954bfe0bf6bc0f3657dc0938d6a40816f663f9d3d32bedadb34c04d0614c0063bddbe"),
+]
+
+
+@pytest.mark.parametrize("row", NEAR, ids=["a", "b"])
+def test_a_tokens_weights_do_not_depend_on_the_number_of_tokens(row):
+    l = torch.from_numpy(np.frombuffer(bytes.fromhex(row), np.float32).copy()).to(DEV).expand(2700, -1).contiguous()
+    idx, w = T.route(l, 32, renorm=False)
+    one = T.route(l[:1], 32, renorm=False)
+    assert torch.equal(idx, one[0].expand_as(idx)) and torch.equal(w, one[1].expand_as(w))
+    s = moe.scores(l[0].cpu().numpy(), "softmax")[one[0][0].cpu().numpy()]
+    assert np.all(np.abs(one[1][0].cpu().numpy() - s) <= 1.001 * U * s)
+
+
+@pytest.mark.parametrize("E,k,groups,top_groups", [(96, 32, 1, 1), (100, 16, 1, 1), (240, 8, 6, 2), (256, 8, 8, 4), (256, 32, 1, 1)])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_long_and_short_calls_agree_bit_for_bit(E, k, groups, top_groups, renorm, score):
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(E + k)
+    l = torch.randn((16384, E), generator=gen, device=DEV) * 2
+    kw = dict(groups=groups, top_groups=top_groups, renorm=renorm, score=score, scale=1.5)
+    idx, w = T.route(l, k, **kw)
+    few = [T.route(l[i:i + 2048], k, **kw) for i in range(0, 16384, 2048)]
+    assert torch.equal(idx, torch.cat([f[0] for f in few])) and torch.equal(w, torch.cat([f[1] for f in few]))
