@@ -298,7 +298,7 @@ int fp8_rmsnorm_quantize(const void* x, int x_type, int64_t rows, int64_t cols, 
 }
 
 int64_t fp8_rmsnorm_backward_workspace(int64_t rows, int64_t cols) {
-  if (rows < 0 || cols < 0 || cols > fp8fg::kNormMaxCols) return 0;
+  if (rows < 0 || rows > kMaxI32 || cols < 0 || cols % 8 || cols > fp8fg::kNormMaxCols) return 0;
   return fp8fg::norm_grad_strips(rows, cols) * cols * (int64_t)sizeof(float);
 }
 

@@ -224,3 +224,10 @@ def test_under_host_sanitizers():
     assert "ERROR: AddressSanitizer" not in text and "runtime error:" not in text, text[-4000:]
     assert r.returncode == 0, text[-4000:]
     assert " passed" in text and "failed" not in text
+
+
+@pytest.mark.parametrize("rows,cols", [(4, 252), (4, 4), (1 << 31, 256), (1 << 40, 8), (4, 32776)])
+def test_no_workspace_for_a_refused_norm_gradient(rows, cols):
+    assert B.fp8_rmsnorm_backward_workspace(rows, cols) == 0
+    ld = max(cols, 8)
+    assert norm_grad(rows=rows, cols=cols, lddy=ld, lddh=ld, ldh=ld, lddx=ld) in (SHAPE, ALIGN, UNSUP)
