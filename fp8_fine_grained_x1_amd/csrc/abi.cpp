@@ -425,7 +425,7 @@ int fp8_combine(const void* z, int type, int64_t z_rows, int64_t tokens, int64_t
                           check_rows(out, true, ldo, cols, size));
   if (rc != FP8FG_OK) return rc;
   if (!aligned(pos, 4) || !aligned(w, 4)) return FP8FG_EALIGN;
-  if (beyond(kMaxI32, {z_rows, tokens, k}) || cols > kMaxMoveCols || beyond(kMaxPitch, {ldz, ldw, ldb, ldo}))
+  if (beyond(kMaxI32, {z_rows, tokens}) || k > fp8fg::kCombineMaxK || cols > kMaxMoveCols || beyond(kMaxPitch, {ldz, ldw, ldb, ldo}))
     return FP8FG_EUNSUPPORTED;
   const fp8fg::CombineArgs a{z, type, z_rows, tokens, (int)k, cols, ldz, pos, w, ldw, base, ldb, out, ldo};
   return launched(fp8fg::launch_combine(a, reinterpret_cast<hipStream_t>(stream)));
@@ -447,7 +447,7 @@ int fp8_combine_backward(const void* dy, int type, int64_t z_rows, int64_t token
                           check_rows(dz, z_rows > 0 && cols > 0, lddz, cols, size));
   if (rc != FP8FG_OK) return rc;
   if (!aligned(pos, 4) || !aligned(w, 4) || !aligned(dw, 4)) return FP8FG_EALIGN;
-  if (beyond(kMaxI32, {z_rows, tokens, k}) || cols > kMaxMoveCols ||
+  if (beyond(kMaxI32, {z_rows, tokens}) || k > fp8fg::kCombineMaxK || cols > kMaxMoveCols ||
       beyond(kMaxPitch, {lddy, ldz, ldw, lddz, lddw}))
     return FP8FG_EUNSUPPORTED;
   const fp8fg::CombineGradArgs a{dy, type, z_rows, tokens, (int)k, cols, lddy, z, ldz, pos, w, ldw, dz, lddz, dw, lddw};

@@ -501,7 +501,7 @@ static void combine_t(const CombineArgs& a, hipStream_t st) {
   const int64_t blocks = (a.cols / kPer16<XT> + kCombineThreads - 1) / kCombineThreads;
   const int64_t units = a.tokens * blocks;
   const unsigned grid = (unsigned)(units < kMaxCombineBlocks ? units : kMaxCombineBlocks);
-  if (a.tokens * a.k * a.cols * (XT == 0 ? 2 : 4) > kStreamBytes)
+  if (past_caches(a.tokens, a.k, a.cols, XT == 0 ? 2 : 4))
     hipLaunchKernelGGL((combine_kernel<XT, true>), dim3(grid), dim3(kCombineThreads), 0, st, a, units, (int)blocks);
   else
     hipLaunchKernelGGL((combine_kernel<XT, false>), dim3(grid), dim3(kCombineThreads), 0, st, a, units, (int)blocks);
@@ -517,7 +517,7 @@ hipError_t launch_combine(const CombineArgs& a, hipStream_t st) {
 
 hipError_t launch_combine_grad(const CombineGradArgs& a, hipStream_t st) {
   const dim3 grid(token_blocks(a.tokens)), block(row_threads(a.cols / (a.type == 0 ? kPer16<0> : kPer16<1>)));
-  const bool stream = a.tokens * a.k * a.cols * (a.type == 0 ? 2 : 4) > kStreamBytes;
+  const bool stream = past_caches(a.tokens, a.k, a.cols, a.type == 0 ? 2 : 4);
   if (a.type == 0 && stream)
     hipLaunchKernelGGL((combine_grad_kernel<0, true>), grid, block, 0, st, a);
   else if (a.type == 0)

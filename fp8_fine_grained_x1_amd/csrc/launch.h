@@ -90,6 +90,13 @@ ColumnPlan plan_columns(int64_t tiles_m, int64_t N, int cus);
 // likely to lie in the 256 MB Infinity Cache, where their producer left them.
 constexpr int64_t kStreamBytes = (int64_t)128 << 20;
 
+// Whether `rows * per * cols` elements of `size` bytes are more than that.
+// The combine's product passes 64 bits at sizes that it takes (rows read
+// again and again): compared in fp64.
+inline bool past_caches(int64_t rows, int64_t per, int64_t cols, int size) {
+  return (double)rows * (double)per * (double)cols * size > (double)kStreamBytes;
+}
+
 // ------------------------------------------------- norm (norm.hip)
 struct NormArgs {
   const void* x;
@@ -215,6 +222,9 @@ struct CombineArgs {
   int64_t ldo;
 };
 hipError_t launch_combine(const CombineArgs& a, hipStream_t st);
+// The kernels step through the places in int32, 8 at a time, and past the
+// last ones.
+constexpr int64_t kCombineMaxK = 0x7FFFFFFF - 15;
 
 struct CombineGradArgs {
   const void* dy;

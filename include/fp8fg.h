@@ -409,8 +409,8 @@ FP8FG_API int fp8_dispatch(const int32_t* idx, int64_t ld_idx, int64_t tokens, i
  *   pos    : int32 [tokens][k], contiguous.
  *   Requires k >= 1, cols % 8 == 0.  Alignment: z, base, out 16-byte aligned,
  *   pitches multiples of 16 bytes; pos and w 4-byte aligned.
- *   Limits (FP8FG_EUNSUPPORTED): z_rows, tokens, k <= 2^31 - 1, cols <= 2^28;
- *   pitches as above.
+ *   Limits (FP8FG_EUNSUPPORTED): z_rows, tokens <= 2^31 - 1, k <= 2^31 - 16,
+ *   cols <= 2^28; pitches as above.
  */
 FP8FG_API int fp8_combine(const void* z, int type, int64_t z_rows, int64_t tokens, int64_t k,
                 int64_t cols, int64_t ldz, const int32_t* pos, const float* w,

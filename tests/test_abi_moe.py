@@ -231,3 +231,10 @@ def test_no_workspace_for_a_refused_norm_gradient(rows, cols):
     assert B.fp8_rmsnorm_backward_workspace(rows, cols) == 0
     ld = max(cols, 8)
     assert norm_grad(rows=rows, cols=cols, lddy=ld, lddh=ld, ldh=ld, lddx=ld) in (SHAPE, ALIGN, UNSUP)
+
+
+@pytest.mark.parametrize("k", [(1 << 31) - 15, (1 << 31) - 1, 1 << 31, 1 << 40])
+def test_combine_refuses_places_past_its_steps(k):
+    # (the kernels count the places in int32, 8 at a time)
+    assert combine(tokens=1, k=k, w=None) == UNSUP
+    assert combine_grad(tokens=1, k=k, w=None, dw=None, z=None) == UNSUP

@@ -89,3 +89,22 @@ def test_planner_sweep_under_sanitizers(sanitized, tmp_path):
     _no_reports(text)
     assert r.returncode == 0, text[-4000:]
     assert " 0 failures" in text, text[-2000:]
+
+
+def test_size_rules_under_sanitizers(tmp_path):
+    if not os.path.exists(build.HIPCC):
+        pytest.skip("hipcc not available")
+    runtime = build.asan_runtime()
+    src = os.path.join(ROOT, "tests", "native", "size_check.cpp")
+    obj, exe = str(tmp_path / "size_check.o"), str(tmp_path / "size_check")
+    cmd = ([build.HIPCC] + build.COMMON + build.DEVICE + build.HOST_SANITIZE + ["-x", "hip", "-c", src, "-o", obj])
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-4000:]
+    rtdir, rtlib = os.path.dirname(runtime), os.path.basename(runtime)[len("lib"):-len(".so")]
+    cmd = [build.HIPCC, "--offload-arch=gfx950", "-o", exe, obj, "-L" + rtdir, "-l" + rtlib, "-Wl,-rpath," + rtdir]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-4000:]
+    r = subprocess.run([exe], env=_env(runtime), capture_output=True, text=True, timeout=600)
+    text = r.stdout + r.stderr
+    _no_reports(text)
+    assert r.returncode == 0 and "0 failures" in text, text[-4000:]
