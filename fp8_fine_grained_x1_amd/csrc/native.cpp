@@ -50,6 +50,13 @@ int64_t integer(PyObject* o) {
   return v;
 }
 
+// An enumerator or another small number of the C interface, where -1 is refused:
+// what no int holds is as well.
+int small(PyObject* o) {
+  const int64_t v = integer(o);
+  return v == (int)v ? (int)v : -1;
+}
+
 double number(PyObject* o) {
   const double v = PyFloat_AsDouble(o);
   if (v == -1.0 && PyErr_Occurred()) throw python_error();
@@ -164,7 +171,7 @@ PyObject* rmsnorm_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const bool want_y = truth(a[6]);
   const Tensor y = want_y ? make(M, C, x.scalar_type(), x) : Tensor();
   check(fp8_rmsnorm_quantize(ptr(x), xtype(x), M, C, pitch(x), ptr(r), pitch(r), ptr(gamma), xtype(gamma),
-                             (float)number(a[3]), (int)integer(a[4]), r ? ptr(h) : nullptr, C,
+                             (float)number(a[3]), small(a[4]), r ? ptr(h) : nullptr, C,
                              want_y ? ptr(y) : nullptr, C, ptr<uint8_t>(q), C, ptr<float>(s), s.stride(0), s.stride(1),
                              ptr<float>(rstd), handle(a[7])),
         "fp8_rmsnorm_quantize");
@@ -207,9 +214,10 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor* bias = tensor_or_none(a[2], "bias");
   vec1(bias, E, l, true, "bias");
   const c10::DeviceGuard guard(l.device());
-  const Tensor idx = make(M, k, at::kInt, l), w = make(M, k, at::kFloat, l);
-  check(fp8_route(ptr(l), xtype(l), M, E, pitch(l), ptr<float>(bias), (int)integer(a[3]), integer(a[4]), integer(a[5]),
-                  (int)integer(a[6]), k, truth(a[7]), (float)number(a[8]), ptr<int32_t>(idx), k, ptr<float>(w), k,
+  const int64_t slots = k <= E ? k : 0;  // (beyond: the call below refuses)
+  const Tensor idx = make(M, slots, at::kInt, l), w = make(M, slots, at::kFloat, l);
+  check(fp8_route(ptr(l), xtype(l), M, E, pitch(l), ptr<float>(bias), small(a[3]), integer(a[4]), integer(a[5]),
+                  small(a[6]), k, truth(a[7]), (float)number(a[8]), ptr<int32_t>(idx), k, ptr<float>(w), k,
                   handle(a[9])),
         "fp8_route");
   return give({&idx, &w});
@@ -232,7 +240,7 @@ PyObject* route_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
        "must be f32 [tokens][k] on the logits' device");
   const c10::DeviceGuard guard(l.device());
   const Tensor dl = make(M, E, l.scalar_type(), l);
-  check(fp8_route_backward(ptr(l), xtype(l), M, E, pitch(l), (int)integer(a[3]), k, truth(a[4]), (float)number(a[5]),
+  check(fp8_route_backward(ptr(l), xtype(l), M, E, pitch(l), small(a[3]), k, truth(a[4]), (float)number(a[5]),
                            ptr<int32_t>(idx), pitch(idx), ptr<float>(dw), pitch(dw), ptr(dl), E, handle(a[6])),
         "fp8_route_backward");
   return give({&dl});
@@ -261,11 +269,12 @@ PyObject* dispatch(PyObject*, PyObject* const* a, Py_ssize_t n) {
              s->device() == x.device(),
          "s", "must be the f32 [tokens][columns / 128] scales of x");
   const c10::DeviceGuard guard(x.device());
-  const Tensor out = make(M * k, C, x.scalar_type(), x), offsets = make1(E + 1, at::kInt, x), pos = make(M, k, at::kInt, x);
-  const Tensor token = make1(M * k, at::kInt, x);
-  const Tensor os = s ? make_scales(M * k, C / 128, truth(a[4]), x) : Tensor();
-  const int64_t bytes = fp8_dispatch_workspace(M, k, E);
-  const Tensor ws = make1(bytes + 16, at::kByte, x);  // (0 bytes: the call below says why)
+  // 0 bytes: sizes that the call below refuses, saying why; nothing of them is allocated
+  const int64_t bytes = fp8_dispatch_workspace(M, k, E), rows = bytes ? M * k : 1;
+  const Tensor out = make(rows, C, x.scalar_type(), x), offsets = make1(bytes ? E + 1 : 1, at::kInt, x);
+  const Tensor pos = bytes ? make(M, k, at::kInt, x) : make1(1, at::kInt, x), token = make1(rows, at::kInt, x);
+  const Tensor os = s ? make_scales(rows, C / 128, truth(a[4]), x) : Tensor();
+  const Tensor ws = make1(bytes + 16, at::kByte, x);
   check(fp8_dispatch(ptr<int32_t>(idx), pitch(idx), M, k, E, ptr(x), type, C, pitch(x), ptr<float>(s), s ? s->stride(0) : 0,
                      s ? s->stride(1) : 0, ptr<int32_t>(offsets), ptr<int32_t>(pos), ptr<int32_t>(token), ptr(out), C,
                      s ? ptr<float>(os) : nullptr, s ? os.stride(0) : 0, s ? os.stride(1) : 0, ptr(ws), bytes, handle(a[5])),

@@ -270,3 +270,21 @@ def test_refusals_on_the_gpu():
     assert e.value.status == B.FP8FG_EUNSUPPORTED
     with pytest.raises(TypeError):
         T.route(f, "k")
+
+
+@pytest.mark.parametrize("call,status", [
+    (lambda f, i: T.route(f, 1 << 31), B.FP8FG_ESHAPE), (lambda f, i: T.route(f, 1 << 45), B.FP8FG_ESHAPE),
+    (lambda f, i: T.route(f, (1 << 63) - 1), B.FP8FG_ESHAPE), (lambda f, i: T.route(f, 0), B.FP8FG_EINVAL),
+    (lambda f, i: T.route(f, 2, group_top=(1 << 32) + 1), B.FP8FG_EINVAL), (lambda f, i: T.route(f, 2, groups=1 << 40), B.FP8FG_ESHAPE),
+    (lambda f, i: T.dispatch(i, 1 << 40, f), B.FP8FG_EUNSUPPORTED), (lambda f, i: T.dispatch(i, (1 << 63) - 1, f), B.FP8FG_EUNSUPPORTED),
+    (lambda f, i: T.dispatch(i, 0, f), B.FP8FG_EINVAL), (lambda f, i: T.dispatch(i[:, :0], 8, f), B.FP8FG_EINVAL),
+])
+def test_sizes_are_refused_before_anything_is_allocated(call, status):
+    f, i = torch.zeros((4, 256), device=DEV), torch.zeros((4, 2), dtype=torch.int32, device=DEV)
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    held = torch.cuda.memory_allocated()
+    with pytest.raises(B.Fp8fgError) as e:
+        call(f, i)
+    assert e.value.status == status
+    assert torch.cuda.max_memory_allocated() - held <= 1 << 16
