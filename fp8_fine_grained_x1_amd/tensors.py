@@ -164,9 +164,9 @@ def _call(name, stream, x, inputs, args):
     still be in use there."""
     f = getattr(_native(), name)
     if stream is None:
-        d = x.get_device()
+        d = x.get_device() if isinstance(x, torch.Tensor) else -1
         return f(*args, torch._C._cuda_getCurrentRawStream(d) if d >= 0 else 0)
-    if not x.is_cuda:
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
         return f(*args, 0)  # refuses
     if not hasattr(stream, "cuda_stream"):
         stream = (torch.cuda.ExternalStream(int(stream), device=x.device) if int(stream) else

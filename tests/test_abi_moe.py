@@ -238,3 +238,15 @@ def test_combine_refuses_places_past_its_steps(k):
     # (the kernels count the places in int32, 8 at a time)
     assert combine(tokens=1, k=k, w=None) == UNSUP
     assert combine_grad(tokens=1, k=k, w=None, dw=None, z=None) == UNSUP
+
+
+def test_tensor_helpers_refuse_what_is_no_tensor():
+    i = torch.zeros((4, 2), dtype=torch.int32)
+    for bad in (None, 3, [[1.0]], "x"):
+        for call in (lambda **k: T.rmsnorm_quantize(bad, bad, **k), lambda **k: T.rmsnorm_backward(bad, bad, bad, bad, **k),
+                     lambda **k: T.route(bad, 2, **k), lambda **k: T.route_backward(bad, bad, i, **k),
+                     lambda **k: T.dispatch(i, 8, bad, **k), lambda **k: T.combine(bad, i, **k),
+                     lambda **k: T.combine_backward(bad, bad, i, None, **k)):
+            for kw in (dict(), dict(stream=0)):
+                with pytest.raises(ValueError):
+                    call(**kw)
