@@ -171,6 +171,8 @@ def _call(name, stream, x, inputs, args):
     if not hasattr(stream, "cuda_stream"):
         stream = (torch.cuda.ExternalStream(int(stream), device=x.device) if int(stream) else
                   torch.cuda.default_stream(x.device))
+    if stream.device != x.device:
+        raise ValueError("stream must be one of the inputs' device")
     current = torch.cuda.current_stream(x.device)
     with torch.cuda.stream(stream):
         out = f(*args, stream.cuda_stream)

@@ -288,3 +288,12 @@ def test_sizes_are_refused_before_anything_is_allocated(call, status):
         call(f, i)
     assert e.value.status == status
     assert torch.cuda.max_memory_allocated() - held <= 1 << 16
+
+
+def test_a_stream_of_another_device_is_refused():
+    class Other:
+        cuda_stream, device = 1, torch.device("cuda", 1)
+
+    x = torch.randn((5, 256), device=DEV)
+    with pytest.raises(ValueError):
+        T.route(x, 2, stream=Other())
