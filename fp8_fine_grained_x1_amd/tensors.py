@@ -26,10 +26,13 @@ A mixture-of-experts layer around them:
   combine(z [R][C], pos, w, base)  -> [M][C]
   combine_backward(dy, z, pos, w)  -> dz [R][C], dw [M][k]
 These check the shapes, types, devices and row layouts that the C interface
-cannot see and raise ValueError.  With ``stream`` they allocate and run on
-that one (the caller orders it after the producers of the inputs, and the
-current stream after it before the outputs are used); the inputs are marked
-as in use there, the outputs as in use on the current stream too.
+cannot see and raise ValueError.
+
+With ``stream`` every function here allocates and runs on that one (the caller
+orders it after the producers of the inputs, and the current stream after it
+before the outputs are used); the inputs are marked as in use there, the
+outputs as in use on the current stream too.  Outputs carry no autograd graph,
+also where inputs require gradients: the backward functions are called.
 """
 
 import torch
@@ -38,6 +41,31 @@ from . import binding as B
 
 _XTYPE = {torch.bfloat16: B.FP8FG_BF16, torch.float32: B.FP8FG_F32}
 _CTYPE = {torch.bfloat16: B.FP8FG_BF16, torch.float32: B.FP8FG_F32}
+
+
+def _on_stream(f, stream, x, inputs):
+    """f() with `stream` (a torch stream or a raw handle) as the current one of
+    x's device.
+
+    On another stream than the current one the outputs and workspaces come
+    from that stream's memory: a block that the current stream has freed may
+    still be in use there.  The inputs are marked as in use on it, the outputs
+    as in use on the current one."""
+    if not hasattr(stream, "cuda_stream"):
+        stream = (torch.cuda.ExternalStream(int(stream), device=x.device) if int(stream) else
+                  torch.cuda.default_stream(x.device))
+    if stream.device != x.device:
+        raise ValueError("stream must be one of the inputs' device")
+    current = torch.cuda.current_stream(x.device)
+    with torch.cuda.stream(stream):
+        out = f()
+    for t in inputs:
+        if t is not None:
+            t.record_stream(stream)
+    for t in (out if isinstance(out, tuple) else (out,)):
+        if t is not None:
+            t.record_stream(current)
+    return out
 
 
 def _rule(pow2):
@@ -54,6 +82,8 @@ def _scales(rows, groups, layout, device):
 
 
 def quantize_1x128(x, pow2=False, scale_layout="group_major", stream=None):
+    if stream is not None and x.is_cuda:
+        return _on_stream(lambda: quantize_1x128(x, pow2, scale_layout), stream, x, (x,))
     M, K = x.shape
     q = torch.empty((M, K), dtype=torch.uint8, device=x.device)
     s = _scales(M, K // 128, scale_layout, x.device)
@@ -64,6 +94,8 @@ def quantize_1x128(x, pow2=False, scale_layout="group_major", stream=None):
 
 
 def quantize_128x1(x, pow2=False, scale_layout="group_major", stream=None):
+    if stream is not None and x.is_cuda:
+        return _on_stream(lambda: quantize_128x1(x, pow2, scale_layout), stream, x, (x,))
     T, F = x.shape
     qt = torch.empty((F, T), dtype=torch.uint8, device=x.device)
     st = _scales(F, T // 128, scale_layout, x.device)
@@ -74,6 +106,8 @@ def quantize_128x1(x, pow2=False, scale_layout="group_major", stream=None):
 
 
 def requantize_128x1(q, s, pow2=False, scale_layout="group_major", stream=None):
+    if stream is not None and q.is_cuda:
+        return _on_stream(lambda: requantize_128x1(q, s, pow2, scale_layout), stream, q, (q, s))
     T, F = q.shape
     qt = torch.empty((F, T), dtype=torch.uint8, device=q.device)
     st = _scales(F, T // 128, scale_layout, q.device)
@@ -84,6 +118,8 @@ def requantize_128x1(q, s, pow2=False, scale_layout="group_major", stream=None):
 
 
 def quantize_block(w, pow2=False, transpose=True, stream=None):
+    if stream is not None and w.is_cuda:
+        return _on_stream(lambda: quantize_block(w, pow2, transpose), stream, w, (w,))
     K, N = w.shape
     shape = (N, K) if transpose else (K, N)
     q = torch.empty(shape, dtype=torch.uint8, device=w.device)
@@ -107,6 +143,9 @@ def gemm(qa, sa, qb, sb, out_dtype=torch.bfloat16, col_scales=False, no_promotio
     FP8 MFMA instead of the exact default path.  e8m0_scales: the FP8 MFMA
     applies the scales' powers of two as its E8M0 operand scales.  tiles:
     see tile_flags (default path only)."""
+    if stream is not None and qa.is_cuda:
+        return _on_stream(lambda: gemm(qa, sa, qb, sb, out_dtype, col_scales, no_promotion, fp8_mfma, e8m0_scales, out,
+                                       tiles=tiles), stream, qa, (qa, sa, qb, sb, out))
     M, K = qa.shape
     N = qb.shape[0]
     c = out if out is not None else torch.empty((M, N), dtype=out_dtype, device=qa.device)
@@ -129,6 +168,9 @@ def gemm(qa, sa, qb, sb, out_dtype=torch.bfloat16, col_scales=False, no_promotio
 
 def grouped_gemm(qa, sa, offsets, qb, sb, out_dtype=torch.bfloat16, out=None, stream=None,
                  flags=B.FP8FG_GEMM_DEFAULT, tiles=None):
+    if stream is not None and qa.is_cuda:
+        return _on_stream(lambda: grouped_gemm(qa, sa, offsets, qb, sb, out_dtype, out, flags=flags, tiles=tiles), stream, qa,
+                          (qa, sa, offsets, qb, sb, out))
     M, K = qa.shape
     G, N, _ = qb.shape
     c = out if out is not None else torch.empty((M, N), dtype=out_dtype, device=qa.device)
@@ -157,32 +199,12 @@ def _native():
 
 def _call(name, stream, x, inputs, args):
     """The native helper `name` with `args` and a stream's handle, on `stream`
-    (a torch stream or a raw handle) or the current one of x's device.
-
-    On another stream than the current one the outputs and workspaces come
-    from that stream's memory: a block that the current stream has freed may
-    still be in use there."""
-    f = getattr(_native(), name)
-    if stream is None:
-        d = x.get_device() if isinstance(x, torch.Tensor) else -1
-        return f(*args, torch._C._cuda_getCurrentRawStream(d) if d >= 0 else 0)
-    if not isinstance(x, torch.Tensor) or not x.is_cuda:
-        return f(*args, 0)  # refuses
-    if not hasattr(stream, "cuda_stream"):
-        stream = (torch.cuda.ExternalStream(int(stream), device=x.device) if int(stream) else
-                  torch.cuda.default_stream(x.device))
-    if stream.device != x.device:
-        raise ValueError("stream must be one of the inputs' device")
-    current = torch.cuda.current_stream(x.device)
-    with torch.cuda.stream(stream):
-        out = f(*args, stream.cuda_stream)
-    for t in inputs:
-        if t is not None:
-            t.record_stream(stream)
-    for t in out:
-        if t is not None:
-            t.record_stream(current)
-    return out
+    (see _on_stream) or the current one of x's device."""
+    on_gpu = isinstance(x, torch.Tensor) and x.is_cuda
+    if stream is not None and on_gpu:
+        return _on_stream(lambda: _call(name, None, x, inputs, args), stream, x, inputs)
+    # (not on the GPU: the helper refuses)
+    return getattr(_native(), name)(*args, torch._C._cuda_getCurrentRawStream(x.get_device()) if on_gpu else 0)
 
 
 _LAYOUT = {"group_major": True, "row_major": False}
