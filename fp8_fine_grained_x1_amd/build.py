@@ -97,22 +97,24 @@ def _link_native(obj, torch_lib):
 
 
 def build(verbose=True):
+    """Both libraries.  libfp8fg.so needs neither torch nor Python's headers and
+    is linked whether or not _native.so, which does, can be built; an error of
+    the latter is raised after that."""
     if not os.path.exists(HIPCC):
         raise RuntimeError("hipcc not found at %s" % HIPCC)
     os.makedirs(BUILD, exist_ok=True)
     with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         native = ex.submit(_compile_native)
         objs = list(ex.map(_compile, SOURCES))
-        native = native.result()
     tmp = LIB + ".tmp"
     cmd = [HIPCC, "-shared", "--offload-arch=gfx950", "-fPIC", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("link failed: %s\n%s\n%s" % (" ".join(cmd), r.stdout, r.stderr))
     shutil.move(tmp, LIB)
-    _link_native(*native)
     if verbose:
         print("built", LIB)
+    _link_native(*native.result())
     return LIB
 
 
