@@ -31,11 +31,18 @@ constexpr int kPlanWaves = kPlanThreads / 64;
 constexpr int kMaxChunks = 256;
 constexpr int kMinChunk = 1024;
 constexpr int kMaxBuckets = 1025;  // experts and the bucket of dropped entries
-// Lists of up to this many entries are placed by every token's workgroup for
-// itself, in the launch that moves the rows: work that grows with the square
-// of the list (eight of 256 experts, rows of 7168 bytes: 512 entries 5.5 us, in
-// three launches 10.7; 2048: 8.9 and 13.4; 4096: 15.3 and 14.3).
-constexpr int kSmallEntries = 2560;
+// Short lists are placed by every token's workgroup for itself, in the launch
+// that moves the rows: work for each token and entry (reading the list, k
+// comparisons), so that tokens x entries bounds it where k is small and the
+// entries alone where it is not.  In one launch and in three, us, 256 experts,
+// rows of 7168 / 2048 bytes:
+//   k = 1    1536 entries  10.8, 12.3 / 10.0, 10.2     2048  15.3, 13.0 / 13.7, 10.4
+//   k = 2    2048  10.4, 12.5 / 9.3, 10.0              2560  12.6, 12.9 / 12.0, 10.6
+//   k = 4    2560  10.9, 12.2 / 9.4, 10.3              3584  15.8, 13.3 / 14.0, 10.8
+//   k = 8    2560  11.3, 13.8 / 9.7, 11.1              4096  15.0, 14.7 / 12.6, 11.8
+//   k = 16   2560  12.6, 15.3 / 10.8, 11.8             3584  16.4, 16.2 / 13.4, 12.3
+constexpr int64_t kSmallReads = 2400000;
+constexpr int64_t kSmallEntries = 3000;
 constexpr int kSmallK = 16;
 
 struct Plan {
@@ -479,7 +486,7 @@ hipError_t launch_dispatch(const DispatchArgs& a, hipStream_t st) {
   Move m{reinterpret_cast<const uint8_t*>(a.x), a.ldx * size, (int)(a.cols * size / 16), a.xs, a.xs_rs, a.xs_ts,
          a.x_type == 2 ? (int)(a.cols / 128) : 0, a.tokens, (int)entries, a.k, a.pos, a.token,
          reinterpret_cast<uint8_t*>(a.out), a.ldo * size, a.os, a.os_rs, a.os_ts, 0};
-  if (entries <= kSmallEntries && a.k <= kSmallK) {
+  if (entries <= kSmallEntries && a.tokens * entries <= kSmallReads && a.k <= kSmallK) {
     hipLaunchKernelGGL(dispatch_small_kernel, dim3((unsigned)a.tokens + 1), dim3(kPlanThreads), 0, st, p, m);
     return hipGetLastError();
   }

@@ -199,3 +199,18 @@ def test_combine_gradient_against_differences_of_the_kernel():
     for a, b, grad in (((z + dz_dir, w), (z - dz_dir, w), np.sum(dz * dz_dir)), ((z, w + dw_dir), (z, w - dw_dir), np.sum(dw * dw_dir))):
         size = sum(np.sum(np.abs(dy) * moe.combine(np.abs(x), pos, np.abs(y))) for x, y in (a, b))
         assert abs((loss(*a) - loss(*b)) / 2 - grad) <= 32 * U * size
+
+
+@pytest.mark.parametrize("M,k,E", [(1549, 1, 40), (1550, 1, 40), (1095, 2, 9), (1096, 2, 9), (750, 4, 64), (751, 4, 64),
+                                   (375, 8, 256), (376, 8, 256), (187, 16, 60), (188, 16, 60), (100, 17, 60)])
+def test_dispatch_on_both_sides_of_one_launch(M, k, E):
+    # sizes around the border between the one-launch and the three-launch form
+    say("dispatch border %d x %d" % (M, k))
+    rng = np.random.default_rng(M + k)
+    idx = draw_idx(rng, M, k, E, True)
+    x = rng.integers(0, 255, size=(M, 256)).astype(np.uint8)
+    s = rng.random((M, 2)).astype(np.float32)
+    q, qs, *places = T.dispatch(torch.from_numpy(idx).to(DEV), E, torch.from_numpy(x).to(DEV), torch.from_numpy(s).to(DEV))
+    po, to = check_places(idx, E, places)
+    assert np.array_equal(q.cpu().numpy(), np.where(to[:, None] >= 0, x[to], 0))
+    assert np.array_equal(qs.cpu().numpy(), np.where(to[:, None] >= 0, s[to], np.float32(2.0 ** -126)))
