@@ -212,30 +212,70 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs p) {
 // hold both (PREFETCH); the widest rows (1024 threads) leave gamma and dh in
 // memory until their use, too.  A lane holds units of 16 bytes, so that a
 // wave's accesses are contiguous (f32 4096 x 7168 with dh: 94 us; 32 bytes a
-// lane, in two accesses, 101).
-template <int NV>
+// lane, in two accesses, 101); the widest rows units of 8 elements, of which
+// f32 then has half as many to guard (1024 x 20480: 90 us with 8 registers
+// spilled; in 16-byte units 124 with 54).  A row's address is formed once for
+// the wave, in scalar registers (per lane and unit 77 spilled, 140 us).
+template <int XT, int N>
+struct Unit {  // N elements, undecoded
+  uint4 w[N / kPer16<XT>];
+};
+
+// Unit v of the row that starts `row` elements in.
+template <int XT, bool NT, int N>
+__device__ __forceinline__ Unit<XT, N> load_unit(const void* __restrict__ p, int64_t row, uint32_t v) {
+  const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(p) + row * (XT == 0 ? 2 : 4));
+  Unit<XT, N> u;
+#pragma unroll
+  for (int i = 0; i < N / kPer16<XT>; ++i) u.w[i] = NT ? ld_nt16(q + v * (N / kPer16<XT>) + i) : q[v * (N / kPer16<XT>) + i];
+  return u;
+}
+template <int XT, int N>
+__device__ __forceinline__ void store_unit(void* __restrict__ p, int64_t row, uint32_t v, const float (&x)[N]) {
+  constexpr int M = kPer16<XT>;
+  uint4* q = reinterpret_cast<uint4*>(reinterpret_cast<char*>(p) + row * (XT == 0 ? 2 : 4));
+#pragma unroll
+  for (int i = 0; i < N / M; ++i) {
+    float f[M];
+#pragma unroll
+    for (int e = 0; e < M; ++e) f[e] = x[i * M + e];
+    q[v * (N / M) + i] = encode16<XT>(f);
+  }
+}
+template <int XT, int N>
+__device__ __forceinline__ void decode_unit(const Unit<XT, N>& u, float (&v)[N]) {
+  constexpr int M = kPer16<XT>;
+#pragma unroll
+  for (int i = 0; i < N / M; ++i) {
+    float f[M];
+    decode16<XT>(u.w[i], f);
+#pragma unroll
+    for (int e = 0; e < M; ++e) v[i * M + e] = f[e];
+  }
+}
+
+template <int XT, int NV, int N>
 struct GradRow {
-  uint4 d[NV], h[NV], b[NV];
+  Unit<XT, N> d[NV], h[NV], b[NV];
   float rstd;
 };
 
-template <int XT, int NV, bool NT, bool WITH_B>
-__device__ __forceinline__ void load_grad_row(const NormGradArgs& p, int64_t row, int nvec, GradRow<NV>& r) {
-  constexpr int N = kPer16<XT>;
+template <int XT, int NV, int N, bool NT, bool WITH_B>
+__device__ __forceinline__ void load_grad_row(const NormGradArgs& p, int64_t row, int nvec, GradRow<XT, NV, N>& r) {
   r.rstd = p.rstd[row];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int v = threadIdx.x + i * blockDim.x;
     if (v >= nvec) continue;
-    r.d[i] = load16<XT, NT>(p.dy, row * p.lddy + v * N);
-    r.h[i] = load16<XT, NT>(p.h, row * p.ldh + v * N);
-    if (WITH_B && p.dh) r.b[i] = load16<XT, NT>(p.dh, row * p.lddh + v * N);
+    r.d[i] = load_unit<XT, NT, N>(p.dy, row * p.lddy, v);
+    r.h[i] = load_unit<XT, NT, N>(p.h, row * p.ldh, v);
+    if (WITH_B && p.dh) r.b[i] = load_unit<XT, NT, N>(p.dh, row * p.lddh, v);
   }
 }
 
 template <int XT, int NV, int THREADS, bool PREFETCH, bool NT>
 __global__ __launch_bounds__(THREADS) void norm_grad_kernel(NormGradArgs p) {
-  constexpr int N = kPer16<XT>;
+  constexpr int N = THREADS <= 512 ? kPer16<XT> : 8;
   constexpr bool kKeepGamma = THREADS <= 512;
   __shared__ float part[2][kMaxWaves];
   const int nvec = (int)(p.cols / N);
@@ -249,19 +289,19 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(NormGradArgs p) {
     if (kKeepGamma && v < nvec) decode_gamma<N>(load_gamma<N>(p.gamma, p.g_type, v), p.g_type, g[i]);
   }
   int flip = 0;
-  GradRow<NV> r;
+  GradRow<XT, NV, N> r;
   int64_t row = blockIdx.x;
-  if (PREFETCH && row < p.rows) load_grad_row<XT, NV, NT, PREFETCH>(p, row, nvec, r);
+  if (PREFETCH && row < p.rows) load_grad_row<XT, NV, N, NT, PREFETCH>(p, row, nvec, r);
   for (; row < p.rows; row += gridDim.x, flip ^= 1) {
-    if (!PREFETCH) load_grad_row<XT, NV, NT, PREFETCH>(p, row, nvec, r);
+    if (!PREFETCH) load_grad_row<XT, NV, N, NT, PREFETCH>(p, row, nvec, r);
     float c = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
       if (v >= nvec) continue;
       float d[N], h[N];
-      decode16<XT>(r.d[i], d);
-      decode16<XT>(r.h[i], h);
+      decode_unit<XT, N>(r.d[i], d);
+      decode_unit<XT, N>(r.h[i], h);
       if (!kKeepGamma) decode_gamma<N>(load_gamma<N>(p.gamma, p.g_type, v), p.g_type, g[i]);
 #pragma unroll
       for (int e = 0; e < N; ++e) {
@@ -270,8 +310,8 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(NormGradArgs p) {
         acc[i][e] += dx;
       }
     }
-    GradRow<NV> next;
-    if (PREFETCH && row + gridDim.x < p.rows) load_grad_row<XT, NV, NT, PREFETCH>(p, row + gridDim.x, nvec, next);
+    GradRow<XT, NV, N> next;
+    if (PREFETCH && row + gridDim.x < p.rows) load_grad_row<XT, NV, N, NT, PREFETCH>(p, row + gridDim.x, nvec, next);
     c = block_sum(c, part[flip]) * inv_cols;
     // xh = h * rstd once more (rstd * c could leave fp32's range, xh does
     // not).  Formed from a copy that the compiler takes for another value: kept
@@ -283,18 +323,18 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(NormGradArgs p) {
       const int v = threadIdx.x + i * blockDim.x;
       if (v >= nvec) continue;
       float d[N], h[N], o[N];
-      decode16<XT>(r.d[i], d);
-      decode16<XT>(r.h[i], h);
+      decode_unit<XT, N>(r.d[i], d);
+      decode_unit<XT, N>(r.h[i], h);
       if (!kKeepGamma) decode_gamma<N>(load_gamma<N>(p.gamma, p.g_type, v), p.g_type, g[i]);
 #pragma unroll
       for (int e = 0; e < N; ++e) o[e] = rstd * __builtin_fmaf(-(h[e] * rstd), c, d[e] * g[i][e]);
       if (p.dh) {
         float b[N];
-        decode16<XT>(PREFETCH ? r.b[i] : load16<XT, NT>(p.dh, row * p.lddh + v * N), b);
+        decode_unit<XT, N>(PREFETCH ? r.b[i] : load_unit<XT, NT, N>(p.dh, row * p.lddh, v), b);
 #pragma unroll
         for (int e = 0; e < N; ++e) o[e] += b[e];
       }
-      store16<XT, false>(p.dx, row * p.lddx + v * N, encode16<XT>(o));
+      store_unit<XT, N>(p.dx, row * p.lddx, v, o);
     }
     if (PREFETCH) r = next;
   }
@@ -394,7 +434,7 @@ hipError_t norm_grad_as(const NormGradArgs& a, hipStream_t st) {
   else if (sh.threads <= 512)
     hipLaunchKernelGGL((norm_grad_kernel<XT, 4 * U, 512, false, NT>), grid, block, 0, st, a);
   else
-    hipLaunchKernelGGL((norm_grad_kernel<XT, 4 * U, 1024, false, NT>), grid, block, 0, st, a);
+    hipLaunchKernelGGL((norm_grad_kernel<XT, 4, 1024, false, NT>), grid, block, 0, st, a);
   return hipGetLastError();
 }
 

@@ -260,3 +260,22 @@ def test_rows_of_every_magnitude(cols, dtype, eps):
     if eps == 0:
         z = np.flatnonzero(zero[keep])
         assert np.array_equal(host(dx)[z], dh[keep][z])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("cols", [16392, 20480, 24584, 32768])
+def test_gradient_of_the_widest_rows(cols, dtype):
+    # one workgroup of 1024 threads to a row, the last units part of them only
+    say("norm gradient, %d columns %s" % (cols, dtype))
+    rng = np.random.default_rng(cols)
+    rows = 70
+    h, dy, dh = draw(rng, (rows, cols), dtype, 2.0), draw(rng, (rows, cols), dtype, 0.1, False), draw(rng, (rows, cols), dtype, 0.2)
+    gamma = moe.round_to(1 + 0.2 * rng.standard_normal(cols), False)
+    rstd = (1 / np.sqrt(np.mean(h.astype(np.float64) ** 2, axis=1) + 1e-6)).astype(np.float32)
+    dt = TYPES[dtype]
+    dx, dgamma = T.rmsnorm_backward(dev(dy, dt), dev(h, dt), dev(gamma, torch.float32), dev(rstd, torch.float32), dh=dev(dh, dt))
+    dxo, dgo = moe.rmsnorm_grad(dy, h, gamma, rstd, dh)
+    xh, a = h.astype(np.float64) * rstd[:, None].astype(np.float64), dy.astype(np.float64) * gamma
+    size = rstd[:, None] * (np.abs(a) + np.abs(xh) * np.mean(np.abs(a * xh), axis=1, keepdims=True)) + np.abs(dh)
+    assert np.all(np.abs(host(dx) - dxo) <= 80 * U * size + (UB * np.abs(dxo) if dtype == "bf16" else 0))
+    assert np.all(np.abs(host(dgamma) - dgo) <= (rows / 256 + 96) * U * np.sum(np.abs(dy * xh), axis=0))
