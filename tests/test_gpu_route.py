@@ -329,3 +329,37 @@ def test_long_and_short_calls_agree_bit_for_bit(E, k, groups, top_groups, renorm
     idx, w = T.route(l, k, **kw)
     few = [T.route(l[i:i + 2048], k, **kw) for i in range(0, 16384, 2048)]
     assert torch.equal(idx, torch.cat([f[0] for f in few])) and torch.equal(w, torch.cat([f[1] for f in few]))
+
+
+@pytest.mark.parametrize("E,k,groups,top_groups", [(64, 6, 8, 3), (128, 8, 4, 2), (256, 8, 1, 1), (256, 8, 8, 4), (200, 8, 1, 1)])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [2600, 77])
+def test_rows_by_16_bytes_and_by_elements(E, k, groups, top_groups, score, dtype, rows):
+    # aligned rows are read 16 bytes at a time; rows that start elsewhere, or
+    # a bias that does, element by element: the same results, the oracle's
+    say("route by 16 bytes and elements: %d x %d %s" % (rows, E, dtype))
+    rng = np.random.default_rng(E + rows)
+    l = moe.round_to(rng.standard_normal((rows, E)) * 2, dtype == "bf16")
+    l[::9] = np.round(l[::9])
+    l[4::40, : E // 2] = -np.inf
+    l[6::40, 1] = np.nan
+    bias = (rng.standard_normal(E) * 0.05).astype(np.float32)
+    d, b = dev(l, TYPES[dtype]), dev(bias)
+    kw = dict(score=score, groups=groups, top_groups=top_groups, scale=1.5)
+    idx, w = T.route(d, k, bias=b, **kw)
+    at = np.r_[0:48, rows - 20:rows]
+    with np.errstate(all="ignore"):
+        io, wo = moe.route(l[at], k, bias=bias, **kw)
+    assert np.array_equal(idx.cpu().numpy()[at], io)
+    assert np.all(np.abs(w.cpu().numpy()[at] - wo) <= 70 * U * np.abs(wo) + 1e-37)
+    wide = torch.zeros((rows, E + 9), dtype=d.dtype, device=DEV)
+    far = torch.zeros(E + 1, device=DEV)
+    far[1:] = b
+    for start in (0, 1, 8):       # an odd pitch; and an odd start; an aligned start of rows at an odd pitch
+        wide[:, start:start + E] = d
+        for bb in (b, far[1:]):
+            i2, w2 = T.route(wide[:, start:start + E], k, bias=bb, **kw)
+            assert torch.equal(idx, i2) and torch.equal(w, w2)
+    i2, w2 = T.route(d, k, bias=far[1:], **kw)
+    assert torch.equal(idx, i2) and torch.equal(w, w2)
