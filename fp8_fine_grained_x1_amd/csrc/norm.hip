@@ -14,13 +14,16 @@
 //   reaches h along the residual stream.)
 //
 // Both are bound by HBM: a row's elements are read once and stay in
-// registers, undecoded, between the statistics and the outputs.  Streams
-// that are used next (y, or h where there is no y, and dx) are stored
-// ordinarily and may stay in the caches, the others pass them by; measured on
-// 8192 x 7168 bf16 with every output: 91 us (5.8 TB/s), all ordinary 99.5, all
-// non-temporal 95.5; the gradient 85 + 7 us for dgamma's strips (5.5 TB/s),
-// dx non-temporal 90, dy read ordinarily 93.  A large device copy moves
-// 5.1 TB/s on this card.
+// registers, undecoded, between the statistics and the outputs.  Of the
+// outputs y, or h where there is no y, and dx are stored ordinarily and may
+// stay in the caches for what reads them next, the others pass them by;
+// measured on 8192 x 7168 bf16 with every output: 90 us (5.9 TB/s), all
+// ordinary 99.5, all non-temporal 95.  (q, too, passes them by: ordinary stores
+// of it cost the norm itself 7.8 us instead of 7.3 on 1111 x 5120 f32 and 97
+// instead of 90 here, though a dispatch right after it gains more than that
+// while its rows fit the caches.)  The gradient takes 85 us, 7 of them dgamma's
+// strips (5.5 TB/s); dx non-temporal 90, dy read ordinarily 93.  A large device
+// copy moves 5.1 TB/s on this card.
 #include <float.h>
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -449,8 +452,8 @@ hipError_t norm_grad_t(const NormGradArgs& a, hipStream_t st) {
 // Up to 64 rows each their own strip, then four rows to a strip (a strip's
 // partial sums are written and read again: 512 rows of 7168 bf16 take 13.2 us
 // in 128 strips, 19.6 in 512, 14.9 in 256), two strips per CU at most and four
-// where rows are short (16384 x 1024: 23 us in 1024 strips, 27 in 512, 26 in
-// 2048; 8192 x 7168 in 768 strips 92 us, in 512 90).
+// where rows are short (16384 x 1024: 27 us in 1024 strips, 30 in 512, 29 in
+// 2048; 8192 x 7168 in 768 strips 89 us, in 512 85).
 int64_t norm_grad_strips(int64_t rows, int64_t cols) {
   const int64_t most = cols <= 1024 ? 1024 : 512;
   const int64_t n = rows < 64 ? rows : rows < 256 ? 64 : (rows + 3) / 4;
