@@ -200,11 +200,13 @@ def _native():
 def _call(name, stream, x, inputs, args):
     """The native helper `name` with `args` and a stream's handle, on `stream`
     (see _on_stream) or the current one of x's device."""
-    on_gpu = isinstance(x, torch.Tensor) and x.is_cuda
-    if stream is not None and on_gpu:
+    f = getattr(_native(), name)
+    d = x.get_device() if isinstance(x, torch.Tensor) else -1
+    if d < 0:
+        return f(*args, 0)  # refuses
+    if stream is not None:
         return _on_stream(lambda: _call(name, None, x, inputs, args), stream, x, inputs)
-    # (not on the GPU: the helper refuses)
-    return getattr(_native(), name)(*args, torch._C._cuda_getCurrentRawStream(x.get_device()) if on_gpu else 0)
+    return f(*args, torch._C._cuda_getCurrentRawStream(d))
 
 
 _LAYOUT = {"group_major": True, "row_major": False}
