@@ -278,11 +278,12 @@ __device__ __forceinline__ void load_slots(const T* __restrict__ row, int e0, in
 // the lanes (32-bit keys, by DPP and row swaps), a ballot, and scalar
 // arithmetic for the lowest lane that has it.
 //
-// Bound by instruction issue: about 900 vector instructions a wave, 430 of
-// them the scores.  16384 x 256, 8 of 256 in 4 of 8 groups, f32: 13.3 us with
-// two tokens to a wave (the logits' bytes at a device copy's rate: 3.5); 25.7
-// with one (850 instructions for it alone), 22 with four (16 experts to a
-// lane: too few waves to hide the loads).  5 x 256: 3.8 us.
+// Bound by instruction issue: 790 vector instructions a wave, some 200 of them
+// the scores; the vector units issue in 86% of the busy cycles (counters).
+// 16384 x 256, 8 of 256 in 4 of 8 groups, f32: 13.3 us with two tokens to a wave
+// (the logits' bytes at a device copy's rate: 3.5), softmax 14.4; 25.7 with one,
+// 22 with four (16 experts to a lane: too few waves to hide the loads).
+// 5 x 256: 3.8 us.
 template <int LT, int LANES, int NS, int SCORE>
 __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs p, RouteLayout q) {
   constexpr int kTokens = 64 / LANES;  // of a wave
@@ -562,8 +563,9 @@ __device__ __forceinline__ float exp_below(float l, float top) {
 
 // One wave per token: lane j < k has the j-th chosen expert, and lane i the
 // logits (where the gradient is dense) and gradients i, i + 64, ..  Only the
-// dense form reads a whole row.  Bound by instruction issue: 8191 x 160 bf16,
-// dense: 6.0 us (its bytes at a device copy's rate: 1.1).
+// dense form reads a whole row.  Bound by instruction issue (341 vector
+// instructions a token; 89% of the busy cycles): 8191 x 160 bf16, dense: 6.0 us
+// (its bytes at a device copy's rate: 1.1; a smallest kernel 3.8).
 template <int LT, int NE>
 __global__ __launch_bounds__(64 * kRouteWaves) void route_grad_kernel(RouteGradArgs p) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
