@@ -346,4 +346,22 @@ __device__ __forceinline__ float row16_sum(float v) {
 }
 __device__ __forceinline__ float wave_sum(float v) { return pair_sum<32>(pair_sum<16>(row16_sum(v))); }
 
+// exp(x) for x <= 0 by the hardware's 2^t, t = x log2(e) with the product's
+// rounding error and the constant's made good to first order: within 2 ulp
+// down to 2^-126, 0 below.
+__device__ __forceinline__ float exp_neg(float x) {
+  x = fmaxf(x, -120.0f);
+  const float t = x * 1.44269502f;                                    // RN32(log2 e)
+  const float e = __builtin_fmaf(x, 1.44269502f, -t) + x * 1.92596299e-8f;  // log2 e - RN32(log2 e)
+  const float p = __builtin_amdgcn_exp2f(t);
+  return __builtin_fmaf(p, e * 0.693147181f, p);
+}
+
+// exp(l - top), 0 for a masked logit, 1 at the top (also where both are
+// +inf).
+__device__ __forceinline__ float exp_below(float l, float top) {
+  const float e = exp_neg(l == top ? 0.0f : l - top);
+  return l == -INFINITY ? 0.0f : e;
+}
+
 }  // namespace fp8fg

@@ -33,10 +33,9 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include <utility>
-
 #include "device_common.h"
 #include "launch.h"
+#include "tiles.h"
 
 namespace fp8fg {
 
@@ -45,25 +44,10 @@ namespace {
 constexpr int kQThreads = 256;
 constexpr int kGroupsPerBlock = kQThreads / 16;
 constexpr int kUnroll = 2;
-constexpr int kTPitch = 144;  // LDS row pitch (bytes) of the transposing store
 // 1x128 grid: up to 28 workgroups of 256 threads per CU (for the 4096 x 7168
 // activations exactly one pass of two tiles per lane group); 14 measured 10%
 // slower
 constexpr int k1x128BlocksPerCu = 28;
-
-// n / d for 32-bit n by multiply-high and shift (Granlund & Montgomery,
-// "Division by invariant integers using multiplication", PLDI 1994):
-// with l = ceil(log2 d) and m = floor(2^32 (2^l - d) / d) + 1,
-// n / d = (umulhi(n, m) + n) >> l for every n < 2^32 (the sum is formed in
-// 64 bits).
-struct FastDiv {
-  uint32_t d, m, l;
-};
-
-__device__ __forceinline__ uint32_t fast_div(uint32_t n, const FastDiv& f) {
-  const uint64_t t = (uint64_t)__umulhi(n, f.m) + n;
-  return (uint32_t)(t >> f.l);
-}
 
 // Lane group g of the grid handles tiles g, g + G, ... (G = number of lane
 // groups), two per iteration so that both loads are in flight before either
@@ -75,26 +59,6 @@ __device__ __forceinline__ uint32_t fast_div(uint32_t n, const FastDiv& f) {
 // a wave's four tiles are four consecutive rows of one tile column, whose
 // scales are adjacent; the last band may have fewer rows.  (Scattered
 // 4-byte scale stores cost 20% more written bytes than the output itself.)
-template <int ORDER>
-__device__ __forceinline__ void tile_rc(uint32_t t, const FastDiv& tpr, const FastDiv& band,
-                                        uint32_t rows, uint32_t& r, uint32_t& tc) {
-  if constexpr (ORDER == 0) {
-    r = fast_div(t, tpr);
-    tc = t - r * tpr.d;
-  } else {
-    const uint32_t b = fast_div(t, band);
-    const uint32_t u = t - b * band.d;
-    const uint32_t h = rows - 16u * b;  // rows in this band (16 except in the last)
-    if (h >= 16u) {
-      tc = u >> 4;
-      r = 16u * b + (u & 15u);
-    } else {
-      tc = u / h;
-      r = 16u * b + (u - tc * h);
-    }
-  }
-}
-
 template <int XT, int RULE, int ORDER>
 __global__ __launch_bounds__(kQThreads) void quant_1x128_kernel(
     const void* __restrict__ x, uint32_t ntiles, FastDiv tpr, FastDiv band, uint32_t rows,
@@ -144,85 +108,6 @@ __global__ __launch_bounds__(kQThreads) void quant_1x128_kernel(
 // allowed 5-6; the requantizer's 1792-block grid then fits in one round on
 // 256 CUs.  An f32 input is its own decoded form (64 VGPRs of raw data), so
 // that instantiation keeps the compiler's default register budget.
-template <int XT>
-struct RawRow;
-template <>
-struct RawRow<0> {  // 8 bf16
-  uint4 w;
-};
-template <>
-struct RawRow<1> {  // 8 f32
-  uint4 a, b;
-};
-template <>
-struct RawRow<2> {  // 8 E4M3 bytes
-  uint2 w;
-};
-
-template <int XT>
-__device__ __forceinline__ RawRow<XT> load_raw(const void* __restrict__ x, int64_t off) {
-  RawRow<XT> r;
-  if constexpr (XT == 0) {
-    r.w = ld_nt16(reinterpret_cast<const uint16_t*>(x) + off);
-  } else if constexpr (XT == 1) {
-    const float* p = reinterpret_cast<const float*>(x) + off;
-    r.a = ld_nt16(p);
-    r.b = ld_nt16(p + 4);
-  } else {
-    r.w = ld_nt8(reinterpret_cast<const uint8_t*>(x) + off);
-  }
-  return r;
-}
-
-// Elements J and J + 1 (J even) of a raw row, exactly as fp32.
-template <int J, int XT>
-__device__ __forceinline__ void raw_pair(const RawRow<XT>& r, float& a, float& b) {
-  static_assert(J % 2 == 0 && J < 8, "pairs start at even columns");
-  if constexpr (XT == 0) {
-    const uint32_t w = J == 0 ? r.w.x : J == 2 ? r.w.y : J == 4 ? r.w.z : r.w.w;
-    a = bf16_lo(w);
-    b = bf16_hi(w);
-  } else if constexpr (XT == 1) {
-    const uint4& h = J < 4 ? r.a : r.b;
-    a = __uint_as_float((J & 3) == 0 ? h.x : h.z);
-    b = __uint_as_float((J & 3) == 0 ? h.y : h.w);
-  } else {
-    const auto f = __builtin_amdgcn_cvt_pk_f32_fp8((int)(J < 4 ? r.w.x : r.w.y), (J & 2) != 0);
-    a = f[0];
-    b = f[1];
-  }
-}
-
-// Hides a raw row's registers from the optimizer (no instruction is
-// emitted): the values decoded before this point cannot be reused after it,
-// so the second pass decodes again instead of keeping 64 floats live.
-template <int XT>
-__device__ __forceinline__ void refresh(RawRow<XT>& r) {
-  if constexpr (XT == 0) {
-    asm volatile("" : "+v"(r.w.x), "+v"(r.w.y), "+v"(r.w.z), "+v"(r.w.w));
-  } else if constexpr (XT == 1) {
-    asm volatile("" : "+v"(r.a.x), "+v"(r.a.y), "+v"(r.a.z), "+v"(r.a.w));
-    asm volatile("" : "+v"(r.b.x), "+v"(r.b.y), "+v"(r.b.z), "+v"(r.b.w));
-  } else {
-    asm volatile("" : "+v"(r.w.x), "+v"(r.w.y));
-  }
-}
-
-template <int J>
-struct ColTag {
-  static constexpr int value = J;
-};
-template <typename F, int... P>
-__device__ __forceinline__ void for_pairs_impl(F&& f, std::integer_sequence<int, P...>) {
-  (f(ColTag<2 * P>{}), ...);
-}
-// f(ColTag<0>{}), f(ColTag<2>{}), .. f(ColTag<6>{}): the first column of
-// each pair as a compile-time constant.
-template <typename F>
-__device__ __forceinline__ void for_pairs(F&& f) {
-  for_pairs_impl(f, std::make_integer_sequence<int, 4>{});
-}
-
 template <int XT, int RULE, bool PER_COLUMN, bool TRANSPOSE>
 __global__ __launch_bounds__(kQThreads, XT == 1 ? 1 : 8) void quant_tile128_kernel(
     const void* __restrict__ x, int64_t ldx, const float* __restrict__ xs, int64_t xs_rs,
@@ -358,13 +243,6 @@ __global__ __launch_bounds__(kQThreads, XT == 1 ? 1 : 8) void quant_tile128_kern
       st_nt8(q + (r0 + rg * 8 + i) * ldq + c0 + cg * 8, out);
     }
   }
-}
-
-FastDiv make_fast_div(uint32_t d) {
-  uint32_t l = 0;
-  while (l < 32 && (1ull << l) < d) ++l;
-  const uint64_t m = ((1ull << 32) * ((1ull << l) - d)) / d + 1;
-  return FastDiv{d, (uint32_t)m, l};
 }
 
 template <int XT, int RULE>

@@ -543,24 +543,6 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_any_kernel(RouteArgs p
   }
 }
 
-// exp(x) for x <= 0 by the hardware's 2^t, t = x log2(e) with the product's
-// rounding error and the constant's made good to first order: within 2 ulp
-// down to 2^-126, 0 below.
-__device__ __forceinline__ float exp_neg(float x) {
-  x = fmaxf(x, -120.0f);
-  const float t = x * 1.44269502f;                                    // RN32(log2 e)
-  const float e = __builtin_fmaf(x, 1.44269502f, -t) + x * 1.92596299e-8f;  // log2 e - RN32(log2 e)
-  const float p = __builtin_amdgcn_exp2f(t);
-  return __builtin_fmaf(p, e * 0.693147181f, p);
-}
-
-// exp(l - top), 0 for a masked logit, 1 at the top (also where both are
-// +inf).
-__device__ __forceinline__ float exp_below(float l, float top) {
-  const float e = exp_neg(l == top ? 0.0f : l - top);
-  return l == -INFINITY ? 0.0f : e;
-}
-
 // One wave per token: lane j < k has the j-th chosen expert, and lane i the
 // logits (where the gradient is dense) and gradients i, i + 64, ..  Only the
 // dense form reads a whole row.  Bound by instruction issue (341 vector
