@@ -33,7 +33,11 @@ EXPORTED = ("fp8_quantize_rowtile", "fp8_quantize_block", "fp8_gemm_blockscaled"
             "fp8_grouped_gemm_blockscaled", "fp8_rmsnorm_quantize",
             "fp8_rmsnorm_backward_workspace", "fp8_rmsnorm_backward", "fp8_route",
             "fp8_route_backward", "fp8_dispatch_workspace", "fp8_dispatch", "fp8_combine",
-            "fp8_combine_backward", "fp8fg_status_string")
+            "fp8_combine_backward", "fp8_swiglu_quantize", "fp8_swiglu_backward",
+            "fp8_swiglu_backward_128x1", "fp8_balance_loss_workspace", "fp8_balance_loss",
+            "fp8_balance_loss_backward", "fp8_rmsnorm_block_quantize",
+            "fp8_rmsnorm_block_backward_workspace", "fp8_rmsnorm_block_backward",
+            "fp8fg_status_string")
 
 
 class Fp8fgError(RuntimeError):
@@ -66,12 +70,25 @@ _SIGS = {
                      _L, _P, _L, _P],
     "fp8_combine": [_P, _I, _L, _L, _L, _L, _L, _P, _P, _L, _P, _L, _P, _L, _P],
     "fp8_combine_backward": [_P, _I, _L, _L, _L, _L, _L, _P, _L, _P, _P, _L, _P, _L, _P, _L, _P],
+    "fp8_swiglu_quantize": [_P, _I, _L, _L, _L, _P, _I, _P, _L, _P, _L, _L, _P, _L, _P, _L, _L, _P],
+    "fp8_swiglu_backward": [_P, _I, _L, _L, _L, _P, _L, _P, _L, _L, _P, _I, _P, _L, _P, _L, _L, _P,
+                            _L, _P, _L, _P],
+    "fp8_swiglu_backward_128x1": [_P, _I, _L, _L, _L, _P, _L, _P, _L, _L, _I, _P, _L, _P, _L, _L,
+                                  _P, _L, _P, _L, _L, _P, _L, _P, _L, _L, _P],
+    "fp8_balance_loss": [_P, _I, _L, _L, _L, _P, _L, _L, _P, _L, _I, _F, _P, _P, _P, _P, _L, _P],
+    "fp8_balance_loss_backward": [_P, _P, _I, _L, _L, _L, _P, _P, _L, _I, _P, _L, _P, _L, _P],
+    "fp8_rmsnorm_block_quantize": [_P, _I, _L, _L, _L, _P, _L, _P, _P, _I, _P, _L, _F, _F, _F, _I,
+                                   _P, _L, _P, _L, _P, _L, _P, _L, _L, _P, _P, _P],
+    "fp8_rmsnorm_block_backward": [_P, _I, _L, _L, _L, _P, _L, _P, _L, _P, _L, _P, _P, _I, _P, _L,
+                                   _P, _P, _F, _F, _P, _L, _P, _L, _P, _P, _P, _L, _P, _L, _P],
 }
 
 # functions that return a size in bytes instead of a status
 _SIZES = {
     "fp8_rmsnorm_backward_workspace": [_L, _L],
     "fp8_dispatch_workspace": [_L, _L, _L],
+    "fp8_balance_loss_workspace": [_L, _L, _L],
+    "fp8_rmsnorm_block_backward_workspace": [_L, _L],
 }
 
 
@@ -235,3 +252,74 @@ def fp8_combine_backward(dy, type, z_rows, tokens, k, cols, lddy, z, ldz, pos, w
     return _call("fp8_combine_backward", check, (dy, z, pos, w, dz, dw), lambda dev: (
         _ptr(dy), type, z_rows, tokens, k, cols, lddy, _ptr(z), ldz, _ptr(pos), _ptr(w), ldw,
         _ptr(dz), lddz, _ptr(dw), lddw, _stream(stream, dev)))
+
+
+def fp8_swiglu_quantize(u, u_type, rows, inner, ldu, used, scale_rule, q, ldq, s, s_rs, s_ts, uq, lduq,
+                        us, us_rs, us_ts, stream=None, check=True):
+    return _call("fp8_swiglu_quantize", check, (u, used, q, s, uq, us), lambda dev: (
+        _ptr(u), u_type, rows, inner, ldu, _ptr(used), scale_rule, _ptr(q), ldq, _ptr(s), s_rs, s_ts,
+        _ptr(uq), lduq, _ptr(us), us_rs, us_ts, _stream(stream, dev)))
+
+
+def fp8_swiglu_backward(da, type, rows, inner, ldda, uq, lduq, us, us_rs, us_ts, used, scale_rule, dq,
+                        lddq, ds, ds_rs, ds_ts, du, lddu, a, lda, stream=None, check=True):
+    return _call("fp8_swiglu_backward", check, (da, uq, us, used, dq, ds, du, a), lambda dev: (
+        _ptr(da), type, rows, inner, ldda, _ptr(uq), lduq, _ptr(us), us_rs, us_ts, _ptr(used),
+        scale_rule, _ptr(dq), lddq, _ptr(ds), ds_rs, ds_ts, _ptr(du), lddu, _ptr(a), lda,
+        _stream(stream, dev)))
+
+
+def fp8_swiglu_backward_128x1(da, type, rows, inner, ldda, uq, lduq, us, us_rs, us_ts, scale_rule, dq,
+                              lddq, ds, ds_rs, ds_ts, dqt, lddqt, dst, dst_rs, dst_ts, aqt, ldaqt, ast,
+                              ast_rs, ast_ts, stream=None, check=True):
+    return _call("fp8_swiglu_backward_128x1", check, (da, uq, us, dq, ds, dqt, dst, aqt, ast), lambda dev: (
+        _ptr(da), type, rows, inner, ldda, _ptr(uq), lduq, _ptr(us), us_rs, us_ts, scale_rule, _ptr(dq),
+        lddq, _ptr(ds), ds_rs, ds_ts, _ptr(dqt), lddqt, _ptr(dst), dst_rs, dst_ts, _ptr(aqt), ldaqt,
+        _ptr(ast), ast_rs, ast_ts, _stream(stream, dev)))
+
+
+def fp8_balance_loss_workspace(rows, experts, seqs):
+    return lib().fp8_balance_loss_workspace(rows, experts, seqs)
+
+
+def fp8_balance_loss(logits, l_type, rows, experts, ldl, idx, ld_idx, k, offsets, seqs, score, scale,
+                     loss, counts, slope, workspace, workspace_bytes, stream=None, check=True):
+    return _call("fp8_balance_loss", check, (logits, idx, offsets, loss, counts, slope, workspace), lambda dev: (
+        _ptr(logits), l_type, rows, experts, ldl, _ptr(idx), ld_idx, k, _ptr(offsets), seqs, score, scale,
+        _ptr(loss), _ptr(counts), _ptr(slope), _ptr(workspace), workspace_bytes, _stream(stream, dev)))
+
+
+def fp8_balance_loss_backward(dloss, logits, l_type, rows, experts, ldl, slope, offsets, seqs, score,
+                              base, ldb, dlogits, lddl, stream=None, check=True):
+    return _call("fp8_balance_loss_backward", check, (dloss, logits, slope, offsets, base, dlogits), lambda dev: (
+        _ptr(dloss), _ptr(logits), l_type, rows, experts, ldl, _ptr(slope), _ptr(offsets), seqs, score,
+        _ptr(base), ldb, _ptr(dlogits), lddl, _stream(stream, dev)))
+
+
+def fp8_rmsnorm_block_quantize(z, x_type, rows, cols, ldz, r, ldr, gamma_post, gamma, g_type, gate, ldg,
+                               residual_scale, block_scale, eps, scale_rule, h, ldh, y, ldy, q, ldq, s,
+                               s_rs, s_ts, rstd_post, rstd, stream=None, check=True):
+    return _call("fp8_rmsnorm_block_quantize", check,
+                 (z, r, gamma_post, gamma, gate, h, y, q, s, rstd_post, rstd), lambda dev: (
+                     _ptr(z), x_type, rows, cols, ldz, _ptr(r), ldr, _ptr(gamma_post), _ptr(gamma), g_type,
+                     _ptr(gate), ldg, residual_scale, block_scale, eps, scale_rule, _ptr(h), ldh, _ptr(y),
+                     ldy, _ptr(q), ldq, _ptr(s), s_rs, s_ts, _ptr(rstd_post), _ptr(rstd),
+                     _stream(stream, dev)))
+
+
+def fp8_rmsnorm_block_backward_workspace(rows, cols):
+    return lib().fp8_rmsnorm_block_backward_workspace(rows, cols)
+
+
+def fp8_rmsnorm_block_backward(dy, x_type, rows, cols, lddy, dh, lddh, z, ldz, h, ldh, gamma_post, gamma,
+                               g_type, gate, ldg, rstd_post, rstd, residual_scale, block_scale, dz, lddz,
+                               dr, lddr, dgamma_post, dgamma, dgate, lddg, workspace, workspace_bytes,
+                               stream=None, check=True):
+    return _call("fp8_rmsnorm_block_backward", check,
+                 (dy, dh, z, h, gamma_post, gamma, gate, rstd_post, rstd, dz, dr, dgamma_post, dgamma, dgate,
+                  workspace), lambda dev: (
+                     _ptr(dy), x_type, rows, cols, lddy, _ptr(dh), lddh, _ptr(z), ldz, _ptr(h), ldh,
+                     _ptr(gamma_post), _ptr(gamma), g_type, _ptr(gate), ldg, _ptr(rstd_post), _ptr(rstd),
+                     residual_scale, block_scale, _ptr(dz), lddz, _ptr(dr), lddr, _ptr(dgamma_post),
+                     _ptr(dgamma), _ptr(dgate), lddg, _ptr(workspace), workspace_bytes,
+                     _stream(stream, dev)))

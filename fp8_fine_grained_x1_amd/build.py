@@ -29,7 +29,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfp8fg.so")
 NATIVE = os.path.join(PKG, "_native.so")
 
-SOURCES = ["abi.cpp", "quant.hip", "gemm.hip", "norm.hip", "route.hip", "dispatch.hip"]
+SOURCES = ["abi.cpp", "quant.hip", "gemm.hip", "norm.hip", "route.hip", "dispatch.hip", "gate.hip", "balance.hip",
+           "block_norm.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -141,6 +141,17 @@ int check_route(int l_type, int64_t rows, int64_t experts, int64_t ldl, int scor
   return FP8FG_OK;
 }
 
+// Sizes of the silu gate's calls: the status of their common arguments.
+int check_gate(int type, int64_t rows, int64_t inner, int scale_rule) {
+  if (!is_xtype(type)) return FP8FG_EINVAL;
+  if (scale_rule != FP8FG_SCALE_AMAX && scale_rule != FP8FG_SCALE_POW2) return FP8FG_EINVAL;
+  if (rows < 0 || inner < 0) return FP8FG_EINVAL;
+  return inner % 128 ? FP8FG_ESHAPE : FP8FG_OK;
+}
+bool gate_fits(int64_t rows, int64_t inner) {
+  return rows <= kMaxI32 && inner <= ((int64_t)1 << 27) && rows * (inner / 128) <= (int64_t)1 << 31;
+}
+
 // The last row's code, -2 - (tokens * k - 1), has to fit an int32 too.
 bool dispatch_fits(int64_t tokens, int64_t k, int64_t experts) {
   return k <= kMaxI32 && tokens <= (kMaxI32 - 2) / k && experts <= fp8fg::kRouteMaxExperts;
@@ -452,6 +463,204 @@ int fp8_combine_backward(const void* dy, int type, int64_t z_rows, int64_t token
     return FP8FG_EUNSUPPORTED;
   const fp8fg::CombineGradArgs a{dy, type, z_rows, tokens, (int)k, cols, lddy, z, ldz, pos, w, ldw, dz, lddz, dw, lddw};
   return launched(fp8fg::launch_combine_grad(a, reinterpret_cast<hipStream_t>(stream)));
+}
+
+int fp8_swiglu_quantize(const void* u, int u_type, int64_t rows, int64_t inner, int64_t ldu,
+                        const int32_t* used, int scale_rule, uint8_t* q, int64_t ldq, float* s,
+                        int64_t s_rs, int64_t s_ts, uint8_t* uq, int64_t lduq, float* us,
+                        int64_t us_rs, int64_t us_ts, void* stream) {
+  const int sizes = check_gate(u_type, rows, inner, scale_rule);
+  if (sizes != FP8FG_OK) return sizes;
+  if (negative({ldu, ldq, s_rs, s_ts, lduq, us_rs, us_ts})) return FP8FG_EINVAL;
+  if (rows == 0 || inner == 0) return FP8FG_OK;
+  if (!s || (uq && !us)) return FP8FG_EINVAL;
+  if (inner > kMaxPitch) return FP8FG_EUNSUPPORTED;
+  const int rc = first_of(check_rows(u, true, ldu, 2 * inner, elem_size(u_type)), check_rows(q, true, ldq, inner, 1),
+                          check_rows(uq, false, lduq, 2 * inner, 1));
+  if (rc != FP8FG_OK) return rc;
+  if (!aligned(s, 4) || !aligned(us, 4) || !aligned(used, 4)) return FP8FG_EALIGN;
+  if (!gate_fits(rows, inner) || beyond(kMaxPitch, {ldu, ldq, s_rs, lduq, us_rs}) || beyond(kMaxI32, {s_ts, us_ts}))
+    return FP8FG_EUNSUPPORTED;
+  const fp8fg::GateArgs a{u, u_type, rows, inner, ldu, used, scale_rule, q, ldq, s, s_rs, s_ts, uq, lduq, us, us_rs, us_ts};
+  return launched(fp8fg::launch_gate(a, reinterpret_cast<hipStream_t>(stream)));
+}
+
+int fp8_swiglu_backward(const void* da, int type, int64_t rows, int64_t inner, int64_t ldda,
+                        const uint8_t* uq, int64_t lduq, const float* us, int64_t us_rs,
+                        int64_t us_ts, const int32_t* used, int scale_rule, uint8_t* dq,
+                        int64_t lddq, float* ds, int64_t ds_rs, int64_t ds_ts, void* du,
+                        int64_t lddu, void* a, int64_t lda, void* stream) {
+  const int sizes = check_gate(type, rows, inner, scale_rule);
+  if (sizes != FP8FG_OK) return sizes;
+  if (negative({ldda, lduq, us_rs, us_ts, lddq, ds_rs, ds_ts, lddu, lda})) return FP8FG_EINVAL;
+  if (rows == 0 || inner == 0) return FP8FG_OK;
+  if (!us || (dq && !ds) || (!dq && !du && !a)) return FP8FG_EINVAL;
+  if (inner > kMaxPitch) return FP8FG_EUNSUPPORTED;
+  const int size = elem_size(type);
+  const int rc = first_of(check_rows(da, true, ldda, inner, size), check_rows(uq, true, lduq, 2 * inner, 1),
+                          check_rows(dq, false, lddq, 2 * inner, 1), check_rows(du, false, lddu, 2 * inner, size),
+                          check_rows(a, false, lda, inner, size));
+  if (rc != FP8FG_OK) return rc;
+  if (!aligned(us, 4) || !aligned(ds, 4) || !aligned(used, 4)) return FP8FG_EALIGN;
+  if (!gate_fits(rows, inner) || beyond(kMaxPitch, {ldda, lduq, us_rs, lddq, ds_rs, lddu, lda}) ||
+      beyond(kMaxI32, {us_ts, ds_ts}))
+    return FP8FG_EUNSUPPORTED;
+  const fp8fg::GateGradArgs g{da, type, rows, inner, ldda, uq, lduq, us, us_rs, us_ts, used, scale_rule,
+                              dq, lddq, ds, ds_rs, ds_ts, du, lddu, a, lda};
+  return launched(fp8fg::launch_gate_grad(g, reinterpret_cast<hipStream_t>(stream)));
+}
+
+int fp8_swiglu_backward_128x1(const void* da, int type, int64_t rows, int64_t inner, int64_t ldda,
+                              const uint8_t* uq, int64_t lduq, const float* us, int64_t us_rs,
+                              int64_t us_ts, int scale_rule, uint8_t* dq, int64_t lddq, float* ds,
+                              int64_t ds_rs, int64_t ds_ts, uint8_t* dqt, int64_t lddqt, float* dst,
+                              int64_t dst_rs, int64_t dst_ts, uint8_t* aqt, int64_t ldaqt, float* ast,
+                              int64_t ast_rs, int64_t ast_ts, void* stream) {
+  const int sizes = check_gate(type, rows, inner, scale_rule);
+  if (sizes != FP8FG_OK) return sizes;
+  if (negative({ldda, lduq, us_rs, us_ts, lddq, ds_rs, ds_ts, lddqt, dst_rs, dst_ts, ldaqt, ast_rs, ast_ts}))
+    return FP8FG_EINVAL;
+  if (rows % 128) return FP8FG_ESHAPE;
+  if (rows == 0 || inner == 0) return FP8FG_OK;
+  if (!us || !ds || !dst || !ast) return FP8FG_EINVAL;
+  if (inner > kMaxPitch) return FP8FG_EUNSUPPORTED;
+  const int rc = first_of(check_rows(da, true, ldda, inner, elem_size(type)), check_rows(uq, true, lduq, 2 * inner, 1),
+                          check_rows(dq, true, lddq, 2 * inner, 1), check_rows(dqt, true, lddqt, rows, 1),
+                          check_rows(aqt, true, ldaqt, rows, 1));
+  if (rc != FP8FG_OK) return rc;
+  if (!aligned(us, 4) || !aligned(ds, 4) || !aligned(dst, 4) || !aligned(ast, 4)) return FP8FG_EALIGN;
+  if (!gate_fits(rows, inner) || rows / 128 > kMaxGridY ||
+      beyond(kMaxPitch, {ldda, lduq, us_rs, lddq, ds_rs, lddqt, dst_rs, ldaqt, ast_rs}) ||
+      beyond(kMaxI32, {us_ts, ds_ts, dst_ts, ast_ts}))
+    return FP8FG_EUNSUPPORTED;
+  const fp8fg::GateGradTileArgs g{da, type, rows, inner, ldda, uq, lduq, us, us_rs, us_ts, scale_rule, dq, lddq, ds,
+                                  ds_rs, ds_ts, dqt, lddqt, dst, dst_rs, dst_ts, aqt, ldaqt, ast, ast_rs, ast_ts};
+  return launched(fp8fg::launch_gate_grad_tile(g, reinterpret_cast<hipStream_t>(stream)));
+}
+
+int64_t fp8_balance_loss_workspace(int64_t rows, int64_t experts, int64_t seqs) {
+  if (rows < 0 || rows > kMaxI32 || experts < 1 || experts > fp8fg::kRouteMaxExperts || seqs < 0 || seqs > kMaxI32) return 0;
+  return fp8fg::balance_workspace(rows, experts, seqs);
+}
+
+int fp8_balance_loss(const void* logits, int l_type, int64_t rows, int64_t experts, int64_t ldl,
+                     const int32_t* idx, int64_t ld_idx, int64_t k, const int32_t* offsets,
+                     int64_t seqs, int score, float scale, float* loss, int32_t* counts,
+                     float* slope, void* workspace, int64_t workspace_bytes, void* stream) {
+  const int rc = check_route(l_type, rows, experts, ldl, score, k, 0, scale);
+  if (rc != FP8FG_OK) return rc;
+  if (negative({ld_idx, seqs, workspace_bytes}) || (!offsets && seqs != 1)) return FP8FG_EINVAL;
+  if (ld_idx < k) return FP8FG_ESHAPE;
+  if (seqs == 0) return FP8FG_OK;
+  if (!loss || !counts || !slope || !workspace || (rows > 0 && (!logits || !idx))) return FP8FG_EINVAL;
+  if (!aligned(logits, elem_size(l_type)) || !aligned(idx, 4) || !aligned(offsets, 4) || !aligned(loss, 4) ||
+      !aligned(counts, 4) || !aligned(slope, 4) || !aligned(workspace, 16))
+    return FP8FG_EALIGN;
+  if (experts > fp8fg::kRouteMaxExperts || k > fp8fg::kRouteMaxK || beyond(kMaxI32, {rows, seqs}) ||
+      beyond(kMaxPitch, {ldl, ld_idx}))
+    return FP8FG_EUNSUPPORTED;
+  if (workspace_bytes < fp8_balance_loss_workspace(rows, experts, seqs)) return FP8FG_ESHAPE;
+  const fp8fg::BalanceArgs a{logits, l_type, rows, (int)experts, ldl, idx, ld_idx, (int)k, offsets, seqs, score, scale,
+                             loss, counts, slope, workspace};
+  return launched(fp8fg::launch_balance(a, reinterpret_cast<hipStream_t>(stream)));
+}
+
+int fp8_balance_loss_backward(const float* dloss, const void* logits, int l_type, int64_t rows,
+                              int64_t experts, int64_t ldl, const float* slope, const int32_t* offsets,
+                              int64_t seqs, int score, const void* base, int64_t ldb, void* dlogits,
+                              int64_t lddl, void* stream) {
+  const int rc = check_route(l_type, rows, experts, ldl, score, 1, 0, 1.0f);
+  if (rc != FP8FG_OK) return rc;
+  if (negative({seqs, ldb, lddl}) || (!offsets && seqs != 1)) return FP8FG_EINVAL;
+  if (lddl < experts || (base && ldb < experts)) return FP8FG_ESHAPE;
+  if (rows == 0) return FP8FG_OK;
+  if (!logits || !dlogits || (seqs > 0 && !slope)) return FP8FG_EINVAL;
+  const int size = elem_size(l_type);
+  if (!aligned(logits, size) || !aligned(base, size) || !aligned(dlogits, size) || !aligned(dloss, 4) ||
+      !aligned(slope, 4) || !aligned(offsets, 4))
+    return FP8FG_EALIGN;
+  if (experts > fp8fg::kRouteMaxExperts || beyond(kMaxI32, {rows, seqs}) || beyond(kMaxPitch, {ldl, ldb, lddl}))
+    return FP8FG_EUNSUPPORTED;
+  const fp8fg::BalanceGradArgs a{dloss, logits, l_type, rows, (int)experts, ldl, slope, offsets, seqs, score,
+                                 base, ldb, dlogits, lddl};
+  return launched(fp8fg::launch_balance_grad(a, reinterpret_cast<hipStream_t>(stream)));
+}
+
+int fp8_rmsnorm_block_quantize(const void* z, int x_type, int64_t rows, int64_t cols, int64_t ldz,
+                               const void* r, int64_t ldr, const void* gamma_post, const void* gamma,
+                               int g_type, const void* gate, int64_t ldg, float residual_scale,
+                               float block_scale, float eps, int scale_rule, void* h, int64_t ldh,
+                               void* y, int64_t ldy, uint8_t* q, int64_t ldq, float* s, int64_t s_rs,
+                               int64_t s_ts, float* rstd_post, float* rstd, void* stream) {
+  if (!is_xtype(x_type) || !is_xtype(g_type)) return FP8FG_EINVAL;
+  if (scale_rule != FP8FG_SCALE_AMAX && scale_rule != FP8FG_SCALE_POW2) return FP8FG_EINVAL;
+  if (negative({rows, cols, ldz, ldr, ldg, ldh, ldy, ldq, s_rs, s_ts})) return FP8FG_EINVAL;
+  if (!(eps >= 0.0f) || !std::isfinite(eps) || !std::isfinite(residual_scale) || !std::isfinite(block_scale))
+    return FP8FG_EINVAL;
+  if (cols % 128) return FP8FG_ESHAPE;
+  if (rows == 0 || cols == 0) return FP8FG_OK;
+  if (!gamma_post || !gamma || (q && !s)) return FP8FG_EINVAL;
+  const int size = elem_size(x_type);
+  const bool row_gate = gate && ldg > 0;
+  const int rc = first_of(check_rows(z, true, ldz, cols, size), check_rows(r, true, ldr, cols, size),
+                          check_rows(row_gate ? gate : nullptr, false, ldg, cols, size),
+                          check_rows(h, true, ldh, cols, size), check_rows(y, false, ldy, cols, size),
+                          check_rows(q, false, ldq, cols, 1));
+  if (rc != FP8FG_OK) return rc;
+  if (!aligned(gamma_post, 16) || !aligned(gamma, 16) || !aligned(gate, 16) || !aligned(s, 4) || !aligned(rstd_post, 4) ||
+      !aligned(rstd, 4))
+    return FP8FG_EALIGN;
+  if (cols > fp8fg::kBlockNormMaxCols || rows > kMaxI32 || beyond(kMaxPitch, {ldz, ldr, ldg, ldh, ldy, ldq, s_rs}) ||
+      s_ts > kMaxI32)
+    return FP8FG_EUNSUPPORTED;
+  const fp8fg::BlockNormArgs a{z, x_type, rows, cols, ldz, r, ldr, gamma_post, gamma, g_type, gate, ldg,
+                               residual_scale, block_scale, eps, scale_rule, h, ldh, y, ldy, q, ldq, s, s_rs, s_ts,
+                               rstd_post, rstd};
+  return launched(fp8fg::launch_block_norm(a, reinterpret_cast<hipStream_t>(stream)));
+}
+
+int64_t fp8_rmsnorm_block_backward_workspace(int64_t rows, int64_t cols) {
+  if (rows < 0 || rows > kMaxI32 || cols < 0 || cols % 8 || cols > fp8fg::kBlockNormMaxCols) return 0;
+  return 2 * fp8fg::block_norm_strips(rows, cols) * cols * (int64_t)sizeof(float);
+}
+
+int fp8_rmsnorm_block_backward(const void* dy, int x_type, int64_t rows, int64_t cols, int64_t lddy,
+                               const void* dh, int64_t lddh, const void* z, int64_t ldz, const void* h,
+                               int64_t ldh, const void* gamma_post, const void* gamma, int g_type,
+                               const void* gate, int64_t ldg, const float* rstd_post, const float* rstd,
+                               float residual_scale, float block_scale, void* dz, int64_t lddz, void* dr,
+                               int64_t lddr, float* dgamma_post, float* dgamma, void* dgate, int64_t lddg,
+                               void* workspace, int64_t workspace_bytes, void* stream) {
+  if (!is_xtype(x_type) || !is_xtype(g_type)) return FP8FG_EINVAL;
+  if (negative({rows, cols, lddy, lddh, ldz, ldh, ldg, lddz, lddr, lddg, workspace_bytes})) return FP8FG_EINVAL;
+  if (!std::isfinite(residual_scale) || !std::isfinite(block_scale)) return FP8FG_EINVAL;
+  if (cols % 8) return FP8FG_ESHAPE;
+  if (cols == 0) return FP8FG_OK;
+  const bool col_gate = gate && ldg == 0, row_gate = gate && ldg > 0;
+  if (!dgamma_post || !dgamma || (col_gate && !dgate) || (row_gate && rows > 0 && !dgate)) return FP8FG_EINVAL;
+  if (!aligned(dgamma_post, 4) || !aligned(dgamma, 4) || (col_gate && !aligned(dgate, 4))) return FP8FG_EALIGN;
+  if (rows > 0) {
+    if (!rstd_post || !rstd || !workspace) return FP8FG_EINVAL;
+    const int size = elem_size(x_type);
+    const int rc = first_of(check_rows(dy, true, lddy, cols, size), check_rows(dh, false, lddh, cols, size),
+                            check_rows(z, true, ldz, cols, size), check_rows(h, true, ldh, cols, size),
+                            check_rows(row_gate ? gate : nullptr, false, ldg, cols, size),
+                            check_rows(dz, true, lddz, cols, size), check_rows(dr, true, lddr, cols, size),
+                            check_rows(row_gate ? dgate : nullptr, false, lddg, cols, size));
+    if (rc != FP8FG_OK) return rc;
+    if (!aligned(rstd_post, 4) || !aligned(rstd, 4) || !aligned(workspace, 16)) return FP8FG_EALIGN;
+  }
+  // (read also for rows == 0 where a column gate's gradient is formed)
+  if ((rows > 0 || col_gate) && (!gamma_post || !gamma)) return FP8FG_EINVAL;
+  if (!aligned(gamma_post, 16) || !aligned(gamma, 16) || !aligned(gate, 16)) return FP8FG_EALIGN;
+  if (cols > fp8fg::kBlockNormMaxCols || rows > kMaxI32 ||
+      beyond(kMaxPitch, {lddy, lddh, ldz, ldh, ldg, lddz, lddr, lddg}))
+    return FP8FG_EUNSUPPORTED;
+  if (workspace_bytes < fp8_rmsnorm_block_backward_workspace(rows, cols)) return FP8FG_ESHAPE;
+  const fp8fg::BlockNormGradArgs a{dy, x_type, rows, cols, lddy, dh, lddh, z, ldz, h, ldh, gamma_post, gamma, g_type,
+                                   gate, ldg, rstd_post, rstd, residual_scale, block_scale, dz, lddz, dr, lddr,
+                                   dgamma_post, dgamma, dgate, lddg, reinterpret_cast<float*>(workspace)};
+  return launched(fp8fg::launch_block_norm_grad(a, reinterpret_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,548 @@
+// Balance loss of a router over sequences of tokens, with the experts'
+// counts, and its gradient, for gfx950.
+//
+// Of a token t, share[t][i] = s_i / sum_j s_j with s the softmax or the
+// sigmoid of its logits; masked experts (-inf, NaN) have none, and a token
+// with nothing else is not counted.  Over the n counted tokens of a sequence
+//   count[i] = entries of idx that name i,
+//   slope[i] = scale E / (k n^2) count[i],   loss = sum_i slope[i] sum_t share[t][i]
+// (E / (k n) count is the load of an expert relative to an even one, the mean
+// of the shares its probability).  slope is also the loss's derivative by every
+// share, so that the gradient needs nothing else:
+//   c = dloss slope,  m = sum_i c_i share_i
+//   softmax: dl_j = share_j (c_j - m),  sigmoid: dl_j = share_j (1 - s_j) (c_j - m)
+// A sigmoid's share is formed from exp(l - m'), m' = min(max l, 0), in place
+// of s, so that scores that underflow keep their ratios.
+//
+// The tokens are cut into chunks, and the chunks by the sequences that they
+// meet into pieces: the piece of chunk c and sequence s has the number c + s,
+// which no other piece has, since along the tokens every step raises c or s.  Each
+// piece has one partial sum, and a sequence's are added in their order: no
+// result depends on the order in which workgroups run.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "device_common.h"
+#include "launch.h"
+#include "tiles.h"
+
+namespace fp8fg {
+
+namespace {
+
+constexpr int kPartThreads = 512;
+constexpr int kPartWaves = kPartThreads / 64;
+constexpr int kMaxE = kRouteMaxExperts;
+
+// ------------------------------------------------------------- one token
+// LPT lanes hold a token's experts, NE each: 4 consecutive ones at a time
+// (VEC), or every LPT-th.
+template <int LPT, bool VEC>
+__device__ __forceinline__ int expert_of(int lane, int i) {
+  return VEC ? 4 * (lane + LPT * (i >> 2)) + (i & 3) : lane + LPT * i;
+}
+
+template <int LT, int LPT, int NE, bool VEC>
+__device__ __forceinline__ void load_token(const void* __restrict__ p, int64_t at, int lane, int E, float (&y)[NE]) {
+  if constexpr (VEC) {
+#pragma unroll
+    for (int i = 0; i < NE; i += 4) {
+      const int e = expert_of<LPT, true>(lane, i);
+      if (e < E) {
+        if constexpr (LT == 0) {
+          const uint2 w = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(p) + at + e);
+          y[i] = bf16_lo(w.x);
+          y[i + 1] = bf16_hi(w.x);
+          y[i + 2] = bf16_lo(w.y);
+          y[i + 3] = bf16_hi(w.y);
+        } else {
+          const float4 w = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + at + e);
+          y[i] = w.x;
+          y[i + 1] = w.y;
+          y[i + 2] = w.z;
+          y[i + 3] = w.w;
+        }
+      } else {
+        y[i] = y[i + 1] = y[i + 2] = y[i + 3] = -INFINITY;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+      const int e = expert_of<LPT, false>(lane, i);
+      y[i] = -INFINITY;
+      if (e < E)
+        y[i] = LT == 0 ? __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(p)[at + e] << 16)
+                       : reinterpret_cast<const float*>(p)[at + e];
+    }
+  }
+}
+
+template <int LT, int LPT, int NE, bool VEC>
+__device__ __forceinline__ void store_token(void* __restrict__ p, int64_t at, int lane, int E, const float (&y)[NE]) {
+#pragma unroll
+  for (int i = 0; i < NE; i += VEC ? 4 : 1) {
+    const int e = expert_of<LPT, VEC>(lane, i);
+    if (e >= E) continue;
+    if constexpr (VEC) {
+      if constexpr (LT == 0)
+        *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p) + at + e) =
+            make_uint2(pack2_bf16(y[i], y[i + 1]), pack2_bf16(y[i + 2], y[i + 3]));
+      else
+        *reinterpret_cast<float4*>(reinterpret_cast<float*>(p) + at + e) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+    } else if constexpr (LT == 0) {
+      reinterpret_cast<uint16_t*>(p)[at + e] = (uint16_t)pack2_bf16(y[i], 0.0f);
+    } else {
+      reinterpret_cast<float*>(p)[at + e] = y[i];
+    }
+  }
+}
+
+// Sum and maximum over a token's lanes.
+template <int LPT>
+__device__ __forceinline__ float token_sum(float v) {
+  v = row16_sum(v);
+  if constexpr (LPT >= 32) v = pair_sum<16>(v);
+  if constexpr (LPT >= 64) v = pair_sum<32>(v);
+  return v;
+}
+template <int LPT>
+__device__ __forceinline__ float token_max(float v) {
+  v = row16_max(v);
+  if constexpr (LPT >= 32) v = pair_max<16>(v);
+  if constexpr (LPT >= 64) v = pair_max<32>(v);
+  return v;
+}
+
+// Logits to shares, in place; of a sigmoid also 1 - s into r (REST).  False
+// for a token whose experts are all masked: its shares are 0.
+template <int LPT, int NE, bool REST>
+__device__ __forceinline__ bool token_shares(int score, float (&y)[NE], float (&r)[NE]) {
+  float top = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < NE; ++i) {
+    y[i] = y[i] == y[i] ? y[i] : -INFINITY;
+    top = fmaxf(top, y[i]);
+  }
+  top = token_max<LPT>(top);
+  float total = 0.0f;
+  if (score == 0) {
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+      y[i] = exp_below(y[i], top);
+      total += y[i];
+    }
+  } else {
+    const bool low = top < 0.0f;  // every score below 1/2
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+      const float l = y[i], t = exp_neg(-fabsf(l)), inv = __builtin_amdgcn_rcpf(1.0f + t);
+      if (REST) r[i] = l >= 0.0f ? t * inv : inv;
+      float n = l >= 0.0f ? 1.0f : t;
+      if (low) n = exp_below(l, top);
+      y[i] = n * inv;
+      total += y[i];
+    }
+  }
+  total = token_sum<LPT>(total);
+  const bool live = top > -INFINITY;
+  const float inv = live ? 1.0f / total : 0.0f;
+#pragma unroll
+  for (int i = 0; i < NE; ++i) y[i] *= inv;
+  return live;
+}
+
+// ---------------------------------------------------------- sequences
+// Offset i, held within the rows (the caller's offsets are not checked).
+__device__ __forceinline__ int64_t bound(const int32_t* __restrict__ off, int64_t i, int64_t rows) {
+  if (!off) return i ? rows : 0;
+  const int64_t v = off[i];
+  return v < 0 ? 0 : v < rows ? v : rows;
+}
+
+// The first sequence that ends behind token t, or seqs: 64 ends at a time, by a
+// whole wave with the same t.  (In 32 bits: with int64_t bounds the compiler
+// selected the lower one by a stale condition code.)
+__device__ __forceinline__ int64_t find_seq(const int32_t* __restrict__ off, int64_t seqs, int64_t rows, int64_t t) {
+  const uint32_t lane = threadIdx.x & 63;
+  uint32_t lo = 0, hi = (uint32_t)seqs;
+  while (lo < hi) {
+    const uint32_t step = (hi - lo + 63) >> 6, i = lo + (lane + 1) * step - 1;
+    const uint64_t past = __builtin_amdgcn_ballot_w64(i >= hi || bound(off, (int64_t)i + 1, rows) > t);
+    if (past == 0) return hi;
+    const uint32_t f = (uint32_t)__builtin_ctzll(past), end = lo + (f + 1) * step - 1;
+    lo += f * step;
+    hi = end < hi ? end : hi;
+  }
+  return lo;
+}
+
+// ------------------------------------------------------- partial sums
+struct BalanceLds {
+  float sum[kPartWaves][kMaxE];
+  int hist[kMaxE];
+  int live[kPartWaves];
+};
+
+// Sums of the tokens [a, b) by the whole workgroup: on return thread e's
+// column of `sum` is added by column_sum, hist and live are whole.
+template <int LT, int LPT, int NE, bool VEC>
+__device__ __forceinline__ void sum_tokens(const BalanceArgs& p, FastDiv by_k, int64_t a, int64_t b, BalanceLds& m) {
+  constexpr int kPer = 64 / LPT;  // tokens of a wave
+  const int lane = threadIdx.x & (LPT - 1), wave = threadIdx.x >> 6;
+  for (int e = threadIdx.x; e < p.experts; e += blockDim.x) m.hist[e] = 0;
+  __syncthreads();
+  const uint32_t n = (uint32_t)((b - a) * p.k);
+  for (uint32_t i = threadIdx.x; i < n; i += blockDim.x) {
+    const uint32_t t = fast_div(i, by_k), j = i - t * by_k.d;
+    const int e = p.idx[(a + t) * p.ld_idx + j];
+    if ((uint32_t)e < (uint32_t)p.experts) atomicAdd(&m.hist[e], 1);
+  }
+  float acc[NE] = {}, y[NE], none[NE];
+  int live = 0;
+  const int64_t step = (int64_t)(blockDim.x >> 6) * kPer;
+  int64_t t = a + (threadIdx.x / LPT);
+  if (t < b) load_token<LT, LPT, NE, VEC>(p.logits, t * p.ldl, lane, p.experts, y);
+  for (; t < b; t += step) {
+    float next[NE];
+    if (t + step < b) load_token<LT, LPT, NE, VEC>(p.logits, (t + step) * p.ldl, lane, p.experts, next);
+    live += token_shares<LPT, NE, false>(p.score, y, none);
+#pragma unroll
+    for (int i = 0; i < NE; ++i) acc[i] += y[i];
+#pragma unroll
+    for (int i = 0; i < NE; ++i) y[i] = next[i];
+  }
+  // the wave's tokens, then the waves'
+#pragma unroll
+  for (int i = 0; i < NE; ++i) {
+    if constexpr (LPT == 16) acc[i] = pair_sum<16>(acc[i]);
+    if constexpr (LPT <= 32) acc[i] = pair_sum<32>(acc[i]);
+    const int e = expert_of<LPT, VEC>(lane, i);
+    if ((threadIdx.x & 63) < LPT && e < p.experts) m.sum[wave][e] = acc[i];
+  }
+  if constexpr (LPT == 16) live += __shfl_xor(live, 16);
+  if constexpr (LPT <= 32) live += __shfl_xor(live, 32);
+  if ((threadIdx.x & 63) == 0) m.live[wave] = live;
+  __syncthreads();
+}
+
+__device__ __forceinline__ float column_sum(const BalanceLds& m, int e) {
+  float s = m.sum[0][e];
+  for (int w = 1; w < (int)(blockDim.x >> 6); ++w) s += m.sum[w][e];
+  return s;
+}
+__device__ __forceinline__ int live_sum(const BalanceLds& m) {
+  int s = 0;
+  for (int w = 0; w < (int)(blockDim.x >> 6); ++w) s += m.live[w];
+  return s;
+}
+
+// Slope of a count and its part of the loss.
+__device__ __forceinline__ double finish(const BalanceArgs& p, int64_t s, int e, int count, int64_t n, double share) {
+  const double per = n > 0 ? (double)p.scale * p.experts / ((double)p.k * (double)n * (double)n) : 0.0;
+  const double slope = per * count;
+  p.counts[s * p.experts + e] = count;
+  p.slope[s * p.experts + e] = (float)slope;
+  return slope * share;
+}
+
+// Sum over the workgroup, in a fixed order; thread 0 has it.
+__device__ __forceinline__ double block_sum64(double v, double* part) {
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+  __syncthreads();
+  double s = 0.0;
+  if (threadIdx.x == 0)
+    for (int w = 0; w < (int)(blockDim.x >> 6); ++w) s += part[w];
+  __syncthreads();
+  return s;
+}
+
+// Few rows: a workgroup takes a whole sequence.
+template <int LT, int LPT, int NE, bool VEC>
+__global__ __launch_bounds__(kPartThreads) void balance_one_kernel(BalanceArgs p, FastDiv by_k) {
+  __shared__ BalanceLds m;
+  __shared__ double part[kPartWaves];
+  for (int64_t s = blockIdx.x; s < p.seqs; s += gridDim.x) {
+    const int64_t a = bound(p.offsets, s, p.rows), b = bound(p.offsets, s + 1, p.rows);
+    sum_tokens<LT, LPT, NE, VEC>(p, by_k, a, b < a ? a : b, m);
+    const int n = live_sum(m);
+    double v = 0.0;
+    for (int e = threadIdx.x; e < p.experts; e += blockDim.x) v += finish(p, s, e, m.hist[e], n, column_sum(m, e));
+    v = block_sum64(v, part);
+    if (threadIdx.x == 0) p.loss[s] = (float)v;
+  }
+}
+
+struct BalancePieces {
+  int64_t chunk, chunks;  // tokens of a chunk, chunks
+  float* sum;             // [chunks + seqs][experts]
+  int32_t* count;         // the same
+  int32_t* live;          // [chunks + seqs]
+};
+
+template <int LT, int LPT, int NE, bool VEC>
+__global__ __launch_bounds__(kPartThreads) void balance_part_kernel(BalanceArgs p, FastDiv by_k, BalancePieces q) {
+  __shared__ BalanceLds m;
+  for (int64_t c = blockIdx.x; c < q.chunks; c += gridDim.x) {
+    const int64_t lo = c * q.chunk, hi = lo + q.chunk < p.rows ? lo + q.chunk : p.rows;
+    int64_t at = lo;
+    while (at < hi) {
+      const int64_t s = find_seq(p.offsets, p.seqs, p.rows, at);
+      if (s >= p.seqs) break;
+      const int64_t first = bound(p.offsets, s, p.rows), end = bound(p.offsets, s + 1, p.rows);
+      const int64_t a = first > at ? first : at, b = end < hi ? end : hi;
+      at = end > at ? end : at + 1;
+      if (a >= b) continue;
+      sum_tokens<LT, LPT, NE, VEC>(p, by_k, a, b, m);
+      const int64_t piece = c + s;
+      for (int e = threadIdx.x; e < p.experts; e += blockDim.x) {
+        q.sum[piece * p.experts + e] = column_sum(m, e);
+        q.count[piece * p.experts + e] = m.hist[e];
+      }
+      if (threadIdx.x == 0) q.live[piece] = live_sum(m);
+      __syncthreads();  // (the next piece writes m again)
+    }
+  }
+}
+
+// The pieces of a sequence, added: thread (part, e) takes W experts of every
+// PARTS-th piece.
+constexpr int kJoinThreads = 1024;
+
+template <int W>
+__global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(BalanceArgs p, BalancePieces q) {
+  __shared__ double sums[kJoinThreads * W];
+  __shared__ int counts[kJoinThreads * W];
+  __shared__ double part[kJoinThreads / 64];
+  __shared__ int lives[kJoinThreads / 64];
+  const int E = p.experts, groups = E / W;
+  int cols = 1;
+  while (cols < groups) cols <<= 1;
+  const int parts = kJoinThreads / cols, g = threadIdx.x & (cols - 1), mine = threadIdx.x / cols;
+  for (int64_t s = blockIdx.x; s < p.seqs; s += gridDim.x) {
+    const int64_t a = bound(p.offsets, s, p.rows), b = bound(p.offsets, s + 1, p.rows);
+    const int64_t first = a / q.chunk + s, last = b > a ? (b - 1) / q.chunk + s : first - 1;
+    double t[W] = {};
+    int c[W] = {}, live = 0;
+    if (g < groups) {
+#pragma unroll 4
+      for (int64_t i = first + mine; i <= last; i += parts) {
+        float v[W];
+        int w[W];
+        if constexpr (W == 4) {
+          const float4 f = *reinterpret_cast<const float4*>(q.sum + i * E + g * 4);
+          const int4 n = *reinterpret_cast<const int4*>(q.count + i * E + g * 4);
+          v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+          w[0] = n.x; w[1] = n.y; w[2] = n.z; w[3] = n.w;
+        } else {
+          v[0] = q.sum[i * E + g];
+          w[0] = q.count[i * E + g];
+        }
+#pragma unroll
+        for (int x = 0; x < W; ++x) {
+          t[x] += v[x];
+          c[x] += w[x];
+        }
+      }
+    }
+    for (int64_t i = first + threadIdx.x; i <= last; i += kJoinThreads) live += q.live[i];
+#pragma unroll
+    for (int x = 0; x < W; ++x) {
+      sums[(mine * W + x) * cols + g] = t[x];
+      counts[(mine * W + x) * cols + g] = c[x];
+    }
+#pragma unroll
+    for (int k = 1; k < 64; k <<= 1) live += __shfl_xor(live, k);
+    if ((threadIdx.x & 63) == 0) lives[threadIdx.x >> 6] = live;
+    __syncthreads();
+    int64_t n = 0;
+    for (int w = 0; w < kJoinThreads / 64; ++w) n += lives[w];
+    double v = 0.0;
+    for (int i = threadIdx.x; i < cols * W; i += kJoinThreads) {
+      const int gi = i & (cols - 1), x = i / cols;
+      if (gi >= groups) continue;
+      double total = 0.0;
+      int count = 0;
+      for (int r = 0; r < parts; ++r) {
+        total += sums[(r * W + x) * cols + gi];
+        count += counts[(r * W + x) * cols + gi];
+      }
+      v += finish(p, s, gi * W + x, count, n, total);
+    }
+    v = block_sum64(v, part);
+    if (threadIdx.x == 0) p.loss[s] = (float)v;
+  }
+}
+
+// ----------------------------------------------------------- gradient
+constexpr int kGradThreads = 256;
+
+// A wave takes `run` consecutive tokens (per lane group every kPer-th of
+// them); the next token's logits and base are loaded while this one is formed.
+template <int LT, int LPT, int NE, bool VEC>
+__global__ __launch_bounds__(kGradThreads) void balance_grad_kernel(BalanceGradArgs p, int64_t run) {
+  constexpr int kPer = 64 / LPT;
+  const int lane = threadIdx.x & (LPT - 1), E = p.experts;
+  const int64_t wave = (int64_t)blockIdx.x * (kGradThreads / 64) + (threadIdx.x >> 6);
+  const int64_t lo = wave * run, hi = lo + run < p.rows ? lo + run : p.rows;
+  if (lo >= hi) return;
+  int64_t s = find_seq(p.offsets, p.seqs, p.rows, lo);
+  int64_t held = -1;
+  float c[NE], y[NE], base[NE];
+#pragma unroll
+  for (int i = 0; i < NE; ++i) c[i] = base[i] = 0.0f;
+  int64_t t = lo + ((threadIdx.x & 63) / LPT);
+  if (t < hi) {
+    load_token<LT, LPT, NE, VEC>(p.logits, t * p.ldl, lane, E, y);
+    if (p.base) load_token<LT, LPT, NE, VEC>(p.base, t * p.ldb, lane, E, base);
+  }
+  for (; t < hi; t += kPer) {
+    float ny[NE], nb[NE];
+    if (t + kPer < hi) {
+      load_token<LT, LPT, NE, VEC>(p.logits, (t + kPer) * p.ldl, lane, E, ny);
+      if (p.base) load_token<LT, LPT, NE, VEC>(p.base, (t + kPer) * p.ldb, lane, E, nb);
+    }
+    if (s < p.seqs && bound(p.offsets, s + 1, p.rows) <= t) {
+      // the first sequence behind s that ends past t
+      int64_t l = s + 1, h = p.seqs;
+      while (l < h) {
+        const int64_t mid = l + ((h - l) >> 1);
+        if (bound(p.offsets, mid + 1, p.rows) > t) h = mid; else l = mid + 1;
+      }
+      s = l;
+    }
+    const int64_t now = s < p.seqs && bound(p.offsets, s, p.rows) <= t ? s : p.seqs;
+    if (now != held) {
+      held = now;
+      const float d = now < p.seqs ? p.dloss ? p.dloss[now] : 1.0f : 0.0f;
+#pragma unroll
+      for (int i = 0; i < NE; ++i) {
+        const int e = expert_of<LPT, VEC>(lane, i);
+        c[i] = now < p.seqs && e < E ? d * p.slope[now * E + e] : 0.0f;
+      }
+    }
+    float r[NE], o[NE];
+    token_shares<LPT, NE, true>(p.score, y, r);
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) m = __builtin_fmaf(c[i], y[i], m);
+    m = token_sum<LPT>(m);
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+      o[i] = y[i] * (c[i] - m);
+      if (p.score != 0) o[i] *= r[i];
+      if (p.base) o[i] += base[i];
+    }
+    store_token<LT, LPT, NE, VEC>(p.dl, t * p.lddl, lane, E, o);
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+      y[i] = ny[i];
+      base[i] = nb[i];
+    }
+  }
+}
+
+// Up to this many rows a workgroup takes a whole sequence, in one launch.
+constexpr int64_t kOneRows = 512;
+constexpr int64_t kMostChunks = 256;
+constexpr int64_t kMaxChunk = 4096;
+constexpr int64_t kMaxBlocks = 1 << 20;
+
+int64_t chunk_tokens(int64_t rows) {
+  int64_t c = (rows + kMostChunks - 1) / kMostChunks;
+  c = (c + 7) / 8 * 8;
+  return c < 32 ? 32 : c < kMaxChunk ? c : kMaxChunk;
+}
+
+template <int LT, int LPT, int NE, bool VEC>
+hipError_t balance_as(const BalanceArgs& a, hipStream_t st) {
+  const FastDiv by_k = make_fast_div((uint32_t)a.k);
+  const unsigned seqs = (unsigned)(a.seqs < kMaxBlocks ? a.seqs : kMaxBlocks);
+  if (a.rows <= kOneRows) {
+    hipLaunchKernelGGL((balance_one_kernel<LT, LPT, NE, VEC>), dim3(seqs), dim3(kPartThreads), 0, st, a, by_k);
+    return hipGetLastError();
+  }
+  BalancePieces q;
+  q.chunk = chunk_tokens(a.rows);
+  q.chunks = (a.rows + q.chunk - 1) / q.chunk;
+  const int64_t pieces = q.chunks + a.seqs;
+  q.sum = reinterpret_cast<float*>(a.workspace);
+  q.count = reinterpret_cast<int32_t*>(q.sum + pieces * a.experts);
+  q.live = q.count + pieces * a.experts;
+  const unsigned blocks = (unsigned)(q.chunks < kMaxBlocks ? q.chunks : kMaxBlocks);
+  hipLaunchKernelGGL((balance_part_kernel<LT, LPT, NE, VEC>), dim3(blocks), dim3(kPartThreads), 0, st, a, by_k, q);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if (a.experts % 4 == 0)
+    hipLaunchKernelGGL((balance_join_kernel<4>), dim3(seqs), dim3(kJoinThreads), 0, st, a, q);
+  else
+    hipLaunchKernelGGL((balance_join_kernel<1>), dim3(seqs), dim3(kJoinThreads), 0, st, a, q);
+  return hipGetLastError();
+}
+
+template <int LT, int LPT, int NE, bool VEC>
+hipError_t grad_as(const BalanceGradArgs& a, hipStream_t st) {
+  constexpr int kPer = 64 / LPT;
+  const int64_t waves = (int64_t)device_cu_count() * 32;
+  int64_t run = (a.rows + waves - 1) / waves;
+  run = (run + kPer - 1) / kPer * kPer;
+  const int64_t per = run * (kGradThreads / 64);
+  hipLaunchKernelGGL((balance_grad_kernel<LT, LPT, NE, VEC>), dim3((unsigned)((a.rows + per - 1) / per)), dim3(kGradThreads),
+                     0, st, a, run);
+  return hipGetLastError();
+}
+
+// f.template go<LT, LPT, NE, VEC>() by the number of experts.
+template <int LT, bool VEC, typename F>
+hipError_t by_experts(int E, F f) {
+  if (E <= 64) return f.template go<LT, 16, 4, VEC>();
+  if (E <= 128) return f.template go<LT, 32, 4, VEC>();
+  if (E <= 256) return f.template go<LT, 64, 4, VEC>();
+  if (E <= 512) return f.template go<LT, 64, 8, VEC>();
+  return f.template go<LT, 64, 16, VEC>();
+}
+template <typename F>
+hipError_t choose(int l_type, bool vec, int E, F f) {
+  if (l_type == 0) return vec ? by_experts<0, true>(E, f) : by_experts<0, false>(E, f);
+  return vec ? by_experts<1, true>(E, f) : by_experts<1, false>(E, f);
+}
+
+struct GoBalance {
+  const BalanceArgs& a;
+  hipStream_t st;
+  template <int LT, int LPT, int NE, bool VEC>
+  hipError_t go() const { return balance_as<LT, LPT, NE, VEC>(a, st); }
+};
+struct GoGrad {
+  const BalanceGradArgs& a;
+  hipStream_t st;
+  template <int LT, int LPT, int NE, bool VEC>
+  hipError_t go() const { return grad_as<LT, LPT, NE, VEC>(a, st); }
+};
+
+// Whether rows of 4 elements at a time are aligned.
+bool fours(const void* p, int64_t ld, int l_type) {
+  return reinterpret_cast<uintptr_t>(p) % (l_type == 0 ? 8 : 16) == 0 && ld % 4 == 0;
+}
+
+}  // namespace
+
+int64_t balance_workspace(int64_t rows, int64_t experts, int64_t seqs) {
+  if (rows <= kOneRows) return 16;
+  const int64_t chunk = chunk_tokens(rows), pieces = (rows + chunk - 1) / chunk + seqs;
+  return pieces * (2 * experts + 1) * (int64_t)sizeof(float);
+}
+
+hipError_t launch_balance(const BalanceArgs& a, hipStream_t st) {
+  return choose(a.l_type, a.experts % 4 == 0 && fours(a.logits, a.ldl, a.l_type), a.experts, GoBalance{a, st});
+}
+
+hipError_t launch_balance_grad(const BalanceGradArgs& a, hipStream_t st) {
+  const bool vec = a.experts % 4 == 0 && fours(a.logits, a.ldl, a.l_type) && fours(a.base, a.ldb, a.l_type) &&
+                   fours(a.dl, a.lddl, a.l_type);
+  return choose(a.l_type, vec, a.experts, GoGrad{a, st});
+}
+
+}  // namespace fp8fg

@@ -1,0 +1,389 @@
+// Root-mean-square norms after and before a block, with the block's gate, the
+// scaled residual addition and an E4M3 output, and their gradient, for gfx950.
+//
+// Forward, per row, z the block's output and r the residual stream:
+//   zh = z rstd_post,  t = zh gamma_post gate block_scale
+//   h = RN(residual_scale r + t) in z's type
+//   y = (h rstd) gamma;  q, s as the norm's (norm.hip)
+// rstd = 1 / sqrt(mean of squares + eps) of z and of the rounded h.
+// Backward, dy the gradient of y, dh what reaches h along the stream:
+//   xh = h rstd,  a = dy gamma,  dH = rstd (a - xh mean(a xh)) + dh
+//   dr = residual_scale dH
+//   b = block_scale dH gate,  dz = rstd_post (b gamma_post - zh mean(b gamma_post zh))
+//   dgamma = sum over rows dy xh,  dgamma_post = sum over rows b zh
+//   dgate = block_scale dH zh gamma_post: of a gate per column summed over
+//   the rows, which is gamma_post's sum without the gate: one sum
+//   D = sum dH zh gives both.
+// A row stays in the workgroup's registers, undecoded, from its one reading to
+// its outputs.
+#include <float.h>
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "device_common.h"
+#include "launch.h"
+#include "norm_common.h"
+
+namespace fp8fg {
+
+namespace {
+
+enum { kGateNone = 0, kGateCols = 1, kGateRows = 2 };
+
+template <int XT, int NV>
+__device__ __forceinline__ float rstd_of(const Raw8<XT> (&raw)[NV], float ss, int nvec, int64_t cols, float eps, double* wide) {
+  const float mean = ss / (float)cols + eps;
+  if (__builtin_expect(!(mean >= kLeastMean && mean <= FLT_MAX), 0)) return wide_range_rstd<XT, NV>(raw, nvec, cols, eps, wide);
+  return 1.0f / sqrtf(mean);
+}
+
+// One row per workgroup iteration, as in norm_kernel: thread t holds the
+// 8-element vectors t, t + blockDim, ..
+template <int XT, int NV, int GATE, bool STREAM>
+__global__ __launch_bounds__(512) void block_norm_kernel(BlockNormArgs p) {
+  __shared__ float part[2][kMaxWaves];
+  __shared__ double wide[kMaxWaves];
+  const int nvec = (int)(p.cols >> 3);
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    Raw8<XT> z[NV], r[NV], gr[NV];
+    float ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = threadIdx.x + i * blockDim.x;
+      if (v >= nvec) continue;
+      z[i] = load_raw8<XT, STREAM>(p.z, row * p.ldz + v * 8);
+      r[i] = load_raw8<XT, STREAM>(p.r, row * p.ldr + v * 8);
+      if (GATE == kGateRows) gr[i] = load_raw8<XT, STREAM>(p.gate, row * p.ldg + v * 8);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = threadIdx.x + i * blockDim.x;
+      if (v >= nvec) continue;
+      float f[8];
+      decode8<XT>(z[i], f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss += f[e] * f[e];
+    }
+    ss = block_sum(ss, part[0]);
+    const float post = rstd_of<XT, NV>(z, ss, nvec, p.cols, p.eps, wide);
+    ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = threadIdx.x + i * blockDim.x;
+      if (v >= nvec) continue;
+      float f[8], g[8], x[8];
+      decode8<XT>(z[i], f);
+      decode_gamma<8>(load_gamma<8>(p.gamma_post, p.g_type, v), p.g_type, g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = f[e] * post * g[e];
+      if (GATE != kGateNone) {
+        if (GATE == kGateCols)
+          decode_gamma<8>(load_gamma<8>(p.gate, p.g_type, v), p.g_type, g);
+        else
+          decode8<XT>(gr[i], g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] *= g[e];
+      }
+      decode8<XT>(r[i], x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = p.residual_scale * x[e] + p.block_scale * f[e];
+      r[i] = encode8<XT>(x);
+      store_raw8<XT, false>(p.h, row * p.ldh + v * 8, r[i]);
+      decode8<XT>(r[i], x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss += x[e] * x[e];
+    }
+    ss = block_sum(ss, part[1]);
+    const float rstd = rstd_of<XT, NV>(r, ss, nvec, p.cols, p.eps, wide);
+    if (threadIdx.x == 0) {
+      if (p.rstd_post) p.rstd_post[row] = post;
+      if (p.rstd) p.rstd[row] = rstd;
+    }
+    if (!p.q && !p.y) continue;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = threadIdx.x + i * blockDim.x;
+      if (v >= nvec) continue;
+      float f[8], g[8];
+      decode8<XT>(r[i], f);
+      decode_gamma<8>(load_gamma<8>(p.gamma, p.g_type, v), p.g_type, g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = f[e] * rstd * g[e];
+      if (p.y) store_raw8<XT, false>(p.y, row * p.ldy + v * 8, encode8<XT>(f));
+      if (p.q) {
+        float m = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]));
+        m = row16_max(m);
+        TileScale sc;
+        if (p.rule == 0) {
+          sc = scale_amax(m);
+          quotient8<0>(f, sc);
+        } else {
+          sc = scale_pow2(m);
+          quotient8<1>(f, sc);
+        }
+        uint2 out;
+        out.x = pack4_e4m3(f[0], f[1], f[2], f[3]);
+        out.y = pack4_e4m3(f[4], f[5], f[6], f[7]);
+        st_nt8(p.q + row * p.ldq + v * 8, out);
+        if ((threadIdx.x & 15) == 0) p.s[row * p.s_rs + (int64_t)(v >> 4) * p.s_ts] = sc.s;
+      }
+    }
+  }
+}
+
+// A workgroup takes the rows blockIdx.x, blockIdx.x + gridDim.x, ..; its
+// threads keep their columns' part of the two sums over rows in registers
+// (D = sum dH zh, with a gate of rows sum dH zh gate; and sum dy xh) and
+// write them once.
+template <int XT, int NV, int GATE, bool NT>
+__global__ __launch_bounds__(512) void block_norm_grad_kernel(BlockNormGradArgs p) {
+  constexpr int N = kPer16<XT>;
+  __shared__ float part[2][kMaxWaves];
+  const int nvec = (int)(p.cols / N);
+  const float inv_cols = 1.0f / (float)p.cols;
+  float acc[2][NV][N];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int e = 0; e < N; ++e) acc[0][i][e] = acc[1][i][e] = 0.0f;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    const float rstd = p.rstd[row], post = p.rstd_post[row];
+    Unit<XT, N> d[NV], h[NV], z[NV], b[NV], gr[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = threadIdx.x + i * blockDim.x;
+      if (v >= nvec) continue;
+      d[i] = load_unit<XT, NT, N>(p.dy, row * p.lddy, v);
+      h[i] = load_unit<XT, NT, N>(p.h, row * p.ldh, v);
+      z[i] = load_unit<XT, NT, N>(p.z, row * p.ldz, v);
+      if (p.dh) b[i] = load_unit<XT, NT, N>(p.dh, row * p.lddh, v);
+      if (GATE == kGateRows) gr[i] = load_unit<XT, NT, N>(p.gate, row * p.ldg, v);
+    }
+    float c = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = threadIdx.x + i * blockDim.x;
+      if (v >= nvec) continue;
+      float dy[N], x[N], g[N];
+      decode_unit<XT, N>(d[i], dy);
+      decode_unit<XT, N>(h[i], x);
+      decode_gamma<N>(load_gamma<N>(p.gamma, p.g_type, v), p.g_type, g);
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const float dx = dy[e] * (x[e] * rstd);
+        c = __builtin_fmaf(dx, g[e], c);
+        acc[1][i][e] += dx;
+      }
+    }
+    c = block_sum(c, part[0]) * inv_cols;
+    // dH, kept as b gamma_post (b = block_scale dH gate), and the second mean
+    float w[NV][N], m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = threadIdx.x + i * blockDim.x;
+      if (v >= nvec) continue;
+      float dy[N], x[N], zv[N], g[N], o[N];
+      decode_unit<XT, N>(d[i], dy);
+      decode_unit<XT, N>(h[i], x);
+      decode_unit<XT, N>(z[i], zv);
+      decode_gamma<N>(load_gamma<N>(p.gamma, p.g_type, v), p.g_type, g);
+#pragma unroll
+      for (int e = 0; e < N; ++e) o[e] = rstd * __builtin_fmaf(-(x[e] * rstd), c, dy[e] * g[e]);
+      if (p.dh) {
+        decode_unit<XT, N>(b[i], x);
+#pragma unroll
+        for (int e = 0; e < N; ++e) o[e] += x[e];
+      }
+#pragma unroll
+      for (int e = 0; e < N; ++e) x[e] = p.residual_scale * o[e];
+      store_unit<XT, N>(p.dr, row * p.lddr, v, x);
+      decode_gamma<N>(load_gamma<N>(p.gamma_post, p.g_type, v), p.g_type, g);
+      if (GATE == kGateRows) {
+        float gv[N];
+        decode_unit<XT, N>(gr[i], gv);
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          const float t = o[e] * (zv[e] * post);
+          x[e] = p.block_scale * t * g[e];
+          o[e] *= gv[e];
+          acc[0][i][e] = __builtin_fmaf(t, gv[e], acc[0][i][e]);
+        }
+        store_unit<XT, N>(p.dgate, row * p.lddg, v, x);
+      } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) acc[0][i][e] = __builtin_fmaf(o[e], zv[e] * post, acc[0][i][e]);
+      }
+      if (GATE == kGateCols) {
+        float gv[N];
+        decode_gamma<N>(load_gamma<N>(p.gate, p.g_type, v), p.g_type, gv);
+#pragma unroll
+        for (int e = 0; e < N; ++e) o[e] *= gv[e];
+      }
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        w[i][e] = p.block_scale * o[e] * g[e];
+        m = __builtin_fmaf(w[i][e], zv[e] * post, m);
+      }
+    }
+    m = block_sum(m, part[1]) * inv_cols;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = threadIdx.x + i * blockDim.x;
+      if (v >= nvec) continue;
+      float zv[N], o[N];
+      decode_unit<XT, N>(z[i], zv);
+#pragma unroll
+      for (int e = 0; e < N; ++e) o[e] = post * __builtin_fmaf(-(zv[e] * post), m, w[i][e]);
+      store_unit<XT, N>(p.dz, row * p.lddz, v, o);
+    }
+  }
+  const int64_t strips = gridDim.x;
+#pragma unroll
+  for (int a = 0; a < 2; ++a)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int v = threadIdx.x + i * blockDim.x;
+      if (v >= nvec) continue;
+      float* out = p.partial + (a * strips + blockIdx.x) * p.cols + v * N;
+#pragma unroll
+      for (int e = 0; e < N; e += 4)
+        *reinterpret_cast<float4*>(out + e) =
+            make_float4(acc[a][i][e], acc[a][i][e + 1], acc[a][i][e + 2], acc[a][i][e + 3]);
+    }
+}
+
+// Element c of a vector of g_type.
+__device__ __forceinline__ float gamma_at(const void* g, int g_type, int64_t c) {
+  return g_type == 0 ? __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(g)[c] << 16)
+                     : reinterpret_cast<const float*>(g)[c];
+}
+
+// The strips' sums, added as norm_grad_sum_kernel adds them: blockIdx.y 0
+// gives dgamma_post and a column gate's gradient, 1 dgamma.
+constexpr int kSumThreads = 512;
+
+template <int GATE>
+__global__ __launch_bounds__(kSumThreads) void block_norm_sum_kernel(BlockNormGradArgs p, int strips) {
+  __shared__ float part[kSumThreads / 64][16];
+  const float* partial = p.partial + (int64_t)blockIdx.y * strips * p.cols;
+  const int c = threadIdx.x & 3, s0 = threadIdx.x >> 2;
+  const int64_t col = (int64_t)blockIdx.x * 16 + c * 4;
+  float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (col < p.cols) {
+#pragma unroll 8
+    for (int s = s0; s < strips; s += kSumThreads / 4) {
+      const float4 v = *reinterpret_cast<const float4*>(partial + s * p.cols + col);
+      t[0] += v.x;
+      t[1] += v.y;
+      t[2] += v.z;
+      t[3] += v.w;
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+#pragma unroll
+    for (int m = 4; m < 64; m <<= 1) t[e] += __shfl_xor(t[e], m);
+    if ((threadIdx.x & 63) < 4) part[threadIdx.x >> 6][c * 4 + e] = t[e];
+  }
+  __syncthreads();
+  if (threadIdx.x < 16) {
+    const int64_t at = (int64_t)blockIdx.x * 16 + threadIdx.x;
+    float s = part[0][threadIdx.x];
+#pragma unroll
+    for (int w = 1; w < kSumThreads / 64; ++w) s += part[w][threadIdx.x];
+    if (at < p.cols) {
+      if (blockIdx.y == 1) {
+        p.dgamma[at] = s;
+      } else {
+        s *= p.block_scale;
+        p.dgamma_post[at] = GATE == kGateCols ? s * gamma_at(p.gate, p.g_type, at) : s;
+        if (GATE == kGateCols && p.dgate) reinterpret_cast<float*>(p.dgate)[at] = s * gamma_at(p.gamma_post, p.g_type, at);
+      }
+    }
+  }
+}
+
+template <int XT, int GATE, bool STREAM>
+hipError_t norm_as(const BlockNormArgs& a, hipStream_t st) {
+  const RowShape sh = row_shape(a.cols);
+  const dim3 grid((unsigned)(a.rows < kMaxRowBlocks ? a.rows : kMaxRowBlocks)), block(sh.threads);
+  if (sh.per == 1)
+    hipLaunchKernelGGL((block_norm_kernel<XT, 1, GATE, STREAM>), grid, block, 0, st, a);
+  else if (sh.per == 2)
+    hipLaunchKernelGGL((block_norm_kernel<XT, 2, GATE, STREAM>), grid, block, 0, st, a);
+  else
+    hipLaunchKernelGGL((block_norm_kernel<XT, 4, GATE, STREAM>), grid, block, 0, st, a);
+  return hipGetLastError();
+}
+
+template <int XT, int GATE>
+hipError_t norm_t(const BlockNormArgs& a, hipStream_t st) {
+  const bool big = past_caches(a.rows, GATE == kGateRows ? 3 : 2, a.cols, XT == 0 ? 2 : 4);
+  return big ? norm_as<XT, GATE, true>(a, st) : norm_as<XT, GATE, false>(a, st);
+}
+
+template <int XT, int GATE, bool NT>
+hipError_t grad_as(const BlockNormGradArgs& a, hipStream_t st) {
+  constexpr int U = 8 / kPer16<XT>;
+  const RowShape sh = row_shape(a.cols);
+  const dim3 grid((unsigned)block_norm_strips(a.rows, a.cols)), block(sh.threads);
+  if (sh.per == 1)
+    hipLaunchKernelGGL((block_norm_grad_kernel<XT, U, GATE, NT>), grid, block, 0, st, a);
+  else if (sh.per == 2)
+    hipLaunchKernelGGL((block_norm_grad_kernel<XT, 2 * U, GATE, NT>), grid, block, 0, st, a);
+  else
+    hipLaunchKernelGGL((block_norm_grad_kernel<XT, 4 * U, GATE, NT>), grid, block, 0, st, a);
+  return hipGetLastError();
+}
+
+template <int XT, int GATE>
+hipError_t grad_t(const BlockNormGradArgs& a, hipStream_t st) {
+  const bool big = past_caches(a.rows, 3 + (a.dh != nullptr) + (GATE == kGateRows), a.cols, XT == 0 ? 2 : 4);
+  return big ? grad_as<XT, GATE, true>(a, st) : grad_as<XT, GATE, false>(a, st);
+}
+
+// f.template go<XT, GATE>() by the type and the gate.
+template <typename F>
+hipError_t choose(int x_type, const void* gate, int64_t ldg, F f) {
+  if (x_type == 0)
+    return !gate ? f.template go<0, kGateNone>() : ldg == 0 ? f.template go<0, kGateCols>() : f.template go<0, kGateRows>();
+  return !gate ? f.template go<1, kGateNone>() : ldg == 0 ? f.template go<1, kGateCols>() : f.template go<1, kGateRows>();
+}
+struct GoNorm {
+  const BlockNormArgs& a;
+  hipStream_t st;
+  template <int XT, int GATE>
+  hipError_t go() const { return norm_t<XT, GATE>(a, st); }
+};
+struct GoGrad {
+  const BlockNormGradArgs& a;
+  hipStream_t st;
+  template <int XT, int GATE>
+  hipError_t go() const { return grad_t<XT, GATE>(a, st); }
+};
+
+}  // namespace
+
+int64_t block_norm_strips(int64_t rows, int64_t cols) { return norm_grad_strips(rows, cols); }
+
+hipError_t launch_block_norm(const BlockNormArgs& a, hipStream_t st) {
+  return choose(a.x_type, a.gate, a.ldg, GoNorm{a, st});
+}
+
+hipError_t launch_block_norm_grad(const BlockNormGradArgs& a, hipStream_t st) {
+  if (a.rows > 0) {
+    const hipError_t e = choose(a.x_type, a.gate, a.ldg, GoGrad{a, st});
+    if (e != hipSuccess) return e;
+  }
+  const dim3 grid((unsigned)((a.cols + 15) / 16), 2);
+  const int strips = (int)block_norm_strips(a.rows, a.cols);
+  if (a.gate && a.ldg == 0)
+    hipLaunchKernelGGL((block_norm_sum_kernel<kGateCols>), grid, dim3(kSumThreads), 0, st, a, strips);
+  else
+    hipLaunchKernelGGL((block_norm_sum_kernel<kGateNone>), grid, dim3(kSumThreads), 0, st, a, strips);
+  return hipGetLastError();
+}
+
+}  // namespace fp8fg

@@ -244,4 +244,168 @@ struct CombineGradArgs {
 };
 hipError_t launch_combine_grad(const CombineGradArgs& a, hipStream_t st);
 
+// ------------------------------------------------- silu gate (gate.hip)
+struct GateArgs {
+  const void* u;
+  int u_type;          // 0 bf16, 1 f32
+  int64_t rows, inner, ldu;
+  const int32_t* used; // rows in use; null: all
+  int rule;            // 0 amax, 1 pow2
+  uint8_t* q;
+  int64_t ldq;
+  float* s;
+  int64_t s_rs, s_ts;
+  uint8_t* uq;         // checkpoint of u; null: not kept
+  int64_t lduq;
+  float* us;
+  int64_t us_rs, us_ts;
+};
+hipError_t launch_gate(const GateArgs& a, hipStream_t st);
+
+struct GateGradArgs {
+  const void* da;
+  int type;            // 0 bf16, 1 f32 (da, du, a)
+  int64_t rows, inner, ldda;
+  const uint8_t* uq;
+  int64_t lduq;
+  const float* us;
+  int64_t us_rs, us_ts;
+  const int32_t* used; // null: all
+  int rule;
+  uint8_t* q;          // of [dg | dl]; null: not wanted
+  int64_t ldq;
+  float* s;
+  int64_t s_rs, s_ts;
+  void* du;            // null: not wanted
+  int64_t lddu;
+  void* a;             // null: not wanted
+  int64_t lda;
+};
+hipError_t launch_gate_grad(const GateGradArgs& a, hipStream_t st);
+
+struct GateGradTileArgs {
+  const void* da;
+  int type;
+  int64_t rows, inner, ldda;
+  const uint8_t* uq;
+  int64_t lduq;
+  const float* us;
+  int64_t us_rs, us_ts;
+  int rule;
+  uint8_t* q;          // 1x128 tiles of [dg | dl]
+  int64_t ldq;
+  float* s;
+  int64_t s_rs, s_ts;
+  uint8_t* qt;         // 128x1 tiles of it, transposed
+  int64_t ldqt;
+  float* st;
+  int64_t st_rs, st_ts;
+  uint8_t* aq;         // 128x1 tiles of a, transposed
+  int64_t ldaq;
+  float* as;
+  int64_t as_rs, as_ts;
+};
+hipError_t launch_gate_grad_tile(const GateGradTileArgs& a, hipStream_t st);
+
+// ------------------------------------------------- balance loss (balance.hip)
+struct BalanceArgs {
+  const void* logits;
+  int l_type;          // 0 bf16, 1 f32
+  int64_t rows;
+  int experts;
+  int64_t ldl;
+  const int32_t* idx;
+  int64_t ld_idx;
+  int k;
+  const int32_t* offsets;  // [seqs + 1]; null: one sequence of all rows
+  int64_t seqs;
+  int score;           // 0 softmax, 1 sigmoid
+  float scale;
+  float* loss;         // [seqs]
+  int32_t* counts;     // [seqs][experts]
+  float* slope;        // [seqs][experts]
+  void* workspace;     // balance_workspace(...) bytes
+};
+// Bytes of partial sums; a function of the sizes alone.
+int64_t balance_workspace(int64_t rows, int64_t experts, int64_t seqs);
+hipError_t launch_balance(const BalanceArgs& a, hipStream_t st);
+
+struct BalanceGradArgs {
+  const float* dloss;  // [seqs]; null: ones
+  const void* logits;
+  int l_type;          // of logits, base and dl
+  int64_t rows;
+  int experts;
+  int64_t ldl;
+  const float* slope;
+  const int32_t* offsets;
+  int64_t seqs;
+  int score;
+  const void* base;    // added; null: none
+  int64_t ldb;
+  void* dl;
+  int64_t lddl;
+};
+hipError_t launch_balance_grad(const BalanceGradArgs& a, hipStream_t st);
+
+// ------------------------------------------------- norms after and before a block (block_norm.hip)
+struct BlockNormArgs {
+  const void* z;
+  int x_type;          // 0 bf16, 1 f32: z, r, h, y and a gate of rows
+  int64_t rows, cols, ldz;
+  const void* r;
+  int64_t ldr;
+  const void* gamma_post;
+  const void* gamma;
+  int g_type;          // 0 bf16, 1 f32: the gammas and a gate of columns
+  const void* gate;    // null: none
+  int64_t ldg;         // 0: one per column; otherwise the pitch of a gate of rows
+  float residual_scale, block_scale, eps;
+  int rule;
+  void* h;
+  int64_t ldh;
+  void* y;             // null: not stored
+  int64_t ldy;
+  uint8_t* q;          // null: no quantized output
+  int64_t ldq;
+  float* s;
+  int64_t s_rs, s_ts;
+  float* rstd_post;    // null: not stored
+  float* rstd;         // null: not stored
+};
+hipError_t launch_block_norm(const BlockNormArgs& a, hipStream_t st);
+
+struct BlockNormGradArgs {
+  const void* dy;
+  int x_type;          // dy, dh, z, h, dz, dr, and gate and dgate of rows
+  int64_t rows, cols, lddy;
+  const void* dh;      // null: none
+  int64_t lddh;
+  const void* z;
+  int64_t ldz;
+  const void* h;
+  int64_t ldh;
+  const void* gamma_post;
+  const void* gamma;
+  int g_type;
+  const void* gate;
+  int64_t ldg;
+  const float* rstd_post;
+  const float* rstd;
+  float residual_scale, block_scale;
+  void* dz;
+  int64_t lddz;
+  void* dr;
+  int64_t lddr;
+  float* dgamma_post;
+  float* dgamma;
+  void* dgate;         // f32 [cols], or rows of x_type; null without a gate
+  int64_t lddg;
+  float* partial;      // [2][block_norm_strips(rows, cols)][cols]
+};
+int64_t block_norm_strips(int64_t rows, int64_t cols);
+hipError_t launch_block_norm_grad(const BlockNormGradArgs& a, hipStream_t st);
+// Widest row a workgroup of 512 threads holds in registers.
+constexpr int64_t kBlockNormMaxCols = 16384;
+
 }  // namespace fp8fg

@@ -335,6 +335,232 @@ PyObject* combine_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// int32, one value on the rows' device: the rows in use.
+void one_count(const Tensor* t, const Tensor& x) {
+  if (!t) return;
+  need(t->numel() == 1 && t->scalar_type() == at::kInt && t->device() == x.device(), "used",
+       "must be one int32 value on the rows' device");
+}
+
+// E4M3 bytes [rows][cols] and their 1x128 scales.
+void tiles(const Tensor& q, const Tensor& s, int64_t rows, int64_t cols, const Tensor& x, const char* qn, const char* sn) {
+  rows2d(q, qn);
+  need(q.scalar_type() == at::kByte && q.size(0) == rows && q.size(1) == cols && q.device() == x.device(), qn,
+       "must be the E4M3 bytes (uint8) [rows][2 columns] of the checkpoint on the gradient's device");
+  need(s.dim() == 2 && s.size(0) == rows && s.size(1) == cols / 128 && s.scalar_type() == at::kFloat &&
+           s.device() == x.device(),
+       sn, "must be the f32 [rows][columns / 128] scales of the checkpoint");
+}
+
+// (u, used, keep, rule, group_major, stream)
+PyObject* swiglu_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arity(n, 6);
+  const Tensor& u = tensor(a[0], "u");
+  rows2d(u, "u");
+  need(xtype(u) >= 0, "u", "must be bf16 or f32");
+  need(u.size(1) % 2 == 0, "u", "must have two halves of columns");
+  const Tensor* used = tensor_or_none(a[1], "used");
+  one_count(used, u);
+  const int64_t M = u.size(0), C = u.size(1) / 2;
+  const bool keep = truth(a[2]), gm = truth(a[4]);
+  const c10::DeviceGuard guard(u.device());
+  const Tensor q = make(M, C, at::kByte, u), s = make_scales(M, C / 128, gm, u);
+  const Tensor uq = keep ? make(M, 2 * C, at::kByte, u) : Tensor(), us = keep ? make_scales(M, 2 * C / 128, gm, u) : Tensor();
+  check(fp8_swiglu_quantize(ptr(u), xtype(u), M, C, pitch(u), ptr<int32_t>(used), small(a[3]), ptr<uint8_t>(q), C,
+                            ptr<float>(s), s.stride(0), s.stride(1), keep ? ptr<uint8_t>(uq) : nullptr, 2 * C,
+                            keep ? ptr<float>(us) : nullptr, keep ? us.stride(0) : 0, keep ? us.stride(1) : 0,
+                            handle(a[5])),
+        "fp8_swiglu_quantize");
+  return give({&q, &s, keep ? &uq : nullptr, keep ? &us : nullptr});
+  END_HANDLE_TH_ERRORS
+}
+
+// (da, uq, us, used, want_du, want_a, rule, group_major, stream)
+PyObject* swiglu_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arity(n, 9);
+  const Tensor &da = tensor(a[0], "da"), &uq = tensor(a[1], "uq"), &us = tensor(a[2], "us");
+  const Tensor* used = tensor_or_none(a[3], "used");
+  rows2d(da, "da");
+  need(xtype(da) >= 0, "da", "must be bf16 or f32");
+  const int64_t M = da.size(0), C = da.size(1);
+  tiles(uq, us, M, 2 * C, da, "uq", "us");
+  one_count(used, da);
+  const bool want_du = truth(a[4]), want_a = truth(a[5]);
+  const c10::DeviceGuard guard(da.device());
+  const Tensor q = make(M, 2 * C, at::kByte, da), s = make_scales(M, 2 * C / 128, truth(a[7]), da);
+  const Tensor du = want_du ? make(M, 2 * C, da.scalar_type(), da) : Tensor();
+  const Tensor act = want_a ? make(M, C, da.scalar_type(), da) : Tensor();
+  check(fp8_swiglu_backward(ptr(da), xtype(da), M, C, pitch(da), ptr<uint8_t>(uq), pitch(uq), ptr<float>(us), us.stride(0),
+                            us.stride(1), ptr<int32_t>(used), small(a[6]), ptr<uint8_t>(q), 2 * C, ptr<float>(s),
+                            s.stride(0), s.stride(1), want_du ? ptr(du) : nullptr, 2 * C, want_a ? ptr(act) : nullptr, C,
+                            handle(a[8])),
+        "fp8_swiglu_backward");
+  return give({&q, &s, want_du ? &du : nullptr, want_a ? &act : nullptr});
+  END_HANDLE_TH_ERRORS
+}
+
+// (da, uq, us, rule, group_major, stream)
+PyObject* swiglu_backward_128x1(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arity(n, 6);
+  const Tensor &da = tensor(a[0], "da"), &uq = tensor(a[1], "uq"), &us = tensor(a[2], "us");
+  rows2d(da, "da");
+  need(xtype(da) >= 0, "da", "must be bf16 or f32");
+  const int64_t M = da.size(0), C = da.size(1);
+  tiles(uq, us, M, 2 * C, da, "uq", "us");
+  const bool gm = truth(a[4]);
+  const c10::DeviceGuard guard(da.device());
+  const Tensor q = make(M, 2 * C, at::kByte, da), s = make_scales(M, 2 * C / 128, gm, da);
+  const Tensor qt = make(2 * C, M, at::kByte, da), st = make_scales(2 * C, M / 128, gm, da);
+  const Tensor at_ = make(C, M, at::kByte, da), as = make_scales(C, M / 128, gm, da);
+  check(fp8_swiglu_backward_128x1(ptr(da), xtype(da), M, C, pitch(da), ptr<uint8_t>(uq), pitch(uq), ptr<float>(us),
+                                  us.stride(0), us.stride(1), small(a[3]), ptr<uint8_t>(q), 2 * C, ptr<float>(s),
+                                  s.stride(0), s.stride(1), ptr<uint8_t>(qt), M, ptr<float>(st), st.stride(0),
+                                  st.stride(1), ptr<uint8_t>(at_), M, ptr<float>(as), as.stride(0), as.stride(1),
+                                  handle(a[5])),
+        "fp8_swiglu_backward_128x1");
+  return give({&q, &s, &qt, &st, &at_, &as});
+  END_HANDLE_TH_ERRORS
+}
+
+// Bounds of sequences; how many there are (one without bounds).
+int64_t sequences(const Tensor* offsets, const Tensor& l) {
+  if (!offsets) return 1;
+  need(offsets->dim() == 1 && offsets->size(0) >= 1 && offsets->is_contiguous() && offsets->scalar_type() == at::kInt &&
+           offsets->device() == l.device(),
+       "offsets", "must be a contiguous int32 vector of sequences + 1 bounds on the logits' device");
+  return offsets->size(0) - 1;
+}
+
+// (logits, idx, offsets, score, scale, stream)
+PyObject* balance_loss(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arity(n, 6);
+  const Tensor &l = tensor(a[0], "logits"), &idx = tensor(a[1], "idx");
+  const Tensor* offsets = tensor_or_none(a[2], "offsets");
+  rows2d(l, "logits");
+  rows2d(idx, "idx");
+  need(xtype(l) >= 0, "logits", "must be bf16 or f32");
+  const int64_t M = l.size(0), E = l.size(1), k = idx.size(1), S = sequences(offsets, l);
+  need(idx.scalar_type() == at::kInt && idx.size(0) == M && idx.device() == l.device(), "idx",
+       "must be int32 [tokens][k] on the logits' device");
+  const c10::DeviceGuard guard(l.device());
+  // 0 bytes: sizes that the call below refuses, saying why; nothing of them is allocated
+  const int64_t bytes = fp8_balance_loss_workspace(M, E, S), out = bytes ? S : 1;
+  const Tensor loss = make1(out, at::kFloat, l), counts = make(out, E, at::kInt, l), slope = make(out, E, at::kFloat, l);
+  const Tensor ws = make1(bytes + 16, at::kByte, l);
+  check(fp8_balance_loss(ptr(l), xtype(l), M, E, pitch(l), ptr<int32_t>(idx), pitch(idx), k, ptr<int32_t>(offsets), S,
+                         small(a[3]), (float)number(a[4]), ptr<float>(loss), ptr<int32_t>(counts), ptr<float>(slope),
+                         ptr(ws), bytes, handle(a[5])),
+        "fp8_balance_loss");
+  return give({&loss, &counts, &slope, &ws});
+  END_HANDLE_TH_ERRORS
+}
+
+// (dloss, logits, slope, offsets, base, score, stream)
+PyObject* balance_loss_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arity(n, 7);
+  const Tensor &l = tensor(a[1], "logits"), &slope = tensor(a[2], "slope");
+  const Tensor *dloss = tensor_or_none(a[0], "dloss"), *offsets = tensor_or_none(a[3], "offsets"),
+               *base = tensor_or_none(a[4], "base");
+  rows2d(l, "logits");
+  need(xtype(l) >= 0, "logits", "must be bf16 or f32");
+  const int64_t M = l.size(0), E = l.size(1), S = sequences(offsets, l);
+  need(slope.dim() == 2 && slope.size(0) == S && slope.size(1) == E && slope.is_contiguous() &&
+           slope.scalar_type() == at::kFloat && slope.device() == l.device(),
+       "slope", "must be contiguous f32 [sequences][experts] on the logits' device");
+  if (dloss)
+    need(dloss->dim() == 1 && dloss->size(0) == S && dloss->is_contiguous() && dloss->scalar_type() == at::kFloat &&
+             dloss->device() == l.device(),
+         "dloss", "must be a contiguous f32 vector of the sequences on the logits' device");
+  like(base, l, "base");
+  const c10::DeviceGuard guard(l.device());
+  const Tensor dl = make(M, E, l.scalar_type(), l);
+  check(fp8_balance_loss_backward(ptr<float>(dloss), ptr(l), xtype(l), M, E, pitch(l), ptr<float>(slope),
+                                  ptr<int32_t>(offsets), S, small(a[5]), ptr(base), pitch(base), ptr(dl), E, handle(a[6])),
+        "fp8_balance_loss_backward");
+  return give({&dl});
+  END_HANDLE_TH_ERRORS
+}
+
+// A gate: none, a vector of the columns of the gammas' type, or rows like x.
+void gate_like(const Tensor* gate, const Tensor& x, const Tensor& gamma) {
+  if (!gate) return;
+  if (gate->dim() == 2) {
+    like(gate, x, "gate");
+    return;
+  }
+  vec1(gate, x.size(1), x, false, "gate");
+  need(gate->scalar_type() == gamma.scalar_type(), "gate", "must have the gammas' type (one value per column) or x's (rows)");
+}
+int64_t gate_pitch(const Tensor* gate) { return gate && gate->dim() == 2 ? pitch(*gate) : 0; }
+
+// (z, r, gamma_post, gamma, gate, residual_scale, block_scale, eps, rule, group_major, want_y, stream)
+PyObject* rmsnorm_block_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arity(n, 12);
+  const Tensor &z = tensor(a[0], "z"), &r = tensor(a[1], "r"), &gp = tensor(a[2], "gamma_post"), &gm = tensor(a[3], "gamma");
+  const Tensor* gate = tensor_or_none(a[4], "gate");
+  rows2d(z, "z");
+  need(xtype(z) >= 0, "z", "must be bf16 or f32");
+  like(&r, z, "r");
+  const int64_t M = z.size(0), C = z.size(1);
+  vec1(&gp, C, z, false, "gamma_post");
+  vec1(&gm, C, z, false, "gamma");
+  need(gp.scalar_type() == gm.scalar_type(), "gamma_post", "must have gamma's type");
+  gate_like(gate, z, gm);
+  const bool want_y = truth(a[10]);
+  const c10::DeviceGuard guard(z.device());
+  const Tensor q = make(M, C, at::kByte, z), s = make_scales(M, C / 128, truth(a[9]), z);
+  const Tensor h = make(M, C, z.scalar_type(), z), y = want_y ? make(M, C, z.scalar_type(), z) : Tensor();
+  const Tensor post = make1(M, at::kFloat, z), rstd = make1(M, at::kFloat, z);
+  check(fp8_rmsnorm_block_quantize(ptr(z), xtype(z), M, C, pitch(z), ptr(r), pitch(r), ptr(gp), ptr(gm), xtype(gm),
+                                   ptr(gate), gate_pitch(gate), (float)number(a[5]), (float)number(a[6]),
+                                   (float)number(a[7]), small(a[8]), ptr(h), C, want_y ? ptr(y) : nullptr, C,
+                                   ptr<uint8_t>(q), C, ptr<float>(s), s.stride(0), s.stride(1), ptr<float>(post),
+                                   ptr<float>(rstd), handle(a[11])),
+        "fp8_rmsnorm_block_quantize");
+  return give({&q, &s, &h, want_y ? &y : nullptr, &post, &rstd});
+  END_HANDLE_TH_ERRORS
+}
+
+// (dy, z, h, gamma_post, gamma, rstd_post, rstd, gate, residual_scale, block_scale, dh, stream)
+PyObject* rmsnorm_block_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arity(n, 12);
+  const Tensor &dy = tensor(a[0], "dy"), &z = tensor(a[1], "z"), &h = tensor(a[2], "h"), &gp = tensor(a[3], "gamma_post"),
+               &gm = tensor(a[4], "gamma"), &post = tensor(a[5], "rstd_post"), &rstd = tensor(a[6], "rstd");
+  const Tensor *gate = tensor_or_none(a[7], "gate"), *dh = tensor_or_none(a[10], "dh");
+  rows2d(h, "h");
+  need(xtype(h) >= 0, "h", "must be bf16 or f32");
+  like(&dy, h, "dy");
+  like(&z, h, "z");
+  like(dh, h, "dh");
+  const int64_t M = h.size(0), C = h.size(1);
+  vec1(&gp, C, h, false, "gamma_post");
+  vec1(&gm, C, h, false, "gamma");
+  need(gp.scalar_type() == gm.scalar_type(), "gamma_post", "must have gamma's type");
+  vec1(&post, M, h, true, "rstd_post");
+  vec1(&rstd, M, h, true, "rstd");
+  gate_like(gate, h, gm);
+  const c10::DeviceGuard guard(h.device());
+  const int64_t bytes = fp8_rmsnorm_block_backward_workspace(M, C), ldg = gate_pitch(gate);
+  const Tensor dz = make(M, C, h.scalar_type(), h), dr = make(M, C, h.scalar_type(), h), ws = make1(bytes + 16, at::kByte, h);
+  const Tensor dgp = make1(C, at::kFloat, h), dgm = make1(C, at::kFloat, h);
+  const Tensor dgate = !gate ? Tensor() : ldg ? make(M, C, h.scalar_type(), h) : make1(C, at::kFloat, h);
+  check(fp8_rmsnorm_block_backward(ptr(dy), xtype(h), M, C, pitch(dy), ptr(dh), pitch(dh), ptr(z), pitch(z), ptr(h),
+                                   pitch(h), ptr(gp), ptr(gm), xtype(gm), ptr(gate), ldg, ptr<float>(post),
+                                   ptr<float>(rstd), (float)number(a[8]), (float)number(a[9]), ptr(dz), C, ptr(dr), C,
+                                   ptr<float>(dgp), ptr<float>(dgm), gate ? ptr(dgate) : nullptr, C, ptr(ws), bytes,
+                                   handle(a[11])),
+        "fp8_rmsnorm_block_backward");
+  return give({&dz, &dr, &dgp, &dgm, gate ? &dgate : nullptr, &ws});
+  END_HANDLE_TH_ERRORS
+}
+
 PyObject* set_error(PyObject*, PyObject* cls) {
   Py_XDECREF(g_error);
   g_error = Py_NewRef(cls);
@@ -349,6 +575,13 @@ PyMethodDef g_methods[] = {FAST(rmsnorm_quantize),
                            FAST(dispatch),
                            FAST(combine),
                            FAST(combine_backward),
+                           FAST(swiglu_quantize),
+                           FAST(swiglu_backward),
+                           FAST(swiglu_backward_128x1),
+                           FAST(balance_loss),
+                           FAST(balance_loss_backward),
+                           FAST(rmsnorm_block_quantize),
+                           FAST(rmsnorm_block_backward),
                            {"set_error", set_error, METH_O, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

@@ -25,6 +25,14 @@ A mixture-of-experts layer around them:
                                       pos i32 [M][k], token i32 [M k]
   combine(z [R][C], pos, w, base)  -> [M][C]
   combine_backward(dy, z, pos, w)  -> dz [R][C], dw [M][k]
+  swiglu_quantize(u [M][2I])       -> q [M][I], s, and the 8-bit checkpoint uq [M][2I], us
+  swiglu_backward(da [M][I], uq, us)       -> dq [M][2I], ds, du, a
+  swiglu_backward_128x1(da, uq, us)        -> dq, ds, dqT [2I][M], dsT, aqT [I][M], asT
+  balance_loss(logits [M][E], idx, offsets i32 [S+1]) -> loss [S], counts i32 [S][E], slope [S][E]
+  balance_loss_backward(dloss, logits, slope, offsets, base) -> dlogits [M][E]
+  rmsnorm_block_quantize(z [M][C], r, gamma_post, gamma, gate) -> q, s, h, y, rstd_post, rstd
+  rmsnorm_block_backward(dy, z, h, gamma_post, gamma, rstd_post, rstd, gate, dh=dh)
+                                   -> dz, dr, dgamma_post [C], dgamma [C], dgate
 These check the shapes, types, devices and row layouts that the C interface
 cannot see and raise ValueError.
 
@@ -270,3 +278,67 @@ def combine_backward(dy, z, pos, w, stream=None):
     row of z in one place)."""
     args = (dy, z, pos, w)
     return _call("combine_backward", stream, z, args, args)
+
+
+def swiglu_quantize(u, used=None, keep=True, pow2=False, scale_layout="group_major", stream=None):
+    """The silu gate of u = [gate | linear half] in E4M3 with 1x128 scales, and
+    with ``keep`` the E4M3 checkpoint of u for swiglu_backward.  ``used``: one
+    int32 value on the device (offsets[-1:] of a dispatch); rows from there on
+    are neither read nor written.  Returns (q, s, uq, us); uq and us are None
+    without keep."""
+    return _call("swiglu_quantize", stream, u, (u, used),
+                 (u, used, keep, _rule(pow2), _of(_LAYOUT, scale_layout, "scale_layout")))
+
+
+def swiglu_backward(da, uq, us, used=None, want_du=False, want_a=False, pow2=False, scale_layout="group_major",
+                    stream=None):
+    """Gradient of swiglu_quantize from its checkpoint, through the quantizers as
+    they are: [dgate | dlin] in E4M3 with 1x128 scales, and if wanted in da's
+    type, and the gate's result formed again in da's type.  Returns (dq, ds, du,
+    a)."""
+    return _call("swiglu_backward", stream, da, (da, uq, us, used),
+                 (da, uq, us, used, want_du, want_a, _rule(pow2), _of(_LAYOUT, scale_layout, "scale_layout")))
+
+
+def swiglu_backward_128x1(da, uq, us, pow2=False, scale_layout="group_major", stream=None):
+    """The same gradient with the operands of both weight gradients: 128x1
+    tiles, transposed, of [dgate | dlin] and of the gate's result (rows a
+    multiple of 128).  Returns (dq, ds, dqT, dsT, aqT, asT)."""
+    return _call("swiglu_backward_128x1", stream, da, (da, uq, us),
+                 (da, uq, us, _rule(pow2), _of(_LAYOUT, scale_layout, "scale_layout")))
+
+
+def balance_loss(logits, idx, offsets=None, score="softmax", scale=1.0, stream=None):
+    """The router's balance loss of each sequence (tokens offsets[s] to
+    offsets[s + 1]; None: all tokens are one), the experts' counts, and
+    the slope that balance_loss_backward takes; see fp8_balance_loss in
+    include/fp8fg.h for the definition, masks and padding.  Returns (loss,
+    counts, slope)."""
+    return _call("balance_loss", stream, logits, (logits, idx, offsets),
+                 (logits, idx, offsets, _of(_SCORE, score, "score"), scale))[:3]
+
+
+def balance_loss_backward(dloss, logits, slope, offsets=None, score="softmax", base=None, stream=None):
+    """Gradient of balance_loss with respect to the logits (dloss None: ones),
+    added to ``base`` (route_backward's result)."""
+    args = (dloss, logits, slope, offsets, base)
+    return _call("balance_loss_backward", stream, logits, args, args + (_of(_SCORE, score, "score"),))[0]
+
+
+def rmsnorm_block_quantize(z, r, gamma_post, gamma, gate=None, residual_scale=1.0, block_scale=1.0, eps=1e-6,
+                           pow2=False, scale_layout="group_major", want_y=False, stream=None):
+    """h = residual_scale * r + block_scale * gate * norm(z), y = norm(h) in E4M3
+    with 1x128 scales; gate: None, [C] of the gammas' type, or [M][C] like z.
+    Returns (q, s, h, y, rstd_post, rstd); y is None unless want_y."""
+    return _call("rmsnorm_block_quantize", stream, z, (z, r, gamma_post, gamma, gate),
+                 (z, r, gamma_post, gamma, gate, residual_scale, block_scale, eps, _rule(pow2),
+                  _of(_LAYOUT, scale_layout, "scale_layout"), want_y))
+
+
+def rmsnorm_block_backward(dy, z, h, gamma_post, gamma, rstd_post, rstd, gate=None, residual_scale=1.0,
+                           block_scale=1.0, dh=None, stream=None):
+    """Gradients of rmsnorm_block_quantize's y (through the quantizer as it is)
+    and, with dh, of its h.  Returns (dz, dr, dgamma_post, dgamma, dgate); dgate
+    is f32 [C], [M][C] of z's type, or None, as the gate is."""
+    return _call("rmsnorm_block_backward", stream, h, (dy, z, h, gamma_post, gamma, rstd_post, rstd, gate, dh),
+                 (dy, z, h, gamma_post, gamma, rstd_post, rstd, gate, residual_scale, block_scale, dh))[:5]

@@ -434,6 +434,191 @@ FP8FG_API int fp8_combine_backward(const void* dy, int type, int64_t z_rows, int
                          int64_t ldz, const int32_t* pos, const float* w, int64_t ldw,
                          void* dz, int64_t lddz, float* dw, int64_t lddw, void* stream);
 
+/*
+ * fp8_swiglu_quantize -- the silu gate between the two products of an expert:
+ * its result as the E4M3 operand of the second product, and its input kept
+ * in E4M3 for the backward pass ([why-be]: E4M3 on all tensors, 1x128 tiles;
+ * the gate's output is formed again from its input instead of being kept).
+ *
+ *   u      : [rows][2 inner] of u_type BF16 or F32, row pitch ldu: the gate g in
+ *            the first inner columns, the linear half l in the others.
+ *   a      = (g * sigmoid(g)) * l in fp32 (where that overflows, the scale is
+ *            infinite)
+ *   q, s   : E4M3 bytes [rows][inner] and 1x128 scales of the fp32 a, by the
+ *            rules of fp8_quantize_rowtile
+ *   uq, us : E4M3 bytes [rows][2 inner] and 1x128 scales of u; uq may be null
+ *            (nothing is kept: serving), us is then ignored.
+ *   used   : DEVICE int32, or null.  Rows from *used on are neither read nor
+ *            written (offsets + G of the grouped GEMM, which leaves them alone
+ *            too); held within [0, rows].
+ *   A row's results do not depend on the other rows or their number.
+ *   Requires inner % 128 == 0.  rows == 0 or inner == 0 is a valid no-op.
+ *   Alignment: u, q, uq 16-byte aligned, their pitches multiples of 16 bytes;
+ *   s, us, used 4-byte aligned.
+ *   Limits (FP8FG_EUNSUPPORTED), here and in the two functions below: rows *
+ *   inner / 128 <= 2^31, rows <= 2^31 - 1, inner <= 2^27; pitches and scale
+ *   strides as above.
+ */
+FP8FG_API int fp8_swiglu_quantize(const void* u, int u_type, int64_t rows, int64_t inner,
+                        int64_t ldu, const int32_t* used, int scale_rule, uint8_t* q,
+                        int64_t ldq, float* s, int64_t s_rs, int64_t s_ts, uint8_t* uq,
+                        int64_t lduq, float* us, int64_t us_rs, int64_t us_ts, void* stream);
+
+/*
+ * fp8_swiglu_backward -- gradient of the gate above from its 8-bit checkpoint,
+ * passed straight through both quantizers.
+ *
+ *   g, l   = RN32(dec(uq) * us)
+ *   dg     = da * l * sg * (1 + g * (1 - sg)),  dl = da * g * sg,
+ *   a      = g * sg * l,  sg = sigmoid(g), in fp32
+ *   da     : [rows][inner] of type BF16 or F32.
+ *   dq, ds : E4M3 bytes [rows][2 inner] and 1x128 scales of [dg | dl] (the
+ *            operand of the first product's data gradient); may be null.
+ *   du     : [dg | dl] in da's type; may be null.
+ *   a      : [rows][inner] in da's type, for the second product's weight
+ *            gradient; may be null.  One of dq, du and a is needed.
+ *   used, alignment and limits as above.
+ */
+FP8FG_API int fp8_swiglu_backward(const void* da, int type, int64_t rows, int64_t inner,
+                        int64_t ldda, const uint8_t* uq, int64_t lduq, const float* us,
+                        int64_t us_rs, int64_t us_ts, const int32_t* used, int scale_rule,
+                        uint8_t* dq, int64_t lddq, float* ds, int64_t ds_rs, int64_t ds_ts,
+                        void* du, int64_t lddu, void* a, int64_t lda, void* stream);
+
+/*
+ * fp8_swiglu_backward_128x1 -- the same gradient with the operands of both
+ * weight gradients ([why-be] backward-pass paragraph: 1x128 -> 128x1 tiles),
+ * formed from the fp32 values in the same pass.
+ *
+ *   dq, ds   : as above.
+ *   dqt, dst : 128x1 tiles of [dg | dl], transposed: bytes [2 inner][rows],
+ *              scales dst[c * dst_rs + (r / 128) * dst_ts]
+ *   aqt, ast : 128x1 tiles of a, transposed: bytes [inner][rows]
+ *   All are written.  Requires rows % 128 == 0 and inner % 128 == 0.
+ *   Limits also: rows / 128 <= 65535.
+ */
+FP8FG_API int fp8_swiglu_backward_128x1(const void* da, int type, int64_t rows, int64_t inner,
+                        int64_t ldda, const uint8_t* uq, int64_t lduq, const float* us,
+                        int64_t us_rs, int64_t us_ts, int scale_rule, uint8_t* dq,
+                        int64_t lddq, float* ds, int64_t ds_rs, int64_t ds_ts, uint8_t* dqt,
+                        int64_t lddqt, float* dst, int64_t dst_rs, int64_t dst_ts,
+                        uint8_t* aqt, int64_t ldaqt, float* ast, int64_t ast_rs,
+                        int64_t ast_ts, void* stream);
+
+/*
+ * fp8_balance_loss -- the loss that keeps a router's experts evenly loaded over
+ * each sequence of tokens, and the experts' counts.
+ *
+ *   logits : [rows][experts] of l_type, row pitch ldl, as fp8_route takes them;
+ *            score is its score.  share[t][i] = s_i / sum_j s_j (softmax: s
+ *            itself).  A logit of -inf or NaN masks its expert, whose share is
+ *            0; a token whose experts are all masked (padding) is not counted.
+ *   idx    : int32 [rows][k], row pitch ld_idx, as fp8_route gives them;
+ *            entries outside [0, experts) are not counted.
+ *   offsets: DEVICE int32 [seqs + 1], nondecreasing (not checked; held within
+ *            the rows): sequence s has the tokens [offsets[s], offsets[s + 1]);
+ *            the others belong to none.  Null: all rows are one sequence, seqs 1.
+ *   Over the n counted tokens of sequence s:
+ *   counts : int32 [seqs][experts], contiguous: entries of idx that name i
+ *   slope  : fp32 [seqs][experts], contiguous: scale * experts / (k n^2) *
+ *            counts, which is d loss / d share; 0 for n == 0
+ *   loss   : fp32 [seqs]: sum_i slope[s][i] * sum_t share[t][i]
+ *   Sums are in a fixed order (fp32 within at most 4096 tokens, fp64 beyond).
+ *   workspace: at least fp8_balance_loss_workspace(rows, experts, seqs) bytes,
+ *            16-byte aligned; FP8FG_ESHAPE if workspace_bytes is less.
+ *   Requires 1 <= k <= experts, scale finite; seqs == 0 is a no-op, rows == 0
+ *   writes zeros.  No alignment beyond the element's.
+ *   Limits (FP8FG_EUNSUPPORTED): experts <= 1024, k <= 64, seqs <= 2^31 - 1;
+ *   rows and pitches as above.
+ */
+FP8FG_API int64_t fp8_balance_loss_workspace(int64_t rows, int64_t experts, int64_t seqs);
+FP8FG_API int fp8_balance_loss(const void* logits, int l_type, int64_t rows, int64_t experts,
+                     int64_t ldl, const int32_t* idx, int64_t ld_idx, int64_t k,
+                     const int32_t* offsets, int64_t seqs, int score, float scale, float* loss,
+                     int32_t* counts, float* slope, void* workspace, int64_t workspace_bytes,
+                     void* stream);
+
+/*
+ * fp8_balance_loss_backward -- gradient of the loss with respect to the logits
+ * (the counts are constant).
+ *
+ *   dloss  : fp32 [seqs], or null (ones).
+ *   slope  : as the forward stored it.
+ *   base   : [rows][experts] of l_type, added (the gradient of fp8_route's
+ *            weights); may be null.
+ *   dlogits: [rows][experts] of l_type, row pitch lddl, overwritten; base's row
+ *            or zeros for a token in no sequence or with all experts masked.
+ *   Other arguments and limits as above.
+ */
+FP8FG_API int fp8_balance_loss_backward(const float* dloss, const void* logits, int l_type,
+                     int64_t rows, int64_t experts, int64_t ldl, const float* slope,
+                     const int32_t* offsets, int64_t seqs, int score, const void* base,
+                     int64_t ldb, void* dlogits, int64_t lddl, void* stream);
+
+/*
+ * fp8_rmsnorm_block_quantize -- from a block's output to the next block's input:
+ * the norm after the block, its gate, the scaled residual addition and the next
+ * norm with an E4M3 output.
+ *
+ *   rstd_post[m] = 1 / sqrt(sum_c z^2 / cols + eps)
+ *   t[m][c]  = ((z * rstd_post) * gamma_post[c]) * gate, in fp32
+ *   h[m][c]  = RN(residual_scale * r + block_scale * t) in x_type
+ *   rstd, y, q, s: the norm of h with gamma, as fp8_rmsnorm_quantize's
+ *
+ *   z, r, h, y : x_type BF16 or F32 with row pitches ldz, ldr, ldh, ldy.  h is
+ *            needed; y, q with s, rstd_post and rstd may be null.
+ *   gamma_post, gamma : [cols], g_type BF16 or F32.
+ *   gate     : null (1), one value per column (ldg == 0: [cols] of g_type) or
+ *            rows (ldg >= cols: [rows][cols] of x_type).
+ *   residual_scale, block_scale : finite.  eps, and rows beyond fp32's range,
+ *            as for fp8_rmsnorm_quantize.
+ *   A row's results do not depend on the other rows or their number.
+ *   Requires cols % 128 == 0.  rows == 0 or cols == 0 is a valid no-op.
+ *   Alignment: all but the scales, rstd_post and rstd (4 bytes) 16-byte
+ *   aligned, pitches multiples of 16 bytes.
+ *   Limits (FP8FG_EUNSUPPORTED): cols <= 16384; the others as for
+ *   fp8_rmsnorm_quantize.
+ */
+FP8FG_API int fp8_rmsnorm_block_quantize(const void* z, int x_type, int64_t rows, int64_t cols,
+                     int64_t ldz, const void* r, int64_t ldr, const void* gamma_post,
+                     const void* gamma, int g_type, const void* gate, int64_t ldg,
+                     float residual_scale, float block_scale, float eps, int scale_rule,
+                     void* h, int64_t ldh, void* y, int64_t ldy, uint8_t* q, int64_t ldq,
+                     float* s, int64_t s_rs, int64_t s_ts, float* rstd_post, float* rstd,
+                     void* stream);
+
+/*
+ * fp8_rmsnorm_block_backward -- its gradient, passed straight through the
+ * quantizer.
+ *
+ *   xh = h * rstd,  a = dy * gamma,  dH = rstd * (a - xh * mean_c(a * xh)) + dh
+ *   zh = z * rstd_post,  b = block_scale * dH * gate
+ *   dr = residual_scale * dH
+ *   dz = rstd_post * (b * gamma_post - zh * mean_c(b * gamma_post * zh))
+ *   dgamma[c] = sum_m dy * xh,  dgamma_post[c] = sum_m b * zh
+ *   dgate = block_scale * dH * zh * gamma_post, for a gate per column summed over m
+ *
+ *   dy, dh, z, h, dz, dr : x_type.  dh (the gradient reaching h along the
+ *            residual stream) may be null.
+ *   rstd_post, rstd : as the forward stored them.
+ *   dgamma_post, dgamma : fp32 [cols], overwritten (zeros for rows == 0).
+ *   dgate    : needed with a gate: fp32 [cols] (ldg == 0; zeros for rows ==
+ *            0) or [rows][cols] of x_type, row pitch lddg.
+ *   workspace: at least fp8_rmsnorm_block_backward_workspace(rows, cols) bytes,
+ *            16-byte aligned: partial sums over the rows, added in a fixed
+ *            order.  FP8FG_ESHAPE if workspace_bytes is less.
+ *   Requires cols % 8 == 0.  Alignment and limits as above.
+ */
+FP8FG_API int64_t fp8_rmsnorm_block_backward_workspace(int64_t rows, int64_t cols);
+FP8FG_API int fp8_rmsnorm_block_backward(const void* dy, int x_type, int64_t rows, int64_t cols,
+                     int64_t lddy, const void* dh, int64_t lddh, const void* z, int64_t ldz,
+                     const void* h, int64_t ldh, const void* gamma_post, const void* gamma,
+                     int g_type, const void* gate, int64_t ldg, const float* rstd_post,
+                     const float* rstd, float residual_scale, float block_scale, void* dz,
+                     int64_t lddz, void* dr, int64_t lddr, float* dgamma_post, float* dgamma,
+                     void* dgate, int64_t lddg, void* workspace, int64_t workspace_bytes,
+                     void* stream);
+
 /* Static, thread-safe description of a status code. */
 FP8FG_API const char* fp8fg_status_string(int status);
 
