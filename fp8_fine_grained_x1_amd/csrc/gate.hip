@@ -25,48 +25,120 @@ namespace fp8fg {
 namespace {
 
 constexpr int kGThreads = 256;
-constexpr int kGroups = kGThreads / 16;
-constexpr int kUnroll = 2;
-constexpr int kGateBlocksPerCu = 28;
 
-// sigmoid(g) and 1 - sigmoid(g)
+// exp(-|..|) in sigmoid(g) = 1 / (1 + exp(-g)): gates are held to [-87, 87] there.  Below
+// -87 the sigmoid stays at 2^-125.5 instead of falling on to 0, above 87 it
+// is 1 in fp32.  r = 1 - s without cancellation.
 struct Sigmoid {
   float s, r;
 };
 __device__ __forceinline__ Sigmoid sigmoid_of(float g) {
-  const float t = exp_neg(-fabsf(g));
-  const float i = __builtin_amdgcn_rcpf(1.0f + t);
-  const float ti = t * i;
-  return {g >= 0.0f ? i : ti, g >= 0.0f ? ti : i};
+  const float x = __builtin_amdgcn_fmed3f(g, -87.0f, 87.0f);
+  const float t = x * -1.44269502f;                       // -x RN32(log2 e)
+  float e = __builtin_fmaf(x, -1.44269502f, -t);          // the product's rounding error
+  e = __builtin_fmaf(x, -1.92596299e-8f, e);              // log2 e - RN32(log2 e)
+  const float c = __builtin_fmaf(e, 0.693147181f, 1.0f);  // 2^e to first order
+  const float p = __builtin_amdgcn_exp2f(t) * c;
+  const float s = __builtin_amdgcn_rcpf(1.0f + p);
+  return {s, p * s};
 }
+__device__ __forceinline__ float silu_of(float g, float s) { return fmaxf(g, -87.0f) * s; }
 
 struct GateParts {
   float dg, dl, a;
 };
 __device__ __forceinline__ GateParts gate_parts(float da, float g, float l) {
   const Sigmoid s = sigmoid_of(g);
-  const float silu = g * s.s;
-  return {da * l * s.s * __builtin_fmaf(g, s.r, 1.0f), da * silu, silu * l};
+  const float silu = silu_of(g, s.s);
+  return {da * l * __builtin_fmaf(silu, s.r, s.s), da * silu, silu * l};
 }
 
-__device__ __forceinline__ float amax8(const float (&v)[8]) {
+template <int N>
+__device__ __forceinline__ float amax_of(const float (&v)[N]) {
   float m = fabsf(v[0]);
 #pragma unroll
-  for (int i = 1; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+  for (int i = 1; i < N; ++i) m = fmaxf(m, fabsf(v[i]));
   return m;
 }
 
-// A 1x128 tile held by 16 lanes, 8 elements each: its bytes and its scale.
-template <int RULE>
-__device__ __forceinline__ void quantize_tile(float (&v)[8], uint8_t* __restrict__ q, float* __restrict__ s) {
-  const float m = row16_max(amax8(v));
+// Four E4M3 bytes of quotients by a scale of finite values: none exceeds
+// 448 (1 + 2^-24), which rounds to 448 by itself.
+__device__ __forceinline__ uint32_t pack4_unclamped(float a, float b, float c, float d) {
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  w = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+  return (uint32_t)w;
+}
+
+// Whether scale_amax and its quotients need none of their steps for tiny
+// scales, infinities and NaN.
+constexpr float kLeastPlain = 0x1p-55f;
+__device__ __forceinline__ bool plain_amax(float m) { return m >= kLeastPlain && m <= 3.40282347e38f; }
+
+// RN(m / 448) and RN(1 / s) of such an m, as scale_amax has them, in 8
+// instructions instead of 26.  Both are correction steps in fused
+// multiply-adds (Markstein, as in div_by_scale): from RN(1 / 448) for every m,
+// and from the hardware's reciprocal for every s -- checked for all 2^23
+// significands.
+__device__ __forceinline__ TileScale plain_scale(float m) {
+  const float inv448 = 1.0f / 448.0f;
+  const float q = m * inv448;
+  const float s = __builtin_fmaf(__builtin_fmaf(-448.0f, q, m), inv448, q);
+  const float y = __builtin_amdgcn_rcpf(s);
+  return {s, s, __builtin_fmaf(__builtin_fmaf(-s, y, 1.0f), y, y), 1.0f};
+}
+
+// N values (a multiple of 4) to E4M3 with the tile's maximum m; `out` gets
+// N / 4 words.  Returns the scale.
+template <int RULE, int N>
+__device__ __forceinline__ float quantize(float (&v)[N], float m, uint32_t (&out)[N / 4]) {
+  if (RULE == 0 && __builtin_amdgcn_ballot_w64(!plain_amax(m)) == 0) {
+    const TileScale sc = plain_scale(m);
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i)
+      out[i] = pack4_unclamped(div_by_scale(v[4 * i], sc.d, sc.y), div_by_scale(v[4 * i + 1], sc.d, sc.y),
+                               div_by_scale(v[4 * i + 2], sc.d, sc.y), div_by_scale(v[4 * i + 3], sc.d, sc.y));
+    return sc.s;
+  }
   const TileScale sc = RULE == 0 ? scale_amax(m) : scale_pow2(m);
-  quotient8<RULE>(v, sc);
-  uint2 out;
-  out.x = pack4_e4m3(v[0], v[1], v[2], v[3]);
-  out.y = pack4_e4m3(v[4], v[5], v[6], v[7]);
-  st_nt8(q, out);
-  if ((threadIdx.x & 15) == 0) *s = sc.s;
+  quotients<RULE, N>(v, sc);
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) out[i] = pack4_e4m3(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  return sc.s;
+}
+
+// 8 lanes own a tile: lane j holds its columns 8 j .. and 64 + 8 j .., so that
+// 8 lanes read 128 contiguous bytes of bf16.
+__device__ __forceinline__ float row8_max(float v) {
+  v = fmaxf(v, dpp_mov<kDppQuadXor1>(v));
+  v = fmaxf(v, dpp_mov<kDppQuadXor2>(v));
+  return fmaxf(v, dpp_mov<kDppRowHalfMirror>(v));
+}
+template <int RULE>
+__device__ __forceinline__ void quantize_tile(float (&v)[16], uint8_t* __restrict__ q, float* __restrict__ s) {
+  uint32_t w[4];
+  const float sc = quantize<RULE, 16>(v, row8_max(amax_of(v)), w);
+  st_nt8(q, make_uint2(w[0], w[1]));
+  st_nt8(q + 64, make_uint2(w[2], w[3]));
+  if ((threadIdx.x & 7) == 0) *s = sc;
+}
+
+template <int XT>
+struct Raw16 {
+  Raw8<XT> a, b;
+};
+template <int XT, bool NT>
+__device__ __forceinline__ Raw16<XT> load_raw16(const void* __restrict__ p, int64_t off) {
+  return {load_raw8<XT, NT>(p, off), load_raw8<XT, NT>(p, off + 64)};
+}
+template <int XT>
+__device__ __forceinline__ void decode_raw16(const Raw16<XT>& r, float (&v)[16]) {
+  decode8<XT>(r.a, v);
+  decode8<XT>(r.b, v + 8);
+}
+template <int XT>
+__device__ __forceinline__ void store_raw16(void* __restrict__ p, int64_t off, const float (&v)[16]) {
+  store_raw8<XT, false>(p, off, encode8<XT>(v));
+  store_raw8<XT, false>(p, off + 64, encode8<XT>(v + 8));
 }
 
 // Rows in use: all of them, or the first *used.
@@ -79,51 +151,34 @@ __device__ __forceinline__ uint32_t rows_used(int64_t rows, const int32_t* used)
 struct GateGrid {
   FastDiv tpr, band;  // tiles of a row's half, of a band of 16 rows
 };
+constexpr int kGroups = kGThreads / 8;
 
-// 16 lanes own a tile of both halves; two tiles per iteration, so that the
-// loads of both are in flight before either is processed.
 template <int XT, int RULE, int ORDER, bool KEEP, bool NT>
 __global__ __launch_bounds__(kGThreads) void gate_kernel(GateArgs p, GateGrid gr) {
-  const int c = (threadIdx.x & 15) * 8;
-  const uint32_t group = blockIdx.x * kGroups + (threadIdx.x >> 4);
-  const uint32_t ngroups = gridDim.x * kGroups;
-  const uint32_t rows = rows_used(p.rows, p.used);
-  const uint32_t ntiles = rows * gr.tpr.d;
-  for (uint32_t t0 = group; t0 < ntiles; t0 += kUnroll * ngroups) {
-    Raw8<XT> g[kUnroll], l[kUnroll];
-    uint32_t r[kUnroll], tc[kUnroll];
+  const uint32_t c = (threadIdx.x & 7) * 8;
+  const uint32_t rows = rows_used(p.rows, p.used), ntiles = rows * gr.tpr.d;
+  for (uint32_t t = blockIdx.x * kGroups + (threadIdx.x >> 3); t < ntiles; t += gridDim.x * kGroups) {
+    uint32_t r, tc;
+    tile_rc<ORDER>(t, gr.tpr, gr.band, rows, r, tc);
+    const int64_t row = r, col = tc * 128 + c;
+    const Raw16<XT> g = load_raw16<XT, NT>(p.u, row * p.ldu + col), l = load_raw16<XT, NT>(p.u, row * p.ldu + p.inner + col);
+    float a[16], b[16], v[16];
+    decode_raw16<XT>(g, a);
+    decode_raw16<XT>(l, b);
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const uint32_t t = t0 + u * ngroups;
-      if (t >= ntiles) continue;
-      tile_rc<ORDER>(t, gr.tpr, gr.band, rows, r[u], tc[u]);
-      const int64_t at = (int64_t)r[u] * p.ldu + tc[u] * 128 + c;
-      g[u] = load_raw8<XT, NT>(p.u, at);
-      l[u] = load_raw8<XT, NT>(p.u, at + p.inner);
-    }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const uint32_t t = t0 + u * ngroups;
-      if (t >= ntiles) continue;
-      float a[8], b[8], v[8];
-      decode8<XT>(g[u], a);
-      decode8<XT>(l[u], b);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = a[i] * sigmoid_of(a[i]).s * b[i];
-      const int64_t row = r[u], col = tc[u] * 128 + c;
-      quantize_tile<RULE>(v, p.q + row * p.ldq + col, p.s + row * p.s_rs + tc[u] * p.s_ts);
-      if constexpr (KEEP) {
-        uint8_t* k = p.uq + row * p.lduq + col;
-        float* ks = p.us + row * p.us_rs + tc[u] * p.us_ts;
-        quantize_tile<RULE>(a, k, ks);
-        quantize_tile<RULE>(b, k + p.inner, ks + (p.inner >> 7) * p.us_ts);
-      }
+    for (int i = 0; i < 16; ++i) v[i] = silu_of(a[i], sigmoid_of(a[i]).s) * b[i];
+    quantize_tile<RULE>(v, p.q + row * p.ldq + col, p.s + row * p.s_rs + tc * p.s_ts);
+    if constexpr (KEEP) {
+      uint8_t* k = p.uq + row * p.lduq + col;
+      float* ks = p.us + row * p.us_rs + tc * p.us_ts;
+      quantize_tile<RULE>(a, k, ks);
+      quantize_tile<RULE>(b, k + p.inner, ks + (p.inner >> 7) * p.us_ts);
     }
   }
 }
 
 // 8 values of a checkpoint: RN32(dec(q) s).
-__device__ __forceinline__ void decode_kept(uint2 w, float s, float (&v)[8]) {
+__device__ __forceinline__ void decode_kept(uint2 w, float s, float* v) {
   float a[4], b[4];
   unpack4_e4m3(w.x, a);
   unpack4_e4m3(w.y, b);
@@ -136,202 +191,190 @@ __device__ __forceinline__ void decode_kept(uint2 w, float s, float (&v)[8]) {
 
 template <int XT, int RULE, int ORDER, bool WIDE, bool NT>
 __global__ __launch_bounds__(kGThreads) void gate_grad_kernel(GateGradArgs p, GateGrid gr) {
-  const int c = (threadIdx.x & 15) * 8;
-  const uint32_t group = blockIdx.x * kGroups + (threadIdx.x >> 4);
-  const uint32_t ngroups = gridDim.x * kGroups;
-  const uint32_t rows = rows_used(p.rows, p.used);
-  const uint32_t ntiles = rows * gr.tpr.d;
+  const uint32_t c = (threadIdx.x & 7) * 8;
+  const uint32_t rows = rows_used(p.rows, p.used), ntiles = rows * gr.tpr.d;
   const int64_t half = p.inner >> 7;
-  for (uint32_t t0 = group; t0 < ntiles; t0 += kUnroll * ngroups) {
-    Raw8<XT> d[kUnroll];
-    uint2 g[kUnroll], l[kUnroll];
-    float gs[kUnroll], ls[kUnroll];
-    uint32_t r[kUnroll], tc[kUnroll];
+  for (uint32_t t = blockIdx.x * kGroups + (threadIdx.x >> 3); t < ntiles; t += gridDim.x * kGroups) {
+    uint32_t r, tc;
+    tile_rc<ORDER>(t, gr.tpr, gr.band, rows, r, tc);
+    const int64_t row = r, col = tc * 128 + c;
+    const Raw16<XT> d = load_raw16<XT, NT>(p.da, row * p.ldda + col);
+    const uint8_t* k = p.uq + row * p.lduq + col;
+    const float* ks = p.us + row * p.us_rs + tc * p.us_ts;
+    const uint2 g0 = ld_nt8(k), g1 = ld_nt8(k + 64), l0 = ld_nt8(k + p.inner), l1 = ld_nt8(k + p.inner + 64);
+    const float gs = *ks, ls = ks[half * p.us_ts];
+    float dg[16], dl[16], a[16];
+    {
+      float x[16], g[16], l[16];
+      decode_raw16<XT>(d, x);
+      decode_kept(g0, gs, g);
+      decode_kept(g1, gs, g + 8);
+      decode_kept(l0, ls, l);
+      decode_kept(l1, ls, l + 8);
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const uint32_t t = t0 + u * ngroups;
-      if (t >= ntiles) continue;
-      tile_rc<ORDER>(t, gr.tpr, gr.band, rows, r[u], tc[u]);
-      const int64_t row = r[u], col = tc[u] * 128 + c;
-      d[u] = load_raw8<XT, NT>(p.da, row * p.ldda + col);
-      const uint8_t* k = p.uq + row * p.lduq + col;
-      const float* ks = p.us + row * p.us_rs + tc[u] * p.us_ts;
-      g[u] = ld_nt8(k);
-      l[u] = ld_nt8(k + p.inner);
-      gs[u] = *ks;
-      ls[u] = ks[half * p.us_ts];
-    }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const uint32_t t = t0 + u * ngroups;
-      if (t >= ntiles) continue;
-      float x[8], gv[8], lv[8], dg[8], dl[8], a[8];
-      decode8<XT>(d[u], x);
-      decode_kept(g[u], gs[u], gv);
-      decode_kept(l[u], ls[u], lv);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const GateParts o = gate_parts(x[i], gv[i], lv[i]);
+      for (int i = 0; i < 16; ++i) {
+        const GateParts o = gate_parts(x[i], g[i], l[i]);
         dg[i] = o.dg;
         dl[i] = o.dl;
         a[i] = o.a;
       }
-      const int64_t row = r[u], col = tc[u] * 128 + c;
-      if constexpr (WIDE) {
-        if (p.du) {
-          store_raw8<XT, false>(p.du, row * p.lddu + col, encode8<XT>(dg));
-          store_raw8<XT, false>(p.du, row * p.lddu + p.inner + col, encode8<XT>(dl));
-        }
-        if (p.a) store_raw8<XT, false>(p.a, row * p.lda + col, encode8<XT>(a));
-        if (!p.q) continue;
-      }
-      uint8_t* q = p.q + row * p.ldq + col;
-      float* s = p.s + row * p.s_rs + tc[u] * p.s_ts;
-      quantize_tile<RULE>(dg, q, s);
-      quantize_tile<RULE>(dl, q + p.inner, s + half * p.s_ts);
     }
+    if constexpr (WIDE) {
+      if (p.du) {
+        store_raw16<XT>(p.du, row * p.lddu + col, dg);
+        store_raw16<XT>(p.du, row * p.lddu + p.inner + col, dl);
+      }
+      if (p.a) store_raw16<XT>(p.a, row * p.lda + col, a);
+      if (!p.q) continue;
+    }
+    uint8_t* q = p.q + row * p.ldq + col;
+    float* s = p.s + row * p.s_rs + tc * p.s_ts;
+    quantize_tile<RULE>(dg, q, s);
+    quantize_tile<RULE>(dl, q + p.inner, s + half * p.s_ts);
   }
 }
 
 // One 128 x 128 block of da per workgroup, with both halves of the
-// checkpoint: thread (rg, cg) holds rows 8 rg .. + 7 of columns 8 cg .. + 7,
-// undecoded.  The first pass forms the rows' values (1x128 tiles: their
-// maxima within 16 lanes, their bytes stored at once) and the columns' maxima
-// (through LDS); the second forms the values again, in column order, and
-// stages the transposed bytes in LDS.
+// checkpoint: thread (rg, cg) holds rows 4 rg .. + 3 of columns 8 cg .. + 7, and
+// dg, dl and a of them in fp32 from their forming to their last use.  Rows'
+// tiles lie in 16 lanes and leave at once; columns' maxima go through LDS, and
+// the transposed bytes are staged there, so that a wave stores whole 128-byte
+// rows.
+constexpr int kTileThreads = 512;
+
 template <int XT, int RULE>
-__global__ __launch_bounds__(kGThreads) void gate_grad_tile_kernel(GateGradTileArgs p) {
+__global__ __launch_bounds__(kTileThreads, 4) void gate_grad_tile_kernel(GateGradTileArgs p) {
   __shared__ __align__(16) uint8_t tbuf[3 * 128 * kTPitch];
-  __shared__ TileScale col_sc[3][128];
+  __shared__ __align__(16) float col_s[3][128], col_y[3][128];
   __shared__ float row_s[2][128];
-  float(*part)[16][128] = reinterpret_cast<float(*)[16][128]>(tbuf);  // 24 of its 54 KB, before the bytes
+  __shared__ int odd;  // a column's scale is not a plain one
+  float(*part)[32][128] = reinterpret_cast<float(*)[32][128]>(tbuf);  // 48 of its 54 KB, before the bytes
 
   const int tid = threadIdx.x, cg = tid & 15, rg = tid >> 4;
   const int64_t r0 = (int64_t)blockIdx.y * 128, c0 = (int64_t)blockIdx.x * 128;
   const int64_t tr = blockIdx.y, tc = blockIdx.x, half = p.inner >> 7;
+  if (tid == 0) odd = 0;
 
-  RawRow<XT> d[8];
-  RawRow<2> g[8], l[8];
-  float gs[8], ls[8];
+  float v[3][4][8];
+  {
+    RawRow<XT> d[4];
+    RawRow<2> g[4], l[4];
+    float gs[4], ls[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t row = r0 + rg * 8 + i, col = c0 + cg * 8;
-    d[i] = load_raw<XT>(p.da, row * p.ldda + col);
-    g[i] = load_raw<2>(p.uq, row * p.lduq + col);
-    l[i] = load_raw<2>(p.uq, row * p.lduq + p.inner + col);
-    gs[i] = p.us[row * p.us_rs + tc * p.us_ts];
-    ls[i] = p.us[row * p.us_rs + (half + tc) * p.us_ts];
-  }
-  auto pair = [&](int i, auto col, GateParts& x, GateParts& y) {
-    constexpr int J = decltype(col)::value;
-    float d0, d1, g0, g1, l0, l1;
-    raw_pair<J>(d[i], d0, d1);
-    raw_pair<J>(g[i], g0, g1);
-    raw_pair<J>(l[i], l0, l1);
-    x = gate_parts(d0, g0 * gs[i], l0 * ls[i]);
-    y = gate_parts(d1, g1 * gs[i], l1 * ls[i]);
-  };
-
-  float mc[3][8] = {};
+    for (int i = 0; i < 4; ++i) {
+      const int64_t row = r0 + rg * 4 + i, col = c0 + cg * 8;
+      d[i] = load_raw<XT>(p.da, row * p.ldda + col);
+      g[i] = load_raw<2>(p.uq, row * p.lduq + col);
+      l[i] = load_raw<2>(p.uq, row * p.lduq + p.inner + col);
+      gs[i] = p.us[row * p.us_rs + tc * p.us_ts];
+      ls[i] = p.us[row * p.us_rs + (half + tc) * p.us_ts];
+    }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float dg[8], dl[8];
-    for_pairs([&](auto col) {
-      constexpr int J = decltype(col)::value;
-      GateParts x, y;
-      pair(i, col, x, y);
-      dg[J] = x.dg;
-      dg[J + 1] = y.dg;
-      dl[J] = x.dl;
-      dl[J + 1] = y.dl;
-      mc[0][J] = fmaxf(mc[0][J], fabsf(x.dg));
-      mc[0][J + 1] = fmaxf(mc[0][J + 1], fabsf(y.dg));
-      mc[1][J] = fmaxf(mc[1][J], fabsf(x.dl));
-      mc[1][J + 1] = fmaxf(mc[1][J + 1], fabsf(y.dl));
-      mc[2][J] = fmaxf(mc[2][J], fabsf(x.a));
-      mc[2][J + 1] = fmaxf(mc[2][J + 1], fabsf(y.a));
-    });
-    uint8_t* q = p.q + (r0 + rg * 8 + i) * p.ldq + c0 + cg * 8;
-    quantize_tile<RULE>(dg, q, &row_s[0][rg * 8 + i]);
-    quantize_tile<RULE>(dl, q + p.inner, &row_s[1][rg * 8 + i]);
+    for (int i = 0; i < 4; ++i)
+      for_pairs([&](auto col) {
+        constexpr int J = decltype(col)::value;
+        float d0, d1, g0, g1, l0, l1;
+        raw_pair<J>(d[i], d0, d1);
+        raw_pair<J>(g[i], g0, g1);
+        raw_pair<J>(l[i], l0, l1);
+        const GateParts x = gate_parts(d0, g0 * gs[i], l0 * ls[i]), y = gate_parts(d1, g1 * gs[i], l1 * ls[i]);
+        v[0][i][J] = x.dg;
+        v[0][i][J + 1] = y.dg;
+        v[1][i][J] = x.dl;
+        v[1][i][J + 1] = y.dl;
+        v[2][i][J] = x.a;
+        v[2][i][J + 1] = y.a;
+      });
   }
 #pragma unroll
-  for (int o = 0; o < 3; ++o)
+  for (int o = 0; o < 3; ++o) {
+    float m[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) part[o][rg][cg * 8 + j] = mc[o][j];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    refresh(d[i]);
-    refresh(g[i]);
-    refresh(l[i]);
+    for (int j = 0; j < 8; ++j)
+      m[j] = fmaxf(fmaxf(fabsf(v[o][0][j]), fabsf(v[o][1][j])), fmaxf(fabsf(v[o][2][j]), fabsf(v[o][3][j])));
+    float* at = &part[o][rg][cg * 8];
+    *reinterpret_cast<float4*>(at) = make_float4(m[0], m[1], m[2], m[3]);
+    *reinterpret_cast<float4*>(at + 4) = make_float4(m[4], m[5], m[6], m[7]);
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int o = 0; o < 2; ++o) {
+      float x[8];
+      uint32_t w[2];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = v[o][i][j];
+      const float sc = quantize<RULE, 8>(x, row16_max(amax_of(x)), w);
+      st_nt8(p.q + (r0 + rg * 4 + i) * p.ldq + o * p.inner + c0 + cg * 8, make_uint2(w[0], w[1]));
+      if (cg == 0) row_s[o][rg * 4 + i] = sc;
+    }
   __syncthreads();
-  // the rows' scales, and the columns'
-  p.s[(r0 + (tid & 127)) * p.s_rs + (tc + (tid >> 7) * half) * p.s_ts] = row_s[tid >> 7][tid & 127];
-  for (int k = tid; k < 3 * 128; k += kGThreads) {
-    const int o = k >> 7, c = k & 127;
+  if (tid < 3 * 128) {
+    const int o = tid >> 7, c = tid & 127;
     float m = part[o][0][c];
 #pragma unroll
-    for (int r = 1; r < 16; ++r) m = fmaxf(m, part[o][r][c]);
+    for (int r = 1; r < 32; ++r) m = fmaxf(m, part[o][r][c]);
     const TileScale sc = RULE == 0 ? scale_amax(m) : scale_pow2(m);
-    col_sc[o][c] = sc;
+    col_s[o][c] = sc.s;
+    col_y[o][c] = sc.y;
+    if (RULE == 0 && !plain_amax(m)) odd = 1;
     if (o < 2)
       p.st[(o * p.inner + c0 + c) * p.st_rs + tr * p.st_ts] = sc.s;
     else
       p.as[(c0 + c) * p.as_rs + tr * p.as_ts] = sc.s;
   }
+  if (tid < 2 * 128) p.s[(r0 + (tid & 127)) * p.s_rs + (tc + (tid >> 7) * half) * p.s_ts] = row_s[tid >> 7][tid & 127];
   __syncthreads();
-  for_pairs([&](auto col) {
-    constexpr int J = decltype(col)::value;
-    float v[3][2][8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      GateParts x, y;
-      pair(i, col, x, y);
-      v[0][0][i] = x.dg;
-      v[0][1][i] = y.dg;
-      v[1][0][i] = x.dl;
-      v[1][1][i] = y.dl;
-      v[2][0][i] = x.a;
-      v[2][1][i] = y.a;
-    }
-#pragma unroll
-    for (int o = 0; o < 3; ++o)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int c = cg * 8 + J + h;
-        quotient8<RULE>(v[o][h], col_sc[o][c]);
-        const float(&w)[8] = v[o][h];
-        uint2 out;
-        out.x = pack4_e4m3(w[0], w[1], w[2], w[3]);
-        out.y = pack4_e4m3(w[4], w[5], w[6], w[7]);
-        const int chunk = (rg >> 1) ^ ((c >> 4) & 7);
-        *reinterpret_cast<uint2*>(tbuf + (o * 128 + c) * kTPitch + chunk * 16 + (rg & 1) * 8) = out;
-      }
-  });
-  __syncthreads();
+  const bool slow = odd != 0;
 #pragma unroll
   for (int o = 0; o < 3; ++o) {
-    uint8_t* out = o < 2 ? p.qt + (o * p.inner + c0) * p.ldqt : p.aq + c0 * p.ldaq;
-    const int64_t ld = o < 2 ? p.ldqt : p.ldaq;
+    float s[8], y[8];
 #pragma unroll
-    for (int it = 0; it < 4; ++it) {
-      const int k = it * kGThreads + tid;
-      const int c = k >> 3, chunk = k & 7;
-      const uint4 w = *reinterpret_cast<const uint4*>(tbuf + (o * 128 + c) * kTPitch + ((chunk ^ ((c >> 4) & 7)) << 4));
-      st_nt16(out + c * ld + r0 + chunk * 16, w);
+    for (int j = 0; j < 8; j += 4) {
+      const float4 a = *reinterpret_cast<const float4*>(&col_s[o][cg * 8 + j]);
+      const float4 b = *reinterpret_cast<const float4*>(&col_y[o][cg * 8 + j]);
+      s[j] = a.x; s[j + 1] = a.y; s[j + 2] = a.z; s[j + 3] = a.w;
+      y[j] = b.x; y[j + 1] = b.y; y[j + 2] = b.z; y[j + 3] = b.w;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = cg * 8 + j;
+      float x[4] = {v[o][0][j], v[o][1][j], v[o][2][j], v[o][3][j]};
+      uint32_t w;
+      if (RULE == 1) {
+        w = pack4_unclamped(x[0] * y[j], x[1] * y[j], x[2] * y[j], x[3] * y[j]);
+      } else if (!slow) {
+        w = pack4_unclamped(div_by_scale(x[0], s[j], y[j]), div_by_scale(x[1], s[j], y[j]), div_by_scale(x[2], s[j], y[j]),
+                            div_by_scale(x[3], s[j], y[j]));
+      } else {
+        const float pre = s[j] < kTinyScale ? kTinyLift : 1.0f;
+        quotients<RULE, 4>(x, TileScale{s[j], s[j] * pre, y[j], pre});
+        w = pack4_e4m3(x[0], x[1], x[2], x[3]);
+      }
+      const int chunk = (rg >> 2) ^ ((c >> 4) & 7);
+      *reinterpret_cast<uint32_t*>(tbuf + (o * 128 + c) * kTPitch + chunk * 16 + (rg & 3) * 4) = w;
     }
   }
+  __syncthreads();
+#pragma unroll
+  for (int it = 0; it < 6; ++it) {
+    const int k = it * kTileThreads + tid, o = it >> 1;
+    const int c = (k >> 3) & 127, chunk = k & 7;
+    uint8_t* out = o < 2 ? p.qt + (o * p.inner + c0 + c) * p.ldqt : p.aq + (c0 + c) * p.ldaq;
+    const uint4 w = *reinterpret_cast<const uint4*>(tbuf + (o * 128 + c) * kTPitch + ((chunk ^ ((c >> 4) & 7)) << 4));
+    st_nt16(out + r0 + chunk * 16, w);
+  }
 }
+
+constexpr int64_t kMaxGateBlocks = 1 << 20;
 
 // Workgroups for `rows` (all of them: how many are in use is known on the
 // device alone) and the tiles' division constants.
 unsigned gate_grid(int64_t rows, int64_t inner, GateGrid& gr) {
-  const int64_t tpr = inner / 128, ntiles = rows * tpr, per = kGroups * kUnroll;
-  const int64_t want = (ntiles + per - 1) / per, cap = (int64_t)device_cu_count() * kGateBlocksPerCu;
+  const int64_t tpr = inner / 128, blocks = (rows * tpr + kGroups - 1) / kGroups;
   gr.tpr = make_fast_div((uint32_t)tpr);
   gr.band = make_fast_div((uint32_t)(16 * tpr));
-  return (unsigned)(want < cap ? want : cap);
+  return (unsigned)(blocks < kMaxGateBlocks ? blocks : kMaxGateBlocks);
 }
 // Bands of 16 rows where the scales of consecutive rows are adjacent (see
 // the 1x128 quantizer).
@@ -373,7 +416,7 @@ hipError_t grad_t(const GateGradArgs& a, hipStream_t st) {
 template <int XT, int RULE>
 hipError_t grad_tile_t(const GateGradTileArgs& a, hipStream_t st) {
   const dim3 grid((unsigned)(a.inner / 128), (unsigned)(a.rows / 128));
-  hipLaunchKernelGGL((gate_grad_tile_kernel<XT, RULE>), grid, dim3(kGThreads), 0, st, a);
+  hipLaunchKernelGGL((gate_grad_tile_kernel<XT, RULE>), grid, dim3(kTileThreads), 0, st, a);
   return hipGetLastError();
 }
 
