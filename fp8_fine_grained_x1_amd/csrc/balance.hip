@@ -30,8 +30,11 @@ namespace fp8fg {
 
 namespace {
 
-constexpr int kPartThreads = 512;
-constexpr int kPartWaves = kPartThreads / 64;
+// Threads of a workgroup that sums tokens: with 16 experts to a lane the registers of
+// 1024 do not hold two tokens.
+template <int NE>
+constexpr int kPartThreads = NE < 16 ? 1024 : 512;
+constexpr int kMostWaves = 16;
 constexpr int kMaxE = kRouteMaxExperts;
 
 // ------------------------------------------------------------- one token
@@ -44,38 +47,34 @@ __device__ __forceinline__ int expert_of(int lane, int i) {
 
 template <int LT, int LPT, int NE, bool VEC>
 __device__ __forceinline__ void load_token(const void* __restrict__ p, int64_t at, int lane, int E, float (&y)[NE]) {
-  if constexpr (VEC) {
+  // (without branches: past the last expert it reads that one again, which is masked)
 #pragma unroll
-    for (int i = 0; i < NE; i += 4) {
-      const int e = expert_of<LPT, true>(lane, i);
-      if (e < E) {
-        if constexpr (LT == 0) {
-          const uint2 w = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(p) + at + e);
-          y[i] = bf16_lo(w.x);
-          y[i + 1] = bf16_hi(w.x);
-          y[i + 2] = bf16_lo(w.y);
-          y[i + 3] = bf16_hi(w.y);
-        } else {
-          const float4 w = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + at + e);
-          y[i] = w.x;
-          y[i + 1] = w.y;
-          y[i + 2] = w.z;
-          y[i + 3] = w.w;
-        }
-      } else {
-        y[i] = y[i + 1] = y[i + 2] = y[i + 3] = -INFINITY;
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < NE; ++i) {
-      const int e = expert_of<LPT, false>(lane, i);
-      y[i] = -INFINITY;
-      if (e < E)
-        y[i] = LT == 0 ? __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(p)[at + e] << 16)
-                       : reinterpret_cast<const float*>(p)[at + e];
+  for (int i = 0; i < NE; i += VEC ? 4 : 1) {
+    const int e = expert_of<LPT, VEC>(lane, i), last = VEC ? E - 4 : E - 1;
+    const int64_t x = at + (e < last ? e : last);
+    if constexpr (VEC && LT == 0) {
+      const uint2 w = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(p) + x);
+      y[i] = bf16_lo(w.x);
+      y[i + 1] = bf16_hi(w.x);
+      y[i + 2] = bf16_lo(w.y);
+      y[i + 3] = bf16_hi(w.y);
+    } else if constexpr (VEC) {
+      const float4 w = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + x);
+      y[i] = w.x;
+      y[i + 1] = w.y;
+      y[i + 2] = w.z;
+      y[i + 3] = w.w;
+    } else {
+      y[i] = LT == 0 ? __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(p)[x] << 16)
+                     : reinterpret_cast<const float*>(p)[x];
     }
   }
+}
+// -inf past the last expert.
+template <int LPT, int NE, bool VEC>
+__device__ __forceinline__ void mask_token(int lane, int E, float (&y)[NE]) {
+#pragma unroll
+  for (int i = 0; i < NE; ++i) y[i] = expert_of<LPT, VEC>(lane, i) < E ? y[i] : -INFINITY;
 }
 
 template <int LT, int LPT, int NE, bool VEC>
@@ -114,42 +113,84 @@ __device__ __forceinline__ float token_max(float v) {
   return v;
 }
 
-// Logits to shares, in place; of a sigmoid also 1 - s into r (REST).  False
-// for a token whose experts are all masked: its shares are 0.
-template <int LPT, int NE, bool REST>
-__device__ __forceinline__ bool token_shares(int score, float (&y)[NE], float (&r)[NE]) {
-  float top = -INFINITY;
+// exp(x) for x <= 60 within 2 ulp, 0 below 2^-126.
+__device__ __forceinline__ float exp_of(float x) {
+  x = fmaxf(x, -120.0f);
+  const float t = x * 1.44269502f;                        // RN32(log2 e)
+  float e = __builtin_fmaf(x, 1.44269502f, -t);
+  e = __builtin_fmaf(x, 1.92596299e-8f, e);               // log2 e - RN32(log2 e)
+  const float p = __builtin_amdgcn_exp2f(t);
+  return __builtin_fmaf(p, e * 0.693147181f, p);
+}
+
+// RN-close 1 / x of a normal x.
+__device__ __forceinline__ float reciprocal(float x) {
+  const float y = __builtin_amdgcn_rcpf(x);
+  return __builtin_fmaf(__builtin_fmaf(-x, y, 1.0f), y, y);
+}
+
+// Scores of a token below its largest logit (softmax), or of one whose
+// sigmoids may all underflow (their common factor exp(min(top, 0)) taken out),
+// and their sum over the token; masked and NaN logits give 0.
+template <int LPT, int NE, int SCORE, bool REST>
+__device__ __forceinline__ float scores_below_top(const float (&l)[NE], float (&y)[NE], float (&r)[NE]) {
+  float top = -INFINITY, total = 0.0f;
 #pragma unroll
   for (int i = 0; i < NE; ++i) {
-    y[i] = y[i] == y[i] ? y[i] : -INFINITY;
+    y[i] = l[i] == l[i] ? l[i] : -INFINITY;
     top = fmaxf(top, y[i]);
   }
   top = token_max<LPT>(top);
+#pragma unroll
+  for (int i = 0; i < NE; ++i) {
+    const float v = y[i];
+    if (SCORE == 0) {
+      y[i] = exp_below(v, top);
+    } else {
+      const float t = exp_of(-fabsf(v)), inv = __builtin_amdgcn_rcpf(1.0f + t);
+      if (REST) r[i] = v >= 0.0f ? t * inv : inv;
+      y[i] = (top < 0.0f ? exp_below(v, top) : v >= 0.0f ? 1.0f : t) * inv;
+    }
+    total += y[i];
+  }
+  return token_sum<LPT>(total);
+}
+
+// Scores of a token's logits, up to a common factor, in y, of a sigmoid also 1 -
+// s in r (REST); returns 1 / their sum, 0 where all experts are masked (live
+// false).
+//
+// They are formed directly first: exp(l) and 1 / (1 + exp(-l)) are within fp32's
+// range unless the logits are far out, and what underflows is below 2^-126 of
+// a sum that is not small.  The sum tells: with one below 1/2, above 2^100 or
+// NaN in the wave (nearly none but the padding's) the scores are formed again
+// below the largest logit.  That maximum and its checks cost half of the
+// instructions.  The forward pass also does without the product's rounding error
+// in the exponent (|l| 2^-24 of a score, and a sequence's sum averages it).
+template <int LPT, int NE, int SCORE, bool REST>
+__device__ __forceinline__ float token_scores(const float (&l)[NE], float (&y)[NE], float (&r)[NE], bool& live) {
   float total = 0.0f;
-  if (score == 0) {
+  live = true;
 #pragma unroll
-    for (int i = 0; i < NE; ++i) {
-      y[i] = exp_below(y[i], top);
-      total += y[i];
+  for (int i = 0; i < NE; ++i) {
+    if (SCORE == 0) {
+      y[i] = REST ? exp_of(fminf(l[i], 100.0f)) : __builtin_amdgcn_exp2f(l[i] * 1.44269502f);
+    } else if (REST) {
+      const float t = exp_of(-fabsf(l[i])), inv = __builtin_amdgcn_rcpf(1.0f + t);
+      r[i] = l[i] >= 0.0f ? t * inv : inv;
+      y[i] = l[i] >= 0.0f ? inv : t * inv;
+    } else {
+      y[i] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(l[i] * -1.44269502f));
     }
-  } else {
-    const bool low = top < 0.0f;  // every score below 1/2
-#pragma unroll
-    for (int i = 0; i < NE; ++i) {
-      const float l = y[i], t = exp_neg(-fabsf(l)), inv = __builtin_amdgcn_rcpf(1.0f + t);
-      if (REST) r[i] = l >= 0.0f ? t * inv : inv;
-      float n = l >= 0.0f ? 1.0f : t;
-      if (low) n = exp_below(l, top);
-      y[i] = n * inv;
-      total += y[i];
-    }
+    total += y[i];
   }
   total = token_sum<LPT>(total);
-  const bool live = top > -INFINITY;
-  const float inv = live ? 1.0f / total : 0.0f;
-#pragma unroll
-  for (int i = 0; i < NE; ++i) y[i] *= inv;
-  return live;
+  if (__builtin_expect(__builtin_amdgcn_ballot_w64(!(total >= (SCORE == 0 ? 1.0f : 0.5f) && total <= 0x1p100f)) != 0, 0)) {
+    total = scores_below_top<LPT, NE, SCORE, REST>(l, y, r);
+    live = total > 0.0f;
+    return live ? reciprocal(total) : 0.0f;
+  }
+  return reciprocal(total);
 }
 
 // ---------------------------------------------------------- sequences
@@ -177,40 +218,84 @@ __device__ __forceinline__ int64_t find_seq(const int32_t* __restrict__ off, int
   return lo;
 }
 
+// 64 consecutive bounds in a wave's lanes, lane i the start of sequence base + i;
+// with fewer than 64 sequences one load serves a whole chunk.
+struct Bounds {
+  int64_t base;
+  int32_t at;  // (rows fit an int32)
+};
+__device__ __forceinline__ Bounds load_bounds(const int32_t* __restrict__ off, int64_t seqs, int64_t rows, int64_t t) {
+  const int lane = threadIdx.x & 63;
+  const int64_t base = seqs < 64 ? 0 : find_seq(off, seqs, rows, t);
+  const int64_t i = base + lane;
+  return {base, (int32_t)bound(off, i < seqs ? i : seqs, rows)};
+}
+struct Seq {
+  int64_t s, first, end;
+};
+// The first sequence of the window that ends behind t; s = seqs where there is
+// none.  t at least the base sequence's predecessor's end.
+__device__ __forceinline__ Seq seq_of(const Bounds& w, int64_t seqs, int64_t t) {
+  const int lane = threadIdx.x & 63;
+  const uint64_t past = __builtin_amdgcn_ballot_w64(lane > 0 && w.base + lane <= seqs && (int64_t)w.at > t);
+  if (past == 0) return {seqs, 0, 0};
+  const int f = __builtin_ctzll(past);
+  return {w.base + f - 1, __builtin_amdgcn_readlane(w.at, f - 1), __builtin_amdgcn_readlane(w.at, f)};
+}
+
 // ------------------------------------------------------- partial sums
 struct BalanceLds {
-  float sum[kPartWaves][kMaxE];
+  float sum[kMostWaves][kMaxE];
   int hist[kMaxE];
-  int live[kPartWaves];
+  int live[kMostWaves];
 };
 
-// Sums of the tokens [a, b) by the whole workgroup: on return thread e's
-// column of `sum` is added by column_sum, hist and live are whole.
+// What a workgroup loads of the tokens from `a` on before it knows how far its
+// piece reaches: one token of each lane group and one entry of idx.
+template <int NE>
+struct Ahead {
+  float y[NE];
+  int entry;
+};
+__device__ __forceinline__ int load_entry(const BalanceArgs& p, const FastDiv& by_k, int64_t a, uint32_t i, int64_t end) {
+  const uint32_t t = fast_div(i, by_k), j = i - t * by_k.d;
+  return a + t < end ? p.idx[(a + t) * p.ld_idx + j] : -1;
+}
 template <int LT, int LPT, int NE, bool VEC>
-__device__ __forceinline__ void sum_tokens(const BalanceArgs& p, FastDiv by_k, int64_t a, int64_t b, BalanceLds& m) {
-  constexpr int kPer = 64 / LPT;  // tokens of a wave
+__device__ __forceinline__ void load_ahead(const BalanceArgs& p, const FastDiv& by_k, int64_t a, int64_t end, Ahead<NE>& h) {
+  const int64_t t = a + threadIdx.x / LPT;
+  load_token<LT, LPT, NE, VEC>(p.logits, (t < end ? t : end - 1) * p.ldl, threadIdx.x & (LPT - 1), p.experts, h.y);
+  h.entry = load_entry(p, by_k, a, threadIdx.x, end);
+}
+
+// Sums of the tokens [a, b), b > a, by the whole workgroup, h loaded from a on:
+// on return thread e's column of `sum` is added by column_sum, hist and
+// live are whole.  The loops are kept rolled: a workgroup runs through this
+// code once or twice, and what it costs then is the fetching of it.
+template <int LT, int LPT, int NE, bool VEC, int SCORE>
+__device__ __forceinline__ void sum_tokens(const BalanceArgs& p, const FastDiv& by_k, int64_t a, int64_t b, Ahead<NE>& h,
+                                           BalanceLds& m) {
+  constexpr int kThreads = kPartThreads<NE>, kStep = kThreads / LPT;
   const int lane = threadIdx.x & (LPT - 1), wave = threadIdx.x >> 6;
-  for (int e = threadIdx.x; e < p.experts; e += blockDim.x) m.hist[e] = 0;
-  __syncthreads();
-  const uint32_t n = (uint32_t)((b - a) * p.k);
-  for (uint32_t i = threadIdx.x; i < n; i += blockDim.x) {
-    const uint32_t t = fast_div(i, by_k), j = i - t * by_k.d;
-    const int e = p.idx[(a + t) * p.ld_idx + j];
-    if ((uint32_t)e < (uint32_t)p.experts) atomicAdd(&m.hist[e], 1);
-  }
-  float acc[NE] = {}, y[NE], none[NE];
+  float acc[NE] = {}, next[NE];
   int live = 0;
-  const int64_t step = (int64_t)(blockDim.x >> 6) * kPer;
-  int64_t t = a + (threadIdx.x / LPT);
-  if (t < b) load_token<LT, LPT, NE, VEC>(p.logits, t * p.ldl, lane, p.experts, y);
-  for (; t < b; t += step) {
-    float next[NE];
-    if (t + step < b) load_token<LT, LPT, NE, VEC>(p.logits, (t + step) * p.ldl, lane, p.experts, next);
-    live += token_shares<LPT, NE, false>(p.score, y, none);
+  const int64_t t0 = a + threadIdx.x / LPT;
+  load_token<LT, LPT, NE, VEC>(p.logits, (t0 + kStep < b ? t0 + kStep : b - 1) * p.ldl, lane, p.experts, next);
+  for (int e = threadIdx.x; e < p.experts; e += kThreads) m.hist[e] = 0;
+#pragma unroll 1
+  for (int64_t t = t0; t < b; t += kStep) {
+    float after[NE], y[NE], none[NE];
+    load_token<LT, LPT, NE, VEC>(p.logits, (t + 2 * kStep < b ? t + 2 * kStep : b - 1) * p.ldl, lane, p.experts, after);
+    mask_token<LPT, NE, VEC>(lane, p.experts, h.y);
+    bool counts;
+    const float inv = token_scores<LPT, NE, SCORE, false>(h.y, y, none, counts);
+    live += counts;
 #pragma unroll
-    for (int i = 0; i < NE; ++i) acc[i] += y[i];
-#pragma unroll
-    for (int i = 0; i < NE; ++i) y[i] = next[i];
+    for (int i = 0; i < NE; ++i) {
+      acc[i] = __builtin_fmaf(y[i], inv, acc[i]);
+      h.y[i] = next[i];
+      next[i] = after[i];
+    }
   }
   // the wave's tokens, then the waves'
 #pragma unroll
@@ -224,16 +309,28 @@ __device__ __forceinline__ void sum_tokens(const BalanceArgs& p, FastDiv by_k, i
   if constexpr (LPT <= 32) live += __shfl_xor(live, 32);
   if ((threadIdx.x & 63) == 0) m.live[wave] = live;
   __syncthreads();
+  const uint32_t n = (uint32_t)((b - a) * p.k);
+  int entry = h.entry;
+#pragma unroll 1
+  for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
+    if ((uint32_t)entry < (uint32_t)p.experts) atomicAdd(&m.hist[entry], 1);
+    entry = load_entry(p, by_k, a, i + kThreads, b);
+  }
+  __syncthreads();
 }
 
+template <int WAVES>
 __device__ __forceinline__ float column_sum(const BalanceLds& m, int e) {
-  float s = m.sum[0][e];
-  for (int w = 1; w < (int)(blockDim.x >> 6); ++w) s += m.sum[w][e];
+  float s = 0.0f;
+#pragma unroll 4
+  for (int w = 0; w < WAVES; ++w) s += m.sum[w][e];
   return s;
 }
+template <int WAVES>
 __device__ __forceinline__ int live_sum(const BalanceLds& m) {
   int s = 0;
-  for (int w = 0; w < (int)(blockDim.x >> 6); ++w) s += m.live[w];
+#pragma unroll 4
+  for (int w = 0; w < WAVES; ++w) s += m.live[w];
   return s;
 }
 
@@ -260,16 +357,22 @@ __device__ __forceinline__ double block_sum64(double v, double* part) {
 }
 
 // Few rows: a workgroup takes a whole sequence.
-template <int LT, int LPT, int NE, bool VEC>
-__global__ __launch_bounds__(kPartThreads) void balance_one_kernel(BalanceArgs p, FastDiv by_k) {
+template <int LT, int LPT, int NE, bool VEC, int SCORE>
+__global__ __launch_bounds__(kPartThreads<NE>) void balance_one_kernel(BalanceArgs p, FastDiv by_k) {
   __shared__ BalanceLds m;
-  __shared__ double part[kPartWaves];
+  __shared__ double part[kMostWaves];
   for (int64_t s = blockIdx.x; s < p.seqs; s += gridDim.x) {
     const int64_t a = bound(p.offsets, s, p.rows), b = bound(p.offsets, s + 1, p.rows);
-    sum_tokens<LT, LPT, NE, VEC>(p, by_k, a, b < a ? a : b, m);
-    const int n = live_sum(m);
+    constexpr int kThreads = kPartThreads<NE>;
+    if (a < b) {
+      Ahead<NE> h;
+      load_ahead<LT, LPT, NE, VEC>(p, by_k, a, b, h);
+      sum_tokens<LT, LPT, NE, VEC, SCORE>(p, by_k, a, b, h, m);
+    }
+    const int n = a < b ? live_sum<kThreads / 64>(m) : 0;
     double v = 0.0;
-    for (int e = threadIdx.x; e < p.experts; e += blockDim.x) v += finish(p, s, e, m.hist[e], n, column_sum(m, e));
+    for (int e = threadIdx.x; e < p.experts; e += kThreads)
+      v += finish(p, s, e, a < b ? m.hist[e] : 0, n, a < b ? column_sum<kThreads / 64>(m, e) : 0.0f);
     v = block_sum64(v, part);
     if (threadIdx.x == 0) p.loss[s] = (float)v;
   }
@@ -282,26 +385,38 @@ struct BalancePieces {
   int32_t* live;          // [chunks + seqs]
 };
 
-template <int LT, int LPT, int NE, bool VEC>
-__global__ __launch_bounds__(kPartThreads) void balance_part_kernel(BalanceArgs p, FastDiv by_k, BalancePieces q) {
+template <int LT, int LPT, int NE, bool VEC, int SCORE>
+__global__ __launch_bounds__(kPartThreads<NE>) void balance_part_kernel(BalanceArgs p, FastDiv by_k, BalancePieces q) {
   __shared__ BalanceLds m;
   for (int64_t c = blockIdx.x; c < q.chunks; c += gridDim.x) {
     const int64_t lo = c * q.chunk, hi = lo + q.chunk < p.rows ? lo + q.chunk : p.rows;
     int64_t at = lo;
+    Bounds w;
+    bool known = false;
     while (at < hi) {
-      const int64_t s = find_seq(p.offsets, p.seqs, p.rows, at);
-      if (s >= p.seqs) break;
-      const int64_t first = bound(p.offsets, s, p.rows), end = bound(p.offsets, s + 1, p.rows);
-      const int64_t a = first > at ? first : at, b = end < hi ? end : hi;
-      at = end > at ? end : at + 1;
-      if (a >= b) continue;
-      sum_tokens<LT, LPT, NE, VEC>(p, by_k, a, b, m);
-      const int64_t piece = c + s;
-      for (int e = threadIdx.x; e < p.experts; e += blockDim.x) {
-        q.sum[piece * p.experts + e] = column_sum(m, e);
+      // (nearly every piece starts where the last one ended: its loads need not wait for the bounds)
+      Ahead<NE> h;
+      load_ahead<LT, LPT, NE, VEC>(p, by_k, at, hi, h);
+      if (!known) w = load_bounds(p.offsets, p.seqs, p.rows, at);
+      const Seq f = seq_of(w, p.seqs, at);
+      if (f.s >= p.seqs) {
+        if (!known || w.base + 64 > p.seqs) break;
+        known = false;
+        continue;
+      }
+      known = true;
+      if (f.first > at) {
+        at = f.first;
+        continue;
+      }
+      const int64_t b = f.end < hi ? f.end : hi, piece = c + f.s;
+      sum_tokens<LT, LPT, NE, VEC, SCORE>(p, by_k, at, b, h, m);
+      at = b;
+      for (int e = threadIdx.x; e < p.experts; e += kPartThreads<NE>) {
+        q.sum[piece * p.experts + e] = column_sum<kPartThreads<NE> / 64>(m, e);
         q.count[piece * p.experts + e] = m.hist[e];
       }
-      if (threadIdx.x == 0) q.live[piece] = live_sum(m);
+      if (threadIdx.x == 0) q.live[piece] = live_sum<kPartThreads<NE> / 64>(m);
       __syncthreads();  // (the next piece writes m again)
     }
   }
@@ -381,39 +496,43 @@ constexpr int kGradThreads = 256;
 
 // A wave takes `run` consecutive tokens (per lane group every kPer-th of
 // them); the next token's logits and base are loaded while this one is formed.
-template <int LT, int LPT, int NE, bool VEC>
+template <int LT, int LPT, int NE, bool VEC, int SCORE>
 __global__ __launch_bounds__(kGradThreads) void balance_grad_kernel(BalanceGradArgs p, int64_t run) {
   constexpr int kPer = 64 / LPT;
   const int lane = threadIdx.x & (LPT - 1), E = p.experts;
   const int64_t wave = (int64_t)blockIdx.x * (kGradThreads / 64) + (threadIdx.x >> 6);
   const int64_t lo = wave * run, hi = lo + run < p.rows ? lo + run : p.rows;
   if (lo >= hi) return;
-  int64_t s = find_seq(p.offsets, p.seqs, p.rows, lo);
   int64_t held = -1;
   float c[NE], y[NE], base[NE];
 #pragma unroll
   for (int i = 0; i < NE; ++i) c[i] = base[i] = 0.0f;
   int64_t t = lo + ((threadIdx.x & 63) / LPT);
-  if (t < hi) {
-    load_token<LT, LPT, NE, VEC>(p.logits, t * p.ldl, lane, E, y);
-    if (p.base) load_token<LT, LPT, NE, VEC>(p.base, t * p.ldb, lane, E, base);
-  }
+  load_token<LT, LPT, NE, VEC>(p.logits, (t < hi ? t : hi - 1) * p.ldl, lane, E, y);
+  if (p.base) load_token<LT, LPT, NE, VEC>(p.base, (t < hi ? t : hi - 1) * p.ldb, lane, E, base);
+  const Seq f = seq_of(load_bounds(p.offsets, p.seqs, p.rows, lo), p.seqs, lo);
+  int64_t s = f.s, first = f.first, end = f.end;
+#pragma unroll 1
   for (; t < hi; t += kPer) {
     float ny[NE], nb[NE];
-    if (t + kPer < hi) {
-      load_token<LT, LPT, NE, VEC>(p.logits, (t + kPer) * p.ldl, lane, E, ny);
-      if (p.base) load_token<LT, LPT, NE, VEC>(p.base, (t + kPer) * p.ldb, lane, E, nb);
-    }
-    if (s < p.seqs && bound(p.offsets, s + 1, p.rows) <= t) {
+    const int64_t n = t + kPer < hi ? t + kPer : t;
+    load_token<LT, LPT, NE, VEC>(p.logits, n * p.ldl, lane, E, ny);
+    if (p.base) load_token<LT, LPT, NE, VEC>(p.base, n * p.ldb, lane, E, nb);
+    if (s < p.seqs && end <= t) {
       // the first sequence behind s that ends past t
       int64_t l = s + 1, h = p.seqs;
+#pragma unroll 1
       while (l < h) {
         const int64_t mid = l + ((h - l) >> 1);
         if (bound(p.offsets, mid + 1, p.rows) > t) h = mid; else l = mid + 1;
       }
       s = l;
+      if (s < p.seqs) {
+        first = bound(p.offsets, s, p.rows);
+        end = bound(p.offsets, s + 1, p.rows);
+      }
     }
-    const int64_t now = s < p.seqs && bound(p.offsets, s, p.rows) <= t ? s : p.seqs;
+    const int64_t now = s < p.seqs && first <= t ? s : p.seqs;
     if (now != held) {
       held = now;
       const float d = now < p.seqs ? p.dloss ? p.dloss[now] : 1.0f : 0.0f;
@@ -423,16 +542,18 @@ __global__ __launch_bounds__(kGradThreads) void balance_grad_kernel(BalanceGradA
         c[i] = now < p.seqs && e < E ? d * p.slope[now * E + e] : 0.0f;
       }
     }
-    float r[NE], o[NE];
-    token_shares<LPT, NE, true>(p.score, y, r);
+    mask_token<LPT, NE, VEC>(lane, E, y);
+    float r[NE], o[NE], share[NE];
+    bool live;
+    const float inv = token_scores<LPT, NE, SCORE, true>(y, share, r, live);
     float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < NE; ++i) m = __builtin_fmaf(c[i], y[i], m);
-    m = token_sum<LPT>(m);
+    for (int i = 0; i < NE; ++i) m = __builtin_fmaf(c[i], share[i], m);
+    m = token_sum<LPT>(m) * inv;
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
-      o[i] = y[i] * (c[i] - m);
-      if (p.score != 0) o[i] *= r[i];
+      o[i] = share[i] * inv * (c[i] - m);
+      if (SCORE != 0) o[i] *= r[i];
       if (p.base) o[i] += base[i];
     }
     store_token<LT, LPT, NE, VEC>(p.dl, t * p.lddl, lane, E, o);
@@ -456,12 +577,12 @@ int64_t chunk_tokens(int64_t rows) {
   return c < 32 ? 32 : c < kMaxChunk ? c : kMaxChunk;
 }
 
-template <int LT, int LPT, int NE, bool VEC>
+template <int LT, int LPT, int NE, bool VEC, int SCORE>
 hipError_t balance_as(const BalanceArgs& a, hipStream_t st) {
   const FastDiv by_k = make_fast_div((uint32_t)a.k);
   const unsigned seqs = (unsigned)(a.seqs < kMaxBlocks ? a.seqs : kMaxBlocks);
   if (a.rows <= kOneRows) {
-    hipLaunchKernelGGL((balance_one_kernel<LT, LPT, NE, VEC>), dim3(seqs), dim3(kPartThreads), 0, st, a, by_k);
+    hipLaunchKernelGGL((balance_one_kernel<LT, LPT, NE, VEC, SCORE>), dim3(seqs), dim3(kPartThreads<NE>), 0, st, a, by_k);
     return hipGetLastError();
   }
   BalancePieces q;
@@ -472,7 +593,7 @@ hipError_t balance_as(const BalanceArgs& a, hipStream_t st) {
   q.count = reinterpret_cast<int32_t*>(q.sum + pieces * a.experts);
   q.live = q.count + pieces * a.experts;
   const unsigned blocks = (unsigned)(q.chunks < kMaxBlocks ? q.chunks : kMaxBlocks);
-  hipLaunchKernelGGL((balance_part_kernel<LT, LPT, NE, VEC>), dim3(blocks), dim3(kPartThreads), 0, st, a, by_k, q);
+  hipLaunchKernelGGL((balance_part_kernel<LT, LPT, NE, VEC, SCORE>), dim3(blocks), dim3(kPartThreads<NE>), 0, st, a, by_k, q);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (a.experts % 4 == 0)
@@ -482,44 +603,48 @@ hipError_t balance_as(const BalanceArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <int LT, int LPT, int NE, bool VEC>
+template <int LT, int LPT, int NE, bool VEC, int SCORE>
 hipError_t grad_as(const BalanceGradArgs& a, hipStream_t st) {
   constexpr int kPer = 64 / LPT;
-  const int64_t waves = (int64_t)device_cu_count() * 32;
+  const int64_t waves = (int64_t)device_cu_count() * 16;
   int64_t run = (a.rows + waves - 1) / waves;
   run = (run + kPer - 1) / kPer * kPer;
   const int64_t per = run * (kGradThreads / 64);
-  hipLaunchKernelGGL((balance_grad_kernel<LT, LPT, NE, VEC>), dim3((unsigned)((a.rows + per - 1) / per)), dim3(kGradThreads),
+  hipLaunchKernelGGL((balance_grad_kernel<LT, LPT, NE, VEC, SCORE>), dim3((unsigned)((a.rows + per - 1) / per)), dim3(kGradThreads),
                      0, st, a, run);
   return hipGetLastError();
 }
 
-// f.template go<LT, LPT, NE, VEC>() by the number of experts.
-template <int LT, bool VEC, typename F>
+// f.template go<LT, LPT, NE, VEC, SCORE>() by the number of experts.
+template <int LT, bool VEC, int SCORE, typename F>
 hipError_t by_experts(int E, F f) {
-  if (E <= 64) return f.template go<LT, 16, 4, VEC>();
-  if (E <= 128) return f.template go<LT, 32, 4, VEC>();
-  if (E <= 256) return f.template go<LT, 64, 4, VEC>();
-  if (E <= 512) return f.template go<LT, 64, 8, VEC>();
-  return f.template go<LT, 64, 16, VEC>();
+  if (E <= 64) return f.template go<LT, 16, 4, VEC, SCORE>();
+  if (E <= 128) return f.template go<LT, 32, 4, VEC, SCORE>();
+  if (E <= 256) return f.template go<LT, 64, 4, VEC, SCORE>();
+  if (E <= 512) return f.template go<LT, 64, 8, VEC, SCORE>();
+  return f.template go<LT, 64, 16, VEC, SCORE>();
+}
+template <int SCORE, typename F>
+hipError_t by_type(int l_type, bool vec, int E, F f) {
+  if (l_type == 0) return vec ? by_experts<0, true, SCORE>(E, f) : by_experts<0, false, SCORE>(E, f);
+  return vec ? by_experts<1, true, SCORE>(E, f) : by_experts<1, false, SCORE>(E, f);
 }
 template <typename F>
-hipError_t choose(int l_type, bool vec, int E, F f) {
-  if (l_type == 0) return vec ? by_experts<0, true>(E, f) : by_experts<0, false>(E, f);
-  return vec ? by_experts<1, true>(E, f) : by_experts<1, false>(E, f);
+hipError_t choose(int l_type, bool vec, int E, int score, F f) {
+  return score == 0 ? by_type<0>(l_type, vec, E, f) : by_type<1>(l_type, vec, E, f);
 }
 
 struct GoBalance {
   const BalanceArgs& a;
   hipStream_t st;
-  template <int LT, int LPT, int NE, bool VEC>
-  hipError_t go() const { return balance_as<LT, LPT, NE, VEC>(a, st); }
+  template <int LT, int LPT, int NE, bool VEC, int SCORE>
+  hipError_t go() const { return balance_as<LT, LPT, NE, VEC, SCORE>(a, st); }
 };
 struct GoGrad {
   const BalanceGradArgs& a;
   hipStream_t st;
-  template <int LT, int LPT, int NE, bool VEC>
-  hipError_t go() const { return grad_as<LT, LPT, NE, VEC>(a, st); }
+  template <int LT, int LPT, int NE, bool VEC, int SCORE>
+  hipError_t go() const { return grad_as<LT, LPT, NE, VEC, SCORE>(a, st); }
 };
 
 // Whether rows of 4 elements at a time are aligned.
@@ -536,13 +661,13 @@ int64_t balance_workspace(int64_t rows, int64_t experts, int64_t seqs) {
 }
 
 hipError_t launch_balance(const BalanceArgs& a, hipStream_t st) {
-  return choose(a.l_type, a.experts % 4 == 0 && fours(a.logits, a.ldl, a.l_type), a.experts, GoBalance{a, st});
+  return choose(a.l_type, a.experts % 4 == 0 && fours(a.logits, a.ldl, a.l_type), a.experts, a.score, GoBalance{a, st});
 }
 
 hipError_t launch_balance_grad(const BalanceGradArgs& a, hipStream_t st) {
   const bool vec = a.experts % 4 == 0 && fours(a.logits, a.ldl, a.l_type) && fours(a.base, a.ldb, a.l_type) &&
                    fours(a.dl, a.lddl, a.l_type);
-  return choose(a.l_type, vec, a.experts, GoGrad{a, st});
+  return choose(a.l_type, vec, a.experts, a.score, GoGrad{a, st});
 }
 
 }  // namespace fp8fg
