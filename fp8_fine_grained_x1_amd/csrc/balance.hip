@@ -380,6 +380,7 @@ __global__ __launch_bounds__(kPartThreads<NE>) void balance_one_kernel(BalanceAr
 
 struct BalancePieces {
   int64_t chunk, chunks;  // tokens of a chunk, chunks
+  FastDiv by_chunk;
   float* sum;             // [chunks + seqs][experts]
   int32_t* count;         // the same
   int32_t* live;          // [chunks + seqs]
@@ -432,59 +433,60 @@ __global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(BalanceArgs 
   __shared__ int counts[kJoinThreads * W];
   __shared__ double part[kJoinThreads / 64];
   __shared__ int lives[kJoinThreads / 64];
-  const int E = p.experts, groups = E / W;
-  int cols = 1;
-  while (cols < groups) cols <<= 1;
-  const int parts = kJoinThreads / cols, g = threadIdx.x & (cols - 1), mine = threadIdx.x / cols;
+  const uint32_t E = p.experts, groups = E / W;
+  const uint32_t shift = groups > 1 ? 32 - __builtin_clz(groups - 1) : 0, cols = 1u << shift;  // columns of threads
+  const uint32_t parts = kJoinThreads >> shift, g = threadIdx.x & (cols - 1), mine = threadIdx.x >> shift;
   for (int64_t s = blockIdx.x; s < p.seqs; s += gridDim.x) {
-    const int64_t a = bound(p.offsets, s, p.rows), b = bound(p.offsets, s + 1, p.rows);
-    const int64_t first = a / q.chunk + s, last = b > a ? (b - 1) / q.chunk + s : first - 1;
+    const uint32_t a = (uint32_t)bound(p.offsets, s, p.rows), b = (uint32_t)bound(p.offsets, s + 1, p.rows);
+    // the sequence's pieces, from the one in a's chunk on
+    const int64_t first = s + fast_div(a, q.by_chunk);
+    const uint32_t pieces = b > a ? fast_div(b - 1, q.by_chunk) - fast_div(a, q.by_chunk) + 1 : 0;
+    const float* sum = q.sum + first * E;
+    const int32_t* count = q.count + first * E;
     double t[W] = {};
     int c[W] = {}, live = 0;
     if (g < groups) {
-#pragma unroll 4
-      for (int64_t i = first + mine; i <= last; i += parts) {
-        float v[W];
-        int w[W];
+#pragma unroll 2
+      for (uint32_t i = mine; i < pieces; i += parts) {
+        const int64_t at = (int64_t)i * E + g * W;
         if constexpr (W == 4) {
-          const float4 f = *reinterpret_cast<const float4*>(q.sum + i * E + g * 4);
-          const int4 n = *reinterpret_cast<const int4*>(q.count + i * E + g * 4);
-          v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
-          w[0] = n.x; w[1] = n.y; w[2] = n.z; w[3] = n.w;
+          const float4 f = *reinterpret_cast<const float4*>(sum + at);
+          const int4 n = *reinterpret_cast<const int4*>(count + at);
+          t[0] += f.x; t[1] += f.y; t[2] += f.z; t[3] += f.w;
+          c[0] += n.x; c[1] += n.y; c[2] += n.z; c[3] += n.w;
         } else {
-          v[0] = q.sum[i * E + g];
-          w[0] = q.count[i * E + g];
-        }
-#pragma unroll
-        for (int x = 0; x < W; ++x) {
-          t[x] += v[x];
-          c[x] += w[x];
+          t[0] += sum[at];
+          c[0] += count[at];
         }
       }
     }
-    for (int64_t i = first + threadIdx.x; i <= last; i += kJoinThreads) live += q.live[i];
+#pragma unroll 1
+    for (uint32_t i = threadIdx.x; i < pieces; i += kJoinThreads) live += q.live[first + i];
 #pragma unroll
     for (int x = 0; x < W; ++x) {
-      sums[(mine * W + x) * cols + g] = t[x];
-      counts[(mine * W + x) * cols + g] = c[x];
+      sums[((mine * W + x) << shift) + g] = t[x];
+      counts[((mine * W + x) << shift) + g] = c[x];
     }
 #pragma unroll
     for (int k = 1; k < 64; k <<= 1) live += __shfl_xor(live, k);
     if ((threadIdx.x & 63) == 0) lives[threadIdx.x >> 6] = live;
     __syncthreads();
     int64_t n = 0;
+#pragma unroll 4
     for (int w = 0; w < kJoinThreads / 64; ++w) n += lives[w];
     double v = 0.0;
-    for (int i = threadIdx.x; i < cols * W; i += kJoinThreads) {
-      const int gi = i & (cols - 1), x = i / cols;
+#pragma unroll 1
+    for (uint32_t i = threadIdx.x; i < cols * W; i += kJoinThreads) {
+      const uint32_t gi = i & (cols - 1), x = i >> shift;
       if (gi >= groups) continue;
       double total = 0.0;
-      int count = 0;
-      for (int r = 0; r < parts; ++r) {
-        total += sums[(r * W + x) * cols + gi];
-        count += counts[(r * W + x) * cols + gi];
+      int all = 0;
+#pragma unroll 4
+      for (uint32_t r = 0; r < parts; ++r) {
+        total += sums[((r * W + x) << shift) + gi];
+        all += counts[((r * W + x) << shift) + gi];
       }
-      v += finish(p, s, gi * W + x, count, n, total);
+      v += finish(p, s, gi * W + x, all, n, total);
     }
     v = block_sum64(v, part);
     if (threadIdx.x == 0) p.loss[s] = (float)v;
@@ -588,6 +590,7 @@ hipError_t balance_as(const BalanceArgs& a, hipStream_t st) {
   BalancePieces q;
   q.chunk = chunk_tokens(a.rows);
   q.chunks = (a.rows + q.chunk - 1) / q.chunk;
+  q.by_chunk = make_fast_div((uint32_t)q.chunk);
   const int64_t pieces = q.chunks + a.seqs;
   q.sum = reinterpret_cast<float*>(a.workspace);
   q.count = reinterpret_cast<int32_t*>(q.sum + pieces * a.experts);
