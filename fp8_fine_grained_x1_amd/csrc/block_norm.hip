@@ -136,95 +136,125 @@ __global__ __launch_bounds__(512) void block_norm_kernel(BlockNormArgs p) {
 // A workgroup takes the rows blockIdx.x, blockIdx.x + gridDim.x, ..; its
 // threads keep their columns' part of the two sums over rows in registers
 // (D = sum dH zh, with a gate of rows sum dH zh gate; and sum dy xh) and
-// write them once.
+// write them once.  The next row is loaded while this one is worked on
+// (PREFETCH, rows of up to 8192 columns), since one workgroup fills a CU.
+template <int XT, int NV, int GATE>
+struct BlockRow {
+  Unit<XT, kPer16<XT>> d[NV], h[NV], z[NV], b[NV], g[GATE == kGateRows ? NV : 1];
+  float rstd, post;
+};
+
 template <int XT, int NV, int GATE, bool NT>
-__global__ __launch_bounds__(512) void block_norm_grad_kernel(BlockNormGradArgs p) {
+__device__ __forceinline__ void load_block_row(const BlockNormGradArgs& p, int64_t row, int nvec, BlockRow<XT, NV, GATE>& r) {
+  constexpr int N = kPer16<XT>;
+  r.rstd = p.rstd[row];
+  r.post = p.rstd_post[row];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int v = threadIdx.x + i * blockDim.x;
+    if (v >= nvec) continue;
+    r.d[i] = load_unit<XT, NT, N>(p.dy, row * p.lddy, v);
+    r.h[i] = load_unit<XT, NT, N>(p.h, row * p.ldh, v);
+    r.z[i] = load_unit<XT, NT, N>(p.z, row * p.ldz, v);
+    if (p.dh) r.b[i] = load_unit<XT, NT, N>(p.dh, row * p.lddh, v);
+    if (GATE == kGateRows) r.g[i] = load_unit<XT, NT, N>(p.gate, row * p.ldg, v);
+  }
+}
+
+template <int XT, int NV, int GATE, bool NT, bool PREFETCH>
+__global__ __launch_bounds__(1024) void block_norm_grad_kernel(BlockNormGradArgs p) {
   constexpr int N = kPer16<XT>;
   __shared__ float part[2][kMaxWaves];
   const int nvec = (int)(p.cols / N);
   const float inv_cols = 1.0f / (float)p.cols;
-  float acc[2][NV][N];
+  // gamma, and what dH is multiplied by on its way to z (without a gate of
+  // rows): kept, or for the widest rows loaded at each use
+  constexpr int KEPT = PREFETCH ? NV : 1;
+  float gm[KEPT][N], gp[KEPT][N], acc[2][NV][N];
+  auto load_gm = [&](int i, int v) {
+    decode_gamma<N>(load_gamma<N>(p.gamma, p.g_type, v), p.g_type, gm[i]);
+  };
+  auto load_gp = [&](int i, int v) {
+    decode_gamma<N>(load_gamma<N>(p.gamma_post, p.g_type, v), p.g_type, gp[i]);
+    float g[N];
+    if (GATE == kGateCols) decode_gamma<N>(load_gamma<N>(p.gate, p.g_type, v), p.g_type, g);
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+    for (int e = 0; e < N; ++e) gp[i][e] *= GATE == kGateCols ? p.block_scale * g[e] : p.block_scale;
+  };
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int v = threadIdx.x + i * blockDim.x;
 #pragma unroll
     for (int e = 0; e < N; ++e) acc[0][i][e] = acc[1][i][e] = 0.0f;
-  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-    const float rstd = p.rstd[row], post = p.rstd_post[row];
-    Unit<XT, N> d[NV], h[NV], z[NV], b[NV], gr[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = threadIdx.x + i * blockDim.x;
-      if (v >= nvec) continue;
-      d[i] = load_unit<XT, NT, N>(p.dy, row * p.lddy, v);
-      h[i] = load_unit<XT, NT, N>(p.h, row * p.ldh, v);
-      z[i] = load_unit<XT, NT, N>(p.z, row * p.ldz, v);
-      if (p.dh) b[i] = load_unit<XT, NT, N>(p.dh, row * p.lddh, v);
-      if (GATE == kGateRows) gr[i] = load_unit<XT, NT, N>(p.gate, row * p.ldg, v);
-    }
+    if (!PREFETCH || v >= nvec) continue;
+    load_gm(i, v);
+    load_gp(i, v);
+  }
+  BlockRow<XT, NV, GATE> r;
+  int64_t row = blockIdx.x;
+  if (PREFETCH && row < p.rows) load_block_row<XT, NV, GATE, NT>(p, row, nvec, r);
+  for (; row < p.rows; row += gridDim.x) {
+    if (!PREFETCH) load_block_row<XT, NV, GATE, NT>(p, row, nvec, r);
     float c = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
       if (v >= nvec) continue;
-      float dy[N], x[N], g[N];
-      decode_unit<XT, N>(d[i], dy);
-      decode_unit<XT, N>(h[i], x);
-      decode_gamma<N>(load_gamma<N>(p.gamma, p.g_type, v), p.g_type, g);
+      float dy[N], x[N];
+      decode_unit<XT, N>(r.d[i], dy);
+      decode_unit<XT, N>(r.h[i], x);
+      if (!PREFETCH) load_gm(0, v);
 #pragma unroll
       for (int e = 0; e < N; ++e) {
-        const float dx = dy[e] * (x[e] * rstd);
-        c = __builtin_fmaf(dx, g[e], c);
+        const float dx = dy[e] * (x[e] * r.rstd);
+        c = __builtin_fmaf(dx, gm[i % KEPT][e], c);
         acc[1][i][e] += dx;
       }
     }
+    BlockRow<XT, NV, GATE> next;
+    if (PREFETCH && row + gridDim.x < p.rows) load_block_row<XT, NV, GATE, NT>(p, row + gridDim.x, nvec, next);
     c = block_sum(c, part[0]) * inv_cols;
-    // dH, kept as b gamma_post (b = block_scale dH gate), and the second mean
+    // dH, then w = block_scale dH gate gamma_post and its mean with zh
     float w[NV][N], m = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
       if (v >= nvec) continue;
-      float dy[N], x[N], zv[N], g[N], o[N];
-      decode_unit<XT, N>(d[i], dy);
-      decode_unit<XT, N>(h[i], x);
-      decode_unit<XT, N>(z[i], zv);
-      decode_gamma<N>(load_gamma<N>(p.gamma, p.g_type, v), p.g_type, g);
+      float x[N], zv[N], o[N];
+      decode_unit<XT, N>(r.d[i], o);
+      decode_unit<XT, N>(r.h[i], x);
+      decode_unit<XT, N>(r.z[i], zv);
+      if (!PREFETCH) {
+        load_gm(0, v);
+        load_gp(0, v);
+      }
 #pragma unroll
-      for (int e = 0; e < N; ++e) o[e] = rstd * __builtin_fmaf(-(x[e] * rstd), c, dy[e] * g[e]);
+      for (int e = 0; e < N; ++e) o[e] = r.rstd * __builtin_fmaf(-(x[e] * r.rstd), c, o[e] * gm[i % KEPT][e]);
       if (p.dh) {
-        decode_unit<XT, N>(b[i], x);
+        decode_unit<XT, N>(r.b[i], x);
 #pragma unroll
         for (int e = 0; e < N; ++e) o[e] += x[e];
       }
 #pragma unroll
       for (int e = 0; e < N; ++e) x[e] = p.residual_scale * o[e];
       store_unit<XT, N>(p.dr, row * p.lddr, v, x);
-      decode_gamma<N>(load_gamma<N>(p.gamma_post, p.g_type, v), p.g_type, g);
-      if (GATE == kGateRows) {
+#pragma unroll
+      for (int e = 0; e < N; ++e) zv[e] *= r.post;
+      if constexpr (GATE == kGateRows) {
         float gv[N];
-        decode_unit<XT, N>(gr[i], gv);
+        decode_unit<XT, N>(r.g[i], gv);
 #pragma unroll
         for (int e = 0; e < N; ++e) {
-          const float t = o[e] * (zv[e] * post);
-          x[e] = p.block_scale * t * g[e];
+          x[e] = o[e] * zv[e] * gp[i % KEPT][e];
           o[e] *= gv[e];
-          acc[0][i][e] = __builtin_fmaf(t, gv[e], acc[0][i][e]);
         }
         store_unit<XT, N>(p.dgate, row * p.lddg, v, x);
-      } else {
-#pragma unroll
-        for (int e = 0; e < N; ++e) acc[0][i][e] = __builtin_fmaf(o[e], zv[e] * post, acc[0][i][e]);
-      }
-      if (GATE == kGateCols) {
-        float gv[N];
-        decode_gamma<N>(load_gamma<N>(p.gate, p.g_type, v), p.g_type, gv);
-#pragma unroll
-        for (int e = 0; e < N; ++e) o[e] *= gv[e];
       }
 #pragma unroll
       for (int e = 0; e < N; ++e) {
-        w[i][e] = p.block_scale * o[e] * g[e];
-        m = __builtin_fmaf(w[i][e], zv[e] * post, m);
+        acc[0][i][e] = __builtin_fmaf(o[e], zv[e], acc[0][i][e]);
+        w[i][e] = o[e] * gp[i % KEPT][e];
+        m = __builtin_fmaf(w[i][e], zv[e], m);
       }
     }
     m = block_sum(m, part[1]) * inv_cols;
@@ -233,11 +263,12 @@ __global__ __launch_bounds__(512) void block_norm_grad_kernel(BlockNormGradArgs 
       const int v = threadIdx.x + i * blockDim.x;
       if (v >= nvec) continue;
       float zv[N], o[N];
-      decode_unit<XT, N>(z[i], zv);
+      decode_unit<XT, N>(r.z[i], zv);
 #pragma unroll
-      for (int e = 0; e < N; ++e) o[e] = post * __builtin_fmaf(-(zv[e] * post), m, w[i][e]);
+      for (int e = 0; e < N; ++e) o[e] = r.post * __builtin_fmaf(-(zv[e] * r.post), m, w[i][e]);
       store_unit<XT, N>(p.dz, row * p.lddz, v, o);
     }
+    if (PREFETCH) r = next;
   }
   const int64_t strips = gridDim.x;
 #pragma unroll
@@ -326,15 +357,14 @@ hipError_t norm_t(const BlockNormArgs& a, hipStream_t st) {
 
 template <int XT, int GATE, bool NT>
 hipError_t grad_as(const BlockNormGradArgs& a, hipStream_t st) {
-  constexpr int U = 8 / kPer16<XT>;
-  const RowShape sh = row_shape(a.cols);
-  const dim3 grid((unsigned)block_norm_strips(a.rows, a.cols)), block(sh.threads);
-  if (sh.per == 1)
-    hipLaunchKernelGGL((block_norm_grad_kernel<XT, U, GATE, NT>), grid, block, 0, st, a);
-  else if (sh.per == 2)
-    hipLaunchKernelGGL((block_norm_grad_kernel<XT, 2 * U, GATE, NT>), grid, block, 0, st, a);
+  constexpr int U = 8 / kPer16<XT>;  // units of 8 elements
+  const int64_t groups = a.cols / 8;
+  const int per = groups <= 1024 ? 1 : 2;
+  const dim3 grid((unsigned)block_norm_strips(a.rows, a.cols)), block((unsigned)((groups + per - 1) / per + 63) / 64 * 64);
+  if (per == 1)
+    hipLaunchKernelGGL((block_norm_grad_kernel<XT, U, GATE, NT, true>), grid, block, 0, st, a);
   else
-    hipLaunchKernelGGL((block_norm_grad_kernel<XT, 4 * U, GATE, NT>), grid, block, 0, st, a);
+    hipLaunchKernelGGL((block_norm_grad_kernel<XT, 2 * U, GATE, NT, false>), grid, block, 0, st, a);
   return hipGetLastError();
 }
 
@@ -366,7 +396,11 @@ struct GoGrad {
 
 }  // namespace
 
-int64_t block_norm_strips(int64_t rows, int64_t cols) { return norm_grad_strips(rows, cols); }
+int64_t block_norm_strips(int64_t rows, int64_t cols) {
+  const int64_t most = cols > 4096 ? 256 : cols > 2048 ? 512 : 1024;
+  const int64_t n = rows < 64 ? rows : rows < 256 ? 64 : (rows + 3) / 4;
+  return n < most ? n : most;
+}
 
 hipError_t launch_block_norm(const BlockNormArgs& a, hipStream_t st) {
   return choose(a.x_type, a.gate, a.ldg, GoNorm{a, st});
