@@ -23,6 +23,7 @@
 #include "device_common.h"
 #include "launch.h"
 #include "norm_common.h"
+#include "tiles.h"
 
 namespace fp8fg {
 
@@ -31,105 +32,134 @@ namespace {
 enum { kGateNone = 0, kGateCols = 1, kGateRows = 2 };
 
 template <int XT, int NV>
-__device__ __forceinline__ float rstd_of(const Raw8<XT> (&raw)[NV], float ss, int nvec, int64_t cols, float eps, double* wide) {
-  const float mean = ss / (float)cols + eps;
+__device__ __forceinline__ float rstd_of(const Raw8<XT> (&raw)[NV], float ss, float inv_cols, int nvec, int64_t cols, float eps,
+                                         double* wide) {
+  const float mean = __builtin_fmaf(ss, inv_cols, eps);
   if (__builtin_expect(!(mean >= kLeastMean && mean <= FLT_MAX), 0)) return wide_range_rstd<XT, NV>(raw, nvec, cols, eps, wide);
-  return 1.0f / sqrtf(mean);
+  // the hardware's root (1 ulp) and one Newton step, y + y (1 - mean y^2) / 2: within an ulp, in 5
+  // instructions; a root and a quotient take 50, which every wave of the row
+  // runs twice between two barriers
+  const float y = __builtin_amdgcn_rsqf(mean), my = mean * y;
+  return __builtin_fmaf(__builtin_fmaf(-my, y, 1.0f) * 0.5f, y, y);
 }
 
-// One row per workgroup iteration, as in norm_kernel: thread t holds the
-// 8-element vectors t, t + blockDim, ..
+// Thread t holds the 8-element vectors t, t + blockDim, .. of its rows
+// blockIdx.x, blockIdx.x + gridDim.x, ..: 16 consecutive lanes hold one 1x128
+// tile.  With one vector to a thread (up to 8192 columns: AHEAD) the gammas
+// stay in registers and the next row is loaded while this one is worked on.
+template <int XT, int NV, int GATE>
+struct BlockIn {
+  Raw8<XT> z[NV], r[NV], g[GATE == kGateRows ? NV : 1];
+};
 template <int XT, int NV, int GATE, bool STREAM>
-__global__ __launch_bounds__(512) void block_norm_kernel(BlockNormArgs p) {
+__device__ __forceinline__ void load_block_in(const BlockNormArgs& p, int64_t row, int nvec, BlockIn<XT, NV, GATE>& in) {
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int v = threadIdx.x + i * blockDim.x;
+    if (v >= nvec) continue;
+    in.z[i] = load_raw8<XT, STREAM>(p.z, row * p.ldz + v * 8);
+    in.r[i] = load_raw8<XT, STREAM>(p.r, row * p.ldr + v * 8);
+    if (GATE == kGateRows) in.g[i] = load_raw8<XT, STREAM>(p.gate, row * p.ldg + v * 8);
+  }
+}
+
+template <int XT, int NV, int GATE, bool STREAM>
+__global__ __launch_bounds__(1024) void block_norm_kernel(BlockNormArgs p) {
+  constexpr bool AHEAD = NV == 1;
   __shared__ float part[2][kMaxWaves];
   __shared__ double wide[kMaxWaves];
   const int nvec = (int)(p.cols >> 3);
-  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-    Raw8<XT> z[NV], r[NV], gr[NV];
+  const float inv_cols = 1.0f / (float)p.cols;
+  float gm[8], gp[8];  // gamma; block_scale gamma_post (gate per column)
+  RawGamma<8> raw_gm, raw_gp, raw_gate;
+  auto load_gammas = [&](int v) {
+    raw_gp = load_gamma<8>(p.gamma_post, p.g_type, v);
+    if (GATE == kGateCols) raw_gate = load_gamma<8>(p.gate, p.g_type, v);
+    raw_gm = load_gamma<8>(p.gamma, p.g_type, v);
+  };
+  auto decode_gammas = [&]() {
+    float g[8];
+    decode_gamma<8>(raw_gp, p.g_type, gp);
+    if (GATE == kGateCols) decode_gamma<8>(raw_gate, p.g_type, g);
+    decode_gamma<8>(raw_gm, p.g_type, gm);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) gp[e] *= GATE == kGateCols ? p.block_scale * g[e] : p.block_scale;
+  };
+  BlockIn<XT, NV, GATE> in;
+  int64_t row = blockIdx.x;
+  if (AHEAD) {
+    load_block_in<XT, NV, GATE, STREAM>(p, row, nvec, in);
+    if ((int)threadIdx.x < nvec) load_gammas(threadIdx.x);
+  }
+  for (; row < p.rows; row += gridDim.x) {
+    if (!AHEAD) load_block_in<XT, NV, GATE, STREAM>(p, row, nvec, in);
     float ss = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
       if (v >= nvec) continue;
-      z[i] = load_raw8<XT, STREAM>(p.z, row * p.ldz + v * 8);
-      r[i] = load_raw8<XT, STREAM>(p.r, row * p.ldr + v * 8);
-      if (GATE == kGateRows) gr[i] = load_raw8<XT, STREAM>(p.gate, row * p.ldg + v * 8);
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = threadIdx.x + i * blockDim.x;
-      if (v >= nvec) continue;
       float f[8];
-      decode8<XT>(z[i], f);
+      decode8<XT>(in.z[i], f);
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss += f[e] * f[e];
     }
+    BlockIn<XT, NV, GATE> next;
+    if (AHEAD && row + gridDim.x < p.rows) load_block_in<XT, NV, GATE, STREAM>(p, row + gridDim.x, nvec, next);
     ss = block_sum(ss, part[0]);
-    const float post = rstd_of<XT, NV>(z, ss, nvec, p.cols, p.eps, wide);
+    const float post = rstd_of<XT, NV>(in.z, ss, inv_cols, nvec, p.cols, p.eps, wide);
     ss = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
       if (v >= nvec) continue;
-      float f[8], g[8], x[8];
-      decode8<XT>(z[i], f);
-      decode_gamma<8>(load_gamma<8>(p.gamma_post, p.g_type, v), p.g_type, g);
+      float f[8], x[8];
+      if (!AHEAD) load_gammas(v);
+      if (!AHEAD || row == blockIdx.x) decode_gammas();
+      decode8<XT>(in.z[i], f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = f[e] * post * g[e];
-      if (GATE != kGateNone) {
-        if (GATE == kGateCols)
-          decode_gamma<8>(load_gamma<8>(p.gate, p.g_type, v), p.g_type, g);
-        else
-          decode8<XT>(gr[i], g);
+      for (int e = 0; e < 8; ++e) f[e] = f[e] * post * gp[e];
+      if constexpr (GATE == kGateRows) {
+        decode8<XT>(in.g[i], x);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] *= g[e];
+        for (int e = 0; e < 8; ++e) f[e] *= x[e];
       }
-      decode8<XT>(r[i], x);
+      decode8<XT>(in.r[i], x);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = p.residual_scale * x[e] + p.block_scale * f[e];
-      r[i] = encode8<XT>(x);
-      store_raw8<XT, false>(p.h, row * p.ldh + v * 8, r[i]);
-      decode8<XT>(r[i], x);
+      for (int e = 0; e < 8; ++e) x[e] = __builtin_fmaf(p.residual_scale, x[e], f[e]);
+      in.r[i] = encode8<XT>(x);
+      store_raw8<XT, STREAM>(p.h, row * p.ldh + v * 8, in.r[i]);
+      decode8<XT>(in.r[i], x);
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss += x[e] * x[e];
     }
     ss = block_sum(ss, part[1]);
-    const float rstd = rstd_of<XT, NV>(r, ss, nvec, p.cols, p.eps, wide);
+    const float rstd = rstd_of<XT, NV>(in.r, ss, inv_cols, nvec, p.cols, p.eps, wide);
     if (threadIdx.x == 0) {
       if (p.rstd_post) p.rstd_post[row] = post;
       if (p.rstd) p.rstd[row] = rstd;
     }
-    if (!p.q && !p.y) continue;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
-      if (v >= nvec) continue;
-      float f[8], g[8];
-      decode8<XT>(r[i], f);
-      decode_gamma<8>(load_gamma<8>(p.gamma, p.g_type, v), p.g_type, g);
+      if (v >= nvec || (!p.q && !p.y)) continue;
+      float f[8];
+      if (!AHEAD) {
+        load_gammas(v);
+        decode_gammas();
+      }
+      decode8<XT>(in.r[i], f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = f[e] * rstd * g[e];
-      if (p.y) store_raw8<XT, false>(p.y, row * p.ldy + v * 8, encode8<XT>(f));
+      for (int e = 0; e < 8; ++e) f[e] = f[e] * rstd * gm[e];
+      if (p.y) store_raw8<XT, STREAM>(p.y, row * p.ldy + v * 8, encode8<XT>(f));
       if (p.q) {
-        float m = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]));
-        m = row16_max(m);
-        TileScale sc;
-        if (p.rule == 0) {
-          sc = scale_amax(m);
-          quotient8<0>(f, sc);
-        } else {
-          sc = scale_pow2(m);
-          quotient8<1>(f, sc);
-        }
-        uint2 out;
-        out.x = pack4_e4m3(f[0], f[1], f[2], f[3]);
-        out.y = pack4_e4m3(f[4], f[5], f[6], f[7]);
-        st_nt8(p.q + row * p.ldq + v * 8, out);
-        if ((threadIdx.x & 15) == 0) p.s[row * p.s_rs + (int64_t)(v >> 4) * p.s_ts] = sc.s;
+        uint32_t out[2];
+        const float m = row16_max(amax_of(f));
+        const float sc = p.rule == 0 ? quantize<0, 8>(f, m, out) : quantize<1, 8>(f, m, out);
+        st_nt8(p.q + row * p.ldq + v * 8, make_uint2(out[0], out[1]));
+        if ((threadIdx.x & 15) == 0) p.s[row * p.s_rs + (int64_t)(v >> 4) * p.s_ts] = sc;
       }
     }
+    if (AHEAD) in = next;
   }
 }
 
@@ -336,16 +366,25 @@ __global__ __launch_bounds__(kSumThreads) void block_norm_sum_kernel(BlockNormGr
   }
 }
 
+// Threads of a workgroup for rows of up to 8192 columns, 8 to each, and up to 16384,
+// 16 to each: a function of the columns alone, and with it the order of a row's
+// additions.
+int block_threads(int64_t cols) {
+  const int64_t groups = cols / 8, t = groups <= 1024 ? groups : (groups + 1) / 2;
+  return (int)((t + 63) / 64 * 64);
+}
+
 template <int XT, int GATE, bool STREAM>
 hipError_t norm_as(const BlockNormArgs& a, hipStream_t st) {
-  const RowShape sh = row_shape(a.cols);
-  const dim3 grid((unsigned)(a.rows < kMaxRowBlocks ? a.rows : kMaxRowBlocks)), block(sh.threads);
-  if (sh.per == 1)
-    hipLaunchKernelGGL((block_norm_kernel<XT, 1, GATE, STREAM>), grid, block, 0, st, a);
-  else if (sh.per == 2)
-    hipLaunchKernelGGL((block_norm_kernel<XT, 2, GATE, STREAM>), grid, block, 0, st, a);
+  const int threads = block_threads(a.cols);
+  // as many workgroups as the CUs hold at once (AHEAD)
+  const int64_t fit = (int64_t)device_cu_count() * (threads > 448 ? 1 : 14 / (threads / 64));
+  if (a.cols <= 8192)
+    hipLaunchKernelGGL((block_norm_kernel<XT, 1, GATE, STREAM>), dim3((unsigned)(a.rows < fit ? a.rows : fit)), dim3(threads), 0,
+                       st, a);
   else
-    hipLaunchKernelGGL((block_norm_kernel<XT, 4, GATE, STREAM>), grid, block, 0, st, a);
+    hipLaunchKernelGGL((block_norm_kernel<XT, 2, GATE, STREAM>), dim3((unsigned)(a.rows < kMaxRowBlocks ? a.rows : kMaxRowBlocks)),
+                       dim3(threads), 0, st, a);
   return hipGetLastError();
 }
 
@@ -358,10 +397,8 @@ hipError_t norm_t(const BlockNormArgs& a, hipStream_t st) {
 template <int XT, int GATE, bool NT>
 hipError_t grad_as(const BlockNormGradArgs& a, hipStream_t st) {
   constexpr int U = 8 / kPer16<XT>;  // units of 8 elements
-  const int64_t groups = a.cols / 8;
-  const int per = groups <= 1024 ? 1 : 2;
-  const dim3 grid((unsigned)block_norm_strips(a.rows, a.cols)), block((unsigned)((groups + per - 1) / per + 63) / 64 * 64);
-  if (per == 1)
+  const dim3 grid((unsigned)block_norm_strips(a.rows, a.cols)), block(block_threads(a.cols));
+  if (a.cols <= 8192)
     hipLaunchKernelGGL((block_norm_grad_kernel<XT, U, GATE, NT, true>), grid, block, 0, st, a);
   else
     hipLaunchKernelGGL((block_norm_grad_kernel<XT, 2 * U, GATE, NT, false>), grid, block, 0, st, a);

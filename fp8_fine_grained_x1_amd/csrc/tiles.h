@@ -1,5 +1,6 @@
 // Helpers shared by the kernels that work tile by tile: the quantizers
-// (quant.hip) and the silu gate (gate.hip).
+// (quant.hip), the silu gate (gate.hip) and, for the quantization of a tile,
+// the norms around a block (block_norm.hip).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -137,6 +138,59 @@ __device__ __forceinline__ void for_pairs_impl(F&& f, std::integer_sequence<int,
 template <typename F>
 __device__ __forceinline__ void for_pairs(F&& f) {
   for_pairs_impl(f, std::make_integer_sequence<int, 4>{});
+}
+
+template <int N>
+__device__ __forceinline__ float amax_of(const float (&v)[N]) {
+  float m = fabsf(v[0]);
+#pragma unroll
+  for (int i = 1; i < N; ++i) m = fmaxf(m, fabsf(v[i]));
+  return m;
+}
+
+// Four E4M3 bytes of quotients by a scale of finite values: none exceeds
+// 448 (1 + 2^-24), which rounds to 448 by itself.
+__device__ __forceinline__ uint32_t pack4_unclamped(float a, float b, float c, float d) {
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  w = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+  return (uint32_t)w;
+}
+
+// Whether scale_amax and its quotients need none of their steps for tiny
+// scales, infinities and NaN.
+constexpr float kLeastPlain = 0x1p-55f;
+__device__ __forceinline__ bool plain_amax(float m) { return m >= kLeastPlain && m <= 3.40282347e38f; }
+
+// RN(m / 448) and RN(1 / s) of such an m, as scale_amax has them, in 8
+// instructions instead of 26.  Both are correction steps in fused
+// multiply-adds (Markstein, as in div_by_scale): from RN(1 / 448) for every m,
+// and from the hardware's reciprocal for every s -- checked for all 2^23
+// significands.
+__device__ __forceinline__ TileScale plain_scale(float m) {
+  const float inv448 = 1.0f / 448.0f;
+  const float q = m * inv448;
+  const float s = __builtin_fmaf(__builtin_fmaf(-448.0f, q, m), inv448, q);
+  const float y = __builtin_amdgcn_rcpf(s);
+  return {s, s, __builtin_fmaf(__builtin_fmaf(-s, y, 1.0f), y, y), 1.0f};
+}
+
+// N values (a multiple of 4) to E4M3 with the tile's maximum m; `out` gets
+// N / 4 words.  Returns the scale.
+template <int RULE, int N>
+__device__ __forceinline__ float quantize(float (&v)[N], float m, uint32_t (&out)[N / 4]) {
+  if (RULE == 0 && __builtin_amdgcn_ballot_w64(!plain_amax(m)) == 0) {
+    const TileScale sc = plain_scale(m);
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i)
+      out[i] = pack4_unclamped(div_by_scale(v[4 * i], sc.d, sc.y), div_by_scale(v[4 * i + 1], sc.d, sc.y),
+                               div_by_scale(v[4 * i + 2], sc.d, sc.y), div_by_scale(v[4 * i + 3], sc.d, sc.y));
+    return sc.s;
+  }
+  const TileScale sc = RULE == 0 ? scale_amax(m) : scale_pow2(m);
+  quotients<RULE, N>(v, sc);
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) out[i] = pack4_e4m3(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  return sc.s;
 }
 
 }  // namespace
