@@ -395,10 +395,11 @@ __global__ __launch_bounds__(kPartThreads<NE>) void balance_part_kernel(BalanceA
     Bounds w;
     bool known = false;
     while (at < hi) {
-      // (nearly every piece starts where the last one ended: its loads need not wait for the bounds)
+      // (loads return in order: the bounds first; nearly every piece starts where the last one
+      // ended, so that its tokens need not wait for them)
+      if (!known) w = load_bounds(p.offsets, p.seqs, p.rows, at);
       Ahead<NE> h;
       load_ahead<LT, LPT, NE, VEC>(p, by_k, at, hi, h);
-      if (!known) w = load_bounds(p.offsets, p.seqs, p.rows, at);
       const Seq f = seq_of(w, p.seqs, at);
       if (f.s >= p.seqs) {
         if (!known || w.base + 64 > p.seqs) break;
@@ -509,10 +510,11 @@ __global__ __launch_bounds__(kGradThreads) void balance_grad_kernel(BalanceGradA
   float c[NE], y[NE], base[NE];
 #pragma unroll
   for (int i = 0; i < NE; ++i) c[i] = base[i] = 0.0f;
+  const Bounds bounds = load_bounds(p.offsets, p.seqs, p.rows, lo);  // (loads return in order)
   int64_t t = lo + ((threadIdx.x & 63) / LPT);
   load_token<LT, LPT, NE, VEC>(p.logits, (t < hi ? t : hi - 1) * p.ldl, lane, E, y);
   if (p.base) load_token<LT, LPT, NE, VEC>(p.base, (t < hi ? t : hi - 1) * p.ldb, lane, E, base);
-  const Seq f = seq_of(load_bounds(p.offsets, p.seqs, p.rows, lo), p.seqs, lo);
+  const Seq f = seq_of(bounds, p.seqs, lo);
   int64_t s = f.s, first = f.first, end = f.end;
 #pragma unroll 1
   for (; t < hi; t += kPer) {
