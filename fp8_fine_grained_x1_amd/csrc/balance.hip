@@ -19,6 +19,12 @@
 // which no other piece has, since along the tokens every step raises c or s.  Each
 // piece has one partial sum, and a sequence's are added in their order: no
 // result depends on the order in which workgroups run.
+//
+// The bytes are few (16384 x 256 f32: 17 MB, 3.4 us at a device copy's rate); what
+// counts is latency: two dependent launches (9 and 5 us of 14), the loads of
+// bounds, then of tokens, and the fetching of code that each workgroup runs
+// through once or twice.  With the loops unrolled and both scores in one kernel the first
+// took 12 us; with the largest logit of every token 14.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -436,7 +442,9 @@ __global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(BalanceArgs 
   __shared__ int lives[kJoinThreads / 64];
   const uint32_t E = p.experts, groups = E / W;
   const uint32_t shift = groups > 1 ? 32 - __builtin_clz(groups - 1) : 0, cols = 1u << shift;  // columns of threads
-  const uint32_t parts = kJoinThreads >> shift, g = threadIdx.x & (cols - 1), mine = threadIdx.x >> shift;
+  // (the parts are added one after the other: not more of them than 32)
+  const uint32_t parts = (kJoinThreads >> shift) < 32 ? kJoinThreads >> shift : 32;
+  const uint32_t g = threadIdx.x & (cols - 1), mine = threadIdx.x >> shift;
   for (int64_t s = blockIdx.x; s < p.seqs; s += gridDim.x) {
     const uint32_t a = (uint32_t)bound(p.offsets, s, p.rows), b = (uint32_t)bound(p.offsets, s + 1, p.rows);
     // the sequence's pieces, from the one in a's chunk on
@@ -446,7 +454,7 @@ __global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(BalanceArgs 
     const int32_t* count = q.count + first * E;
     double t[W] = {};
     int c[W] = {}, live = 0;
-    if (g < groups) {
+    if (g < groups && mine < parts) {
 #pragma unroll 2
       for (uint32_t i = mine; i < pieces; i += parts) {
         const int64_t at = (int64_t)i * E + g * W;
@@ -499,6 +507,8 @@ constexpr int kGradThreads = 256;
 
 // A wave takes `run` consecutive tokens (per lane group every kPer-th of
 // them); the next token's logits and base are loaded while this one is formed.
+// 16384 x 256 f32 with base: 12.2 us (50 MB, 4.1 TB/s; 16 waves per CU: with 32
+// and two tokens to each 13 to 14, with 8 as many).
 template <int LT, int LPT, int NE, bool VEC, int SCORE>
 __global__ __launch_bounds__(kGradThreads) void balance_grad_kernel(BalanceGradArgs p, int64_t run) {
   constexpr int kPer = 64 / LPT;
@@ -569,8 +579,14 @@ __global__ __launch_bounds__(kGradThreads) void balance_grad_kernel(BalanceGradA
   }
 }
 
-// Up to this many rows a workgroup takes a whole sequence, in one launch.
-constexpr int64_t kOneRows = 512;
+// Whether a workgroup takes a whole sequence, in one launch: while the longest that
+// the rows allow is 12 passes of the workgroup's lane groups (rows of 256
+// experts: 192 in 9.7 us a call, in two launches 10.1 to 11.7; 256 in 11.8, 10.2;
+// of 64 experts 700 in 8.5, 10.2 to 11.9).
+bool one_launch(int64_t rows, int64_t experts) {
+  const int64_t per_pass = experts <= 64 ? 1024 / 16 : experts <= 128 ? 1024 / 32 : experts <= 512 ? 1024 / 64 : 512 / 64;
+  return rows <= 12 * per_pass;
+}
 constexpr int64_t kMostChunks = 256;
 constexpr int64_t kMaxChunk = 4096;
 constexpr int64_t kMaxBlocks = 1 << 20;
@@ -585,7 +601,7 @@ template <int LT, int LPT, int NE, bool VEC, int SCORE>
 hipError_t balance_as(const BalanceArgs& a, hipStream_t st) {
   const FastDiv by_k = make_fast_div((uint32_t)a.k);
   const unsigned seqs = (unsigned)(a.seqs < kMaxBlocks ? a.seqs : kMaxBlocks);
-  if (a.rows <= kOneRows) {
+  if (one_launch(a.rows, a.experts)) {
     hipLaunchKernelGGL((balance_one_kernel<LT, LPT, NE, VEC, SCORE>), dim3(seqs), dim3(kPartThreads<NE>), 0, st, a, by_k);
     return hipGetLastError();
   }
@@ -660,7 +676,7 @@ bool fours(const void* p, int64_t ld, int l_type) {
 }  // namespace
 
 int64_t balance_workspace(int64_t rows, int64_t experts, int64_t seqs) {
-  if (rows <= kOneRows) return 16;
+  if (one_launch(rows, experts)) return 16;
   const int64_t chunk = chunk_tokens(rows), pieces = (rows + chunk - 1) / chunk + seqs;
   return pieces * (2 * experts + 1) * (int64_t)sizeof(float);
 }

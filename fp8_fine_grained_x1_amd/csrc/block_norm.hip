@@ -16,6 +16,13 @@
 //   D = sum dH zh gives both.
 // A row stays in the workgroup's registers, undecoded, from its one reading to
 // its outputs.
+//
+// Both are bound by HBM, and by two sums over the row, one after the other, that
+// the outputs wait for: while they run nothing of that row moves, so the next
+// one is loaded ahead.  Measured on 8192 x 7168 bf16 with a gate per column: 95 us
+// forward with every output (530 MB, 5.6 TB/s), gradient with dh 143 us (705 MB,
+// 4.9 TB/s), 7 of it the sums over strips.  A large device copy moves 5.1 TB/s
+// on this card.
 #include <float.h>
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -46,7 +53,12 @@ __device__ __forceinline__ float rstd_of(const Raw8<XT> (&raw)[NV], float ss, fl
 // Thread t holds the 8-element vectors t, t + blockDim, .. of its rows
 // blockIdx.x, blockIdx.x + gridDim.x, ..: 16 consecutive lanes hold one 1x128
 // tile.  With one vector to a thread (up to 8192 columns: AHEAD) the gammas
-// stay in registers and the next row is loaded while this one is worked on.
+// stay in registers and the next row is loaded while this one is worked on
+// (8192 x 7168 bf16: 95 us; two vectors to a thread and two workgroups per CU,
+// without loading ahead, 121; with it 122).  The gammas are decoded where
+// the first row needs them, not before its first sum (105 us).  Large calls
+// store h and y past the caches (STREAM; 110 instead of 113 us before the
+// other steps).
 template <int XT, int NV, int GATE>
 struct BlockIn {
   Raw8<XT> z[NV], r[NV], g[GATE == kGateRows ? NV : 1];
@@ -166,8 +178,10 @@ __global__ __launch_bounds__(1024) void block_norm_kernel(BlockNormArgs p) {
 // A workgroup takes the rows blockIdx.x, blockIdx.x + gridDim.x, ..; its
 // threads keep their columns' part of the two sums over rows in registers
 // (D = sum dH zh, with a gate of rows sum dH zh gate; and sum dy xh) and
-// write them once.  The next row is loaded while this one is worked on
-// (PREFETCH, rows of up to 8192 columns), since one workgroup fills a CU.
+// write them once.  8 elements to a thread, up to 1024 threads: the next row is
+// loaded while this one is worked on (PREFETCH, rows of up to 8192 columns)
+// at 94 registers, and one strip per CU suffices (8192 x 7168 bf16: 143 us; 16
+// elements to a thread, 512 strips and nothing ahead: 197).
 template <int XT, int NV, int GATE>
 struct BlockRow {
   Unit<XT, kPer16<XT>> d[NV], h[NV], z[NV], b[NV], g[GATE == kGateRows ? NV : 1];
@@ -377,8 +391,11 @@ int block_threads(int64_t cols) {
 template <int XT, int GATE, bool STREAM>
 hipError_t norm_as(const BlockNormArgs& a, hipStream_t st) {
   const int threads = block_threads(a.cols);
-  // as many workgroups as the CUs hold at once (AHEAD)
-  const int64_t fit = (int64_t)device_cu_count() * (threads > 448 ? 1 : 14 / (threads / 64));
+  // Workgroups that take row after row (AHEAD): one to a CU of rows past 4096 columns, 8
+  // waves down to 1152, then 14 (bf16: 8192 x 4096 57.3 us, with two workgroups 63;
+  // 8192 x 2048 31.8, with 16 waves 33; 8192 x 1024 15.7, with 8 waves 16.8).
+  const int waves = threads / 64, per_cu = waves > 8 ? 1 : waves > 2 ? 8 / waves : 14 / waves;
+  const int64_t fit = (int64_t)device_cu_count() * per_cu;
   if (a.cols <= 8192)
     hipLaunchKernelGGL((block_norm_kernel<XT, 1, GATE, STREAM>), dim3((unsigned)(a.rows < fit ? a.rows : fit)), dim3(threads), 0,
                        st, a);

@@ -150,7 +150,7 @@ constexpr int64_t kMaxRowBlocks = 1 << 20;
 struct RowShape {
   int per, threads;
 };
-RowShape row_shape(int64_t cols) {
+inline RowShape row_shape(int64_t cols) {
   const int64_t groups = cols / 8;
   const int per = groups <= 512 ? 1 : groups <= 1024 ? 2 : 4;
   const int64_t t = (groups + per - 1) / per;
