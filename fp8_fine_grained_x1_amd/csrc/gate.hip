@@ -12,11 +12,11 @@
 //               of a.  (Both quantizers are passed straight through.)
 // Every output is rounded once, from the fp32 value.
 //
-// All three kernels are bound by HBM.  An element costs some 40 instructions
-// forward and as many backward, about half of what the vector units issue in the
-// time its bytes take: leaving the sigmoid out changes 16384 x 4096 bf16 by
-// 2%.  Measured there: forward with checkpoint 82 us (476 MB, 5.8 TB/s),
-// gradient 73 us (411 MB, 5.6); with the 128x1 operands, 8192 x 4096, 67 us (309
+// All three kernels are bound by HBM, closely: an element costs 36 vector
+// instructions forward and 35 backward, which keep the vector units busy in 83 and 87%
+// of the cycles; still, leaving the sigmoids out changes the times by 2% at most.
+// Measured on 16384 x 4096 bf16: forward with checkpoint 81 us (476 MB, 5.9 TB/s),
+// gradient 75 us (411 MB, 5.5); with the 128x1 operands, 8192 x 4096, 67 us (309
 // MB, 4.6).  A large device copy moves 5.1 TB/s on this card.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -89,9 +89,11 @@ template <int XT>
 struct Raw16 {
   Raw8<XT> a, b;
 };
-template <int XT, int GAP, bool NT>
+// (Ordinary loads: past the caches 16384 x 4096 takes 82 us instead of 80.5
+// forward, 4096 x 4096, whose producer leaves it in them, 24.6 instead of 22.9.)
+template <int XT, int GAP>
 __device__ __forceinline__ Raw16<XT> load_raw16(const void* __restrict__ p, int64_t off) {
-  return {load_raw8<XT, NT>(p, off), load_raw8<XT, NT>(p, off + GAP)};
+  return {load_raw8<XT, false>(p, off), load_raw8<XT, false>(p, off + GAP)};
 }
 template <int XT>
 __device__ __forceinline__ void decode_raw16(const Raw16<XT>& r, float (&v)[16]) {
@@ -116,7 +118,7 @@ struct GateGrid {
 };
 constexpr int kGroups = kGThreads / 8;
 
-template <int XT, int RULE, int ORDER, bool KEEP, bool NT>
+template <int XT, int RULE, int ORDER, bool KEEP>
 __global__ __launch_bounds__(kGThreads) void gate_kernel(GateArgs p, GateGrid gr) {
   constexpr int GAP = 8;
   const uint32_t c = lane_column<GAP>();
@@ -125,8 +127,8 @@ __global__ __launch_bounds__(kGThreads) void gate_kernel(GateArgs p, GateGrid gr
     uint32_t r, tc;
     tile_rc<ORDER>(t, gr.tpr, gr.band, rows, r, tc);
     const int64_t row = r, col = tc * 128 + c;
-    const Raw16<XT> g = load_raw16<XT, GAP, NT>(p.u, row * p.ldu + col);
-    const Raw16<XT> l = load_raw16<XT, GAP, NT>(p.u, row * p.ldu + p.inner + col);
+    const Raw16<XT> g = load_raw16<XT, GAP>(p.u, row * p.ldu + col);
+    const Raw16<XT> l = load_raw16<XT, GAP>(p.u, row * p.ldu + p.inner + col);
     float a[16], b[16], v[16];
     decode_raw16<XT>(g, a);
     decode_raw16<XT>(l, b);
@@ -164,7 +166,7 @@ __device__ __forceinline__ void decode_kept(uint2 w, float s, float* v) {
   }
 }
 
-template <int XT, int RULE, int ORDER, bool WIDE, bool NT>
+template <int XT, int RULE, int ORDER, bool WIDE>
 __global__ __launch_bounds__(kGThreads) void gate_grad_kernel(GateGradArgs p, GateGrid gr) {
   constexpr int GAP = WIDE ? 64 : 8;
   const uint32_t c = lane_column<GAP>();
@@ -174,7 +176,7 @@ __global__ __launch_bounds__(kGThreads) void gate_grad_kernel(GateGradArgs p, Ga
     uint32_t r, tc;
     tile_rc<ORDER>(t, gr.tpr, gr.band, rows, r, tc);
     const int64_t row = r, col = tc * 128 + c;
-    const Raw16<XT> d = load_raw16<XT, GAP, NT>(p.da, row * p.ldda + col);
+    const Raw16<XT> d = load_raw16<XT, GAP>(p.da, row * p.ldda + col);
     const uint8_t* k = p.uq + row * p.lduq + col;
     const float* ks = p.us + row * p.us_rs + tc * p.us_ts;
     const uint4 gq = load_kept<GAP>(k), lq = load_kept<GAP>(k + p.inner);
@@ -364,38 +366,34 @@ unsigned gate_grid(int64_t rows, int64_t inner, GateGrid& gr) {
 // the 1x128 quantizer).
 bool by_bands(int64_t s_rs) { return s_rs == 1; }
 
-template <int XT, int RULE, int ORDER, bool NT>
+template <int XT, int RULE, int ORDER>
 hipError_t gate_as(const GateArgs& a, hipStream_t st) {
   GateGrid gr;
   const unsigned blocks = gate_grid(a.rows, a.inner, gr);
   if (a.uq)
-    hipLaunchKernelGGL((gate_kernel<XT, RULE, ORDER, true, NT>), dim3(blocks), dim3(kGThreads), 0, st, a, gr);
+    hipLaunchKernelGGL((gate_kernel<XT, RULE, ORDER, true>), dim3(blocks), dim3(kGThreads), 0, st, a, gr);
   else
-    hipLaunchKernelGGL((gate_kernel<XT, RULE, ORDER, false, NT>), dim3(blocks), dim3(kGThreads), 0, st, a, gr);
+    hipLaunchKernelGGL((gate_kernel<XT, RULE, ORDER, false>), dim3(blocks), dim3(kGThreads), 0, st, a, gr);
   return hipGetLastError();
 }
-template <int XT, int RULE, int ORDER, bool NT>
+template <int XT, int RULE, int ORDER>
 hipError_t grad_as(const GateGradArgs& a, hipStream_t st) {
   GateGrid gr;
   const unsigned blocks = gate_grid(a.rows, a.inner, gr);
   if (a.du || a.a)
-    hipLaunchKernelGGL((gate_grad_kernel<XT, RULE, ORDER, true, NT>), dim3(blocks), dim3(kGThreads), 0, st, a, gr);
+    hipLaunchKernelGGL((gate_grad_kernel<XT, RULE, ORDER, true>), dim3(blocks), dim3(kGThreads), 0, st, a, gr);
   else
-    hipLaunchKernelGGL((gate_grad_kernel<XT, RULE, ORDER, false, NT>), dim3(blocks), dim3(kGThreads), 0, st, a, gr);
+    hipLaunchKernelGGL((gate_grad_kernel<XT, RULE, ORDER, false>), dim3(blocks), dim3(kGThreads), 0, st, a, gr);
   return hipGetLastError();
 }
 
 template <int XT, int RULE>
 hipError_t gate_t(const GateArgs& a, hipStream_t st) {
-  const bool nt = past_caches(a.rows, 2, a.inner, XT == 0 ? 2 : 4);
-  if (by_bands(a.s_rs)) return nt ? gate_as<XT, RULE, 1, true>(a, st) : gate_as<XT, RULE, 1, false>(a, st);
-  return nt ? gate_as<XT, RULE, 0, true>(a, st) : gate_as<XT, RULE, 0, false>(a, st);
+  return by_bands(a.s_rs) ? gate_as<XT, RULE, 1>(a, st) : gate_as<XT, RULE, 0>(a, st);
 }
 template <int XT, int RULE>
 hipError_t grad_t(const GateGradArgs& a, hipStream_t st) {
-  const bool nt = past_caches(a.rows, 1, a.inner, XT == 0 ? 2 : 4);
-  if (by_bands(a.q ? a.s_rs : 0)) return nt ? grad_as<XT, RULE, 1, true>(a, st) : grad_as<XT, RULE, 1, false>(a, st);
-  return nt ? grad_as<XT, RULE, 0, true>(a, st) : grad_as<XT, RULE, 0, false>(a, st);
+  return by_bands(a.q ? a.s_rs : 0) ? grad_as<XT, RULE, 1>(a, st) : grad_as<XT, RULE, 0>(a, st);
 }
 template <int XT, int RULE>
 hipError_t grad_tile_t(const GateGradTileArgs& a, hipStream_t st) {
