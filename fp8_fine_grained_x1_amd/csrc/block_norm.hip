@@ -57,8 +57,9 @@ __device__ __forceinline__ float rstd_of(const Raw8<XT> (&raw)[NV], float ss, fl
 // (8192 x 7168 bf16: 95 us; two vectors to a thread and two workgroups per CU,
 // without loading ahead, 121; with it 122).  The gammas are decoded where
 // the first row needs them, not before its first sum (105 us).  Large calls
-// store h and y past the caches (STREAM; 110 instead of 113 us before the
-// other steps).
+// read and store past the caches (STREAM: 95 us, 98 without), others ordinarily,
+// for the readers of h and y: 2048 rows take 29.8 us, with stores past the
+// caches 24.1, but with three readers after it 52.9 and 57.5.
 template <int XT, int NV, int GATE>
 struct BlockIn {
   Raw8<XT> z[NV], r[NV], g[GATE == kGateRows ? NV : 1];

@@ -72,15 +72,23 @@ __device__ __forceinline__ float row8_max(float v) {
   v = fmaxf(v, dpp_mov<kDppQuadXor2>(v));
   return fmaxf(v, dpp_mov<kDppRowHalfMirror>(v));
 }
-template <int RULE, int GAP>
+// PAST: stored past the caches.
+template <int RULE, int GAP, bool PAST>
 __device__ __forceinline__ void quantize_tile(float (&v)[16], uint8_t* __restrict__ q, float* __restrict__ s) {
   uint32_t w[4];
   const float sc = quantize<RULE, 16>(v, row8_max(amax_of(v)), w);
   if constexpr (GAP == 8) {
-    st_nt16(q, make_uint4(w[0], w[1], w[2], w[3]));
+    const uint4 x = make_uint4(w[0], w[1], w[2], w[3]);
+    if constexpr (PAST) st_nt16(q, x); else *reinterpret_cast<uint4*>(q) = x;
   } else {
-    st_nt8(q, make_uint2(w[0], w[1]));
-    st_nt8(q + GAP, make_uint2(w[2], w[3]));
+    const uint2 x = make_uint2(w[0], w[1]), y = make_uint2(w[2], w[3]);
+    if constexpr (PAST) {
+      st_nt8(q, x);
+      st_nt8(q + GAP, y);
+    } else {
+      *reinterpret_cast<uint2*>(q) = x;
+      *reinterpret_cast<uint2*>(q + GAP) = y;
+    }
   }
   if ((threadIdx.x & 7) == 0) *s = sc;
 }
@@ -118,7 +126,7 @@ struct GateGrid {
 };
 constexpr int kGroups = kGThreads / 8;
 
-template <int XT, int RULE, int ORDER, bool KEEP>
+template <int XT, int RULE, int ORDER, bool KEEP, bool PAST>
 __global__ __launch_bounds__(kGThreads) void gate_kernel(GateArgs p, GateGrid gr) {
   constexpr int GAP = 8;
   const uint32_t c = lane_column<GAP>();
@@ -134,12 +142,12 @@ __global__ __launch_bounds__(kGThreads) void gate_kernel(GateArgs p, GateGrid gr
     decode_raw16<XT>(l, b);
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = silu_of(a[i], sigmoid_of(a[i]).s) * b[i];
-    quantize_tile<RULE, GAP>(v, p.q + row * p.ldq + col, p.s + row * p.s_rs + tc * p.s_ts);
+    quantize_tile<RULE, GAP, PAST>(v, p.q + row * p.ldq + col, p.s + row * p.s_rs + tc * p.s_ts);
     if constexpr (KEEP) {
       uint8_t* k = p.uq + row * p.lduq + col;
       float* ks = p.us + row * p.us_rs + tc * p.us_ts;
-      quantize_tile<RULE, GAP>(a, k, ks);
-      quantize_tile<RULE, GAP>(b, k + p.inner, ks + (p.inner >> 7) * p.us_ts);
+      quantize_tile<RULE, GAP, true>(a, k, ks);
+      quantize_tile<RULE, GAP, true>(b, k + p.inner, ks + (p.inner >> 7) * p.us_ts);
     }
   }
 }
@@ -166,7 +174,7 @@ __device__ __forceinline__ void decode_kept(uint2 w, float s, float* v) {
   }
 }
 
-template <int XT, int RULE, int ORDER, bool WIDE>
+template <int XT, int RULE, int ORDER, bool WIDE, bool PAST>
 __global__ __launch_bounds__(kGThreads) void gate_grad_kernel(GateGradArgs p, GateGrid gr) {
   constexpr int GAP = WIDE ? 64 : 8;
   const uint32_t c = lane_column<GAP>();
@@ -207,8 +215,8 @@ __global__ __launch_bounds__(kGThreads) void gate_grad_kernel(GateGradArgs p, Ga
     }
     uint8_t* q = p.q + row * p.ldq + col;
     float* s = p.s + row * p.s_rs + tc * p.s_ts;
-    quantize_tile<RULE, GAP>(dg, q, s);
-    quantize_tile<RULE, GAP>(dl, q + p.inner, s + half * p.s_ts);
+    quantize_tile<RULE, GAP, PAST>(dg, q, s);
+    quantize_tile<RULE, GAP, PAST>(dl, q + p.inner, s + half * p.s_ts);
   }
 }
 
@@ -366,34 +374,44 @@ unsigned gate_grid(int64_t rows, int64_t inner, GateGrid& gr) {
 // the 1x128 quantizer).
 bool by_bands(int64_t s_rs) { return s_rs == 1; }
 
-template <int XT, int RULE, int ORDER>
+template <int XT, int RULE, int ORDER, bool PAST>
 hipError_t gate_as(const GateArgs& a, hipStream_t st) {
   GateGrid gr;
   const unsigned blocks = gate_grid(a.rows, a.inner, gr);
   if (a.uq)
-    hipLaunchKernelGGL((gate_kernel<XT, RULE, ORDER, true>), dim3(blocks), dim3(kGThreads), 0, st, a, gr);
+    hipLaunchKernelGGL((gate_kernel<XT, RULE, ORDER, true, PAST>), dim3(blocks), dim3(kGThreads), 0, st, a, gr);
   else
-    hipLaunchKernelGGL((gate_kernel<XT, RULE, ORDER, false>), dim3(blocks), dim3(kGThreads), 0, st, a, gr);
+    hipLaunchKernelGGL((gate_kernel<XT, RULE, ORDER, false, PAST>), dim3(blocks), dim3(kGThreads), 0, st, a, gr);
   return hipGetLastError();
 }
-template <int XT, int RULE, int ORDER>
+template <int XT, int RULE, int ORDER, bool PAST>
 hipError_t grad_as(const GateGradArgs& a, hipStream_t st) {
   GateGrid gr;
   const unsigned blocks = gate_grid(a.rows, a.inner, gr);
   if (a.du || a.a)
-    hipLaunchKernelGGL((gate_grad_kernel<XT, RULE, ORDER, true>), dim3(blocks), dim3(kGThreads), 0, st, a, gr);
+    hipLaunchKernelGGL((gate_grad_kernel<XT, RULE, ORDER, true, true>), dim3(blocks), dim3(kGThreads), 0, st, a, gr);
   else
-    hipLaunchKernelGGL((gate_grad_kernel<XT, RULE, ORDER, false>), dim3(blocks), dim3(kGThreads), 0, st, a, gr);
+    hipLaunchKernelGGL((gate_grad_kernel<XT, RULE, ORDER, false, PAST>), dim3(blocks), dim3(kGThreads), 0, st, a, gr);
   return hipGetLastError();
 }
 
+// The next product's operand is stored ordinarily while the inputs fit the
+// caches, and past them beyond.  Forward, gradient and a reader after each, inner
+// 4096: 4096 rows 57 us, past the caches 62; 8192 rows 111, 121; 16384 rows 248,
+// 232.  The checkpoint, which is read much later, always passes them by, and so
+// does the operand beside du and a, which stay in them (5003 x 2048: 26.9 us, 28.4
+// with all three ordinary).
 template <int XT, int RULE>
 hipError_t gate_t(const GateArgs& a, hipStream_t st) {
-  return by_bands(a.s_rs) ? gate_as<XT, RULE, 1>(a, st) : gate_as<XT, RULE, 0>(a, st);
+  const bool past = past_caches(a.rows, 2, a.inner, XT == 0 ? 2 : 4);
+  if (by_bands(a.s_rs)) return past ? gate_as<XT, RULE, 1, true>(a, st) : gate_as<XT, RULE, 1, false>(a, st);
+  return past ? gate_as<XT, RULE, 0, true>(a, st) : gate_as<XT, RULE, 0, false>(a, st);
 }
 template <int XT, int RULE>
 hipError_t grad_t(const GateGradArgs& a, hipStream_t st) {
-  return by_bands(a.q ? a.s_rs : 0) ? grad_as<XT, RULE, 1>(a, st) : grad_as<XT, RULE, 0>(a, st);
+  const bool past = past_caches(a.rows, 1, a.inner, XT == 0 ? 4 : 6);
+  if (by_bands(a.q ? a.s_rs : 0)) return past ? grad_as<XT, RULE, 1, true>(a, st) : grad_as<XT, RULE, 1, false>(a, st);
+  return past ? grad_as<XT, RULE, 0, true>(a, st) : grad_as<XT, RULE, 0, false>(a, st);
 }
 template <int XT, int RULE>
 hipError_t grad_tile_t(const GateGradTileArgs& a, hipStream_t st) {
