@@ -3,7 +3,7 @@
 //
 // Forward, per row, z the block's output and r the residual stream:
 //   zh = z rstd_post,  t = zh gamma_post gate block_scale
-//   h = RN(residual_scale r + t) in z's type
+//   h = RN(residual_scale r + t) in z's type, each product in fp32
 //   y = (h rstd) gamma;  q, s as the norm's (norm.hip)
 // rstd = 1 / sqrt(mean of squares + eps) of z and of the rounded h.
 // Backward, dy the gradient of y, dh what reaches h along the stream:
@@ -19,8 +19,8 @@
 //
 // Both are bound by HBM, and by two sums over the row, one after the other, that
 // the outputs wait for: while they run nothing of that row moves, so the next
-// one is loaded ahead.  Measured on 8192 x 7168 bf16 with a gate per column: 95 us
-// forward with every output (530 MB, 5.6 TB/s), gradient with dh 143 us (705 MB,
+// one is loaded ahead.  Measured on 8192 x 7168 bf16 with a gate per column: 99 us
+// forward with every output (530 MB, 5.4 TB/s), gradient with dh 143 us (705 MB,
 // 4.9 TB/s), 7 of it the sums over strips.  A large device copy moves 5.1 TB/s
 // on this card.
 #include <float.h>
@@ -54,10 +54,10 @@ __device__ __forceinline__ float rstd_of(const Raw8<XT> (&raw)[NV], float ss, fl
 // blockIdx.x, blockIdx.x + gridDim.x, ..: 16 consecutive lanes hold one 1x128
 // tile.  With one vector to a thread (up to 8192 columns: AHEAD) the gammas
 // stay in registers and the next row is loaded while this one is worked on
-// (8192 x 7168 bf16: 95 us; two vectors to a thread and two workgroups per CU,
+// (8192 x 7168 bf16: 99 us; two vectors to a thread and two workgroups per CU,
 // without loading ahead, 121; with it 122).  The gammas are decoded where
-// the first row needs them, not before its first sum (105 us).  Large calls
-// read and store past the caches (STREAM: 95 us, 98 without), others ordinarily,
+// the first row needs them, not before its first sum (10 us more).  Large calls
+// read and store past the caches (STREAM: 3 us less than without), others ordinarily,
 // for the readers of h and y: 2048 rows take 29.8 us, with stores past the
 // caches 24.1, but with three readers after it 52.9 and 57.5.
 template <int XT, int NV, int GATE>
@@ -83,7 +83,7 @@ __global__ __launch_bounds__(1024) void block_norm_kernel(BlockNormArgs p) {
   __shared__ double wide[kMaxWaves];
   const int nvec = (int)(p.cols >> 3);
   const float inv_cols = 1.0f / (float)p.cols;
-  float gm[8], gp[8];  // gamma; block_scale gamma_post (gate per column)
+  float gm[8], gp[8], gc[8];  // gamma, gamma_post, a gate per column
   RawGamma<8> raw_gm, raw_gp, raw_gate;
   auto load_gammas = [&](int v) {
     raw_gp = load_gamma<8>(p.gamma_post, p.g_type, v);
@@ -91,12 +91,9 @@ __global__ __launch_bounds__(1024) void block_norm_kernel(BlockNormArgs p) {
     raw_gm = load_gamma<8>(p.gamma, p.g_type, v);
   };
   auto decode_gammas = [&]() {
-    float g[8];
     decode_gamma<8>(raw_gp, p.g_type, gp);
-    if (GATE == kGateCols) decode_gamma<8>(raw_gate, p.g_type, g);
+    if (GATE == kGateCols) decode_gamma<8>(raw_gate, p.g_type, gc);
     decode_gamma<8>(raw_gm, p.g_type, gm);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) gp[e] *= GATE == kGateCols ? p.block_scale * g[e] : p.block_scale;
   };
   BlockIn<XT, NV, GATE> in;
   int64_t row = blockIdx.x;
@@ -131,14 +128,19 @@ __global__ __launch_bounds__(1024) void block_norm_kernel(BlockNormArgs p) {
       decode8<XT>(in.z[i], f);
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] = f[e] * post * gp[e];
-      if constexpr (GATE == kGateRows) {
-        decode8<XT>(in.g[i], x);
+      if constexpr (GATE != kGateNone) {
+        if (GATE == kGateRows) decode8<XT>(in.g[i], gc);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] *= x[e];
+        for (int e = 0; e < 8; ++e) f[e] *= gc[e];
       }
       decode8<XT>(in.r[i], x);
+      // Each product rounded by itself, as in the formula taken step by step:
+      // h then rounds to z's type as that does but for 100 of 58.7 million values
+      // (8192 x 7168 bf16, 99 us).  With the scales and gates multiplied before
+      // the rows and a fused sum 370 differ (96 us), and where one is a tile's
+      // largest, its scale follows by a step of z's type.
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = __builtin_fmaf(p.residual_scale, x[e], f[e]);
+      for (int e = 0; e < 8; ++e) x[e] = p.residual_scale * x[e] + p.block_scale * f[e];
       in.r[i] = encode8<XT>(x);
       store_raw8<XT, STREAM>(p.h, row * p.ldh + v * 8, in.r[i]);
       decode8<XT>(in.r[i], x);
