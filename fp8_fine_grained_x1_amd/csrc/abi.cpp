@@ -556,7 +556,7 @@ int fp8_balance_loss(const void* logits, int l_type, int64_t rows, int64_t exper
   if (!aligned(logits, elem_size(l_type)) || !aligned(idx, 4) || !aligned(offsets, 4) || !aligned(loss, 4) ||
       !aligned(counts, 4) || !aligned(slope, 4) || !aligned(workspace, 16))
     return FP8FG_EALIGN;
-  if (experts > fp8fg::kRouteMaxExperts || k > fp8fg::kRouteMaxK || beyond(kMaxI32, {rows, seqs}) ||
+  if (experts > fp8fg::kRouteMaxExperts || k > fp8fg::kRouteMaxK || beyond(kMaxI32, {rows, seqs}) || rows * k > kMaxI32 ||
       beyond(kMaxPitch, {ldl, ld_idx}))
     return FP8FG_EUNSUPPORTED;
   if (workspace_bytes < fp8_balance_loss_workspace(rows, experts, seqs)) return FP8FG_ESHAPE;

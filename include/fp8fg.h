@@ -529,8 +529,8 @@ FP8FG_API int fp8_swiglu_backward_128x1(const void* da, int type, int64_t rows, 
  *            16-byte aligned; FP8FG_ESHAPE if workspace_bytes is less.
  *   Requires 1 <= k <= experts, scale finite; seqs == 0 is a no-op, rows == 0
  *   writes zeros.  No alignment beyond the element's.
- *   Limits (FP8FG_EUNSUPPORTED): experts <= 1024, k <= 64, seqs <= 2^31 - 1;
- *   rows and pitches as above.
+ *   Limits (FP8FG_EUNSUPPORTED): experts <= 1024, k <= 64, seqs <= 2^31 - 1,
+ *   rows * k <= 2^31 - 1 (the counts); rows and pitches as above.
  */
 FP8FG_API int64_t fp8_balance_loss_workspace(int64_t rows, int64_t experts, int64_t seqs);
 FP8FG_API int fp8_balance_loss(const void* logits, int l_type, int64_t rows, int64_t experts,

@@ -133,7 +133,8 @@ BALANCE_BOTH = [
     (dict(counts=None), INVAL), (dict(workspace=None), INVAL), (dict(workspace_bytes=-1), INVAL), (dict(ld_idx=5), SHAPE),
     (dict(k=65, ld_idx=65), SHAPE), (dict(workspace_bytes=15), SHAPE), (dict(idx=P + 2), ALIGN), (dict(loss=P + 2), ALIGN),
     (dict(counts=P + 2), ALIGN), (dict(workspace=P + 8), ALIGN), (dict(experts=1025, ldl=1025), UNSUP),
-    (dict(experts=128, ldl=128, k=65, ld_idx=65), UNSUP), (dict(seqs=0), OK), (dict(seqs=0, logits=None, loss=None), OK),
+    (dict(experts=128, ldl=128, k=65, ld_idx=65), UNSUP), (dict(rows=1 << 28, k=8, ld_idx=8), UNSUP),
+    (dict(seqs=0), OK), (dict(seqs=0, logits=None, loss=None), OK),
     (dict(rows=0, loss=None), INVAL),
 ])
 def test_balance_refusals(kw, status):
