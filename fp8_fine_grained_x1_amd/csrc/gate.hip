@@ -13,9 +13,9 @@
 // Every output is rounded once, from the fp32 value.
 //
 // All three kernels are bound by HBM, closely: an element costs 36 vector
-// instructions forward and 35 backward, which keep the vector units busy in 83 and 87%
+// instructions forward and 35 backward, which keep the vector units busy in 86 and 90%
 // of the cycles; still, leaving the sigmoids out changes the times by 2% at most.
-// Measured on 16384 x 4096 bf16: forward with checkpoint 81 us (476 MB, 5.9 TB/s),
+// Measured on 16384 x 4096 bf16: forward with checkpoint 80 us (476 MB, 6.0 TB/s),
 // gradient 75 us (411 MB, 5.5); with the 128x1 operands, 8192 x 4096, 67 us (309
 // MB, 4.6).  A large device copy moves 5.1 TB/s on this card.
 #include <hip/hip_runtime.h>
