@@ -19,8 +19,8 @@
 //
 // Both are bound by HBM, and by two sums over the row, one after the other, that
 // the outputs wait for: while they run nothing of that row moves, so the next
-// one is loaded ahead.  Measured on 8192 x 7168 bf16 with a gate per column: 99 us
-// forward with every output (530 MB, 5.4 TB/s), gradient with dh 143 us (705 MB,
+// one is loaded ahead.  Measured on 8192 x 7168 bf16 with a gate per column: 97 us
+// forward with every output (530 MB, 5.5 TB/s), gradient with dh 143 us (705 MB,
 // 4.9 TB/s), 7 of it the sums over strips.  A large device copy moves 5.1 TB/s
 // on this card.
 #include <float.h>
@@ -54,8 +54,9 @@ __device__ __forceinline__ float rstd_of(const Raw8<XT> (&raw)[NV], float ss, fl
 // blockIdx.x, blockIdx.x + gridDim.x, ..: 16 consecutive lanes hold one 1x128
 // tile.  With one vector to a thread (up to 8192 columns: AHEAD) the gammas
 // stay in registers and the next row is loaded while this one is worked on
-// (8192 x 7168 bf16: 99 us; two vectors to a thread and two workgroups per CU,
-// without loading ahead, 121; with it 122).  The gammas are decoded where
+// (8192 x 7168 bf16: 97 us, loaded behind the first sum's squares 99.5, where narrow
+// rows gain, 8192 x 2048: 33.0, this 33.7; two vectors to a thread and two workgroups
+// per CU, without loading ahead, 121; with it 122).  The gammas are decoded where
 // the first row needs them, not before its first sum (10 us more).  Large calls
 // read and store past the caches (STREAM: 3 us less than without), others ordinarily,
 // for the readers of h and y: 2048 rows take 29.8 us, with stores past the
@@ -103,6 +104,8 @@ __global__ __launch_bounds__(1024) void block_norm_kernel(BlockNormArgs p) {
   }
   for (; row < p.rows; row += gridDim.x) {
     if (!AHEAD) load_block_in<XT, NV, GATE, STREAM>(p, row, nvec, in);
+    BlockIn<XT, NV, GATE> next;
+    if (AHEAD && row + gridDim.x < p.rows) load_block_in<XT, NV, GATE, STREAM>(p, row + gridDim.x, nvec, next);
     float ss = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -113,8 +116,6 @@ __global__ __launch_bounds__(1024) void block_norm_kernel(BlockNormArgs p) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss += f[e] * f[e];
     }
-    BlockIn<XT, NV, GATE> next;
-    if (AHEAD && row + gridDim.x < p.rows) load_block_in<XT, NV, GATE, STREAM>(p, row + gridDim.x, nvec, next);
     ss = block_sum(ss, part[0]);
     const float post = rstd_of<XT, NV>(in.z, ss, inv_cols, nvec, p.cols, p.eps, wide);
     ss = 0.0f;
@@ -136,8 +137,8 @@ __global__ __launch_bounds__(1024) void block_norm_kernel(BlockNormArgs p) {
       decode8<XT>(in.r[i], x);
       // Each product rounded by itself, as in the formula taken step by step:
       // h then rounds to z's type as that does but for 100 of 58.7 million values
-      // (8192 x 7168 bf16, 99 us).  With the scales and gates multiplied before
-      // the rows and a fused sum 370 differ (96 us), and where one is a tile's
+      // (8192 x 7168 bf16).  With the scales and gates multiplied before
+      // the rows and a fused sum 370 differ (3 us less), and where one is a tile's
       // largest, its scale follows by a step of z's type.
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] = p.residual_scale * x[e] + p.block_scale * f[e];
@@ -183,7 +184,8 @@ __global__ __launch_bounds__(1024) void block_norm_kernel(BlockNormArgs p) {
 // (D = sum dH zh, with a gate of rows sum dH zh gate; and sum dy xh) and
 // write them once.  8 elements to a thread, up to 1024 threads: the next row is
 // loaded while this one is worked on (PREFETCH, rows of up to 8192 columns)
-// at 94 registers, and one strip per CU suffices (8192 x 7168 bf16: 143 us; 16
+// at 94 registers, and one strip per CU suffices (8192 x 7168 bf16: 143 us, loaded
+// before the first sum's terms 156, behind that sum 149; 16
 // elements to a thread, 512 strips and nothing ahead: 197).
 template <int XT, int NV, int GATE>
 struct BlockRow {
