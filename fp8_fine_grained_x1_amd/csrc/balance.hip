@@ -119,7 +119,7 @@ __device__ __forceinline__ float token_max(float v) {
   return v;
 }
 
-// exp(x) for x <= 60 within 2 ulp, 0 below 2^-126.
+// exp(x) within 2 ulp, 0 below 2^-126 and for a NaN; above 2^128 it is infinite or NaN.
 __device__ __forceinline__ float exp_of(float x) {
   x = fmaxf(x, -120.0f);
   const float t = x * 1.44269502f;                        // RN32(log2 e)
@@ -167,12 +167,12 @@ __device__ __forceinline__ float scores_below_top(const float (&l)[NE], float (&
 // false).
 //
 // They are formed directly first: exp(l) and 1 / (1 + exp(-l)) are within fp32's
-// range unless the logits are far out, and what underflows is below 2^-126 of
-// a sum that is not small.  The sum tells: with one below 1/2, above 2^100 or
-// NaN in the wave (nearly none but the padding's) the scores are formed again
+// range unless the logits are far out, what underflows is below 2^-126 of
+// a sum that is not small, and without a difference to round a score's error
+// does not grow with its logit.  The sum tells: with one below 1 (softmax) or 1/2
+// (sigmoid), above 2^100 or NaN in the wave the scores are formed again
 // below the largest logit.  That maximum and its checks cost half of the
-// instructions.  The forward pass also does without the product's rounding error
-// in the exponent (|l| 2^-24 of a score, and a sequence's sum averages it).
+// instructions.  (A NaN logit comes out as 0, as a masked one.)
 template <int LPT, int NE, int SCORE, bool REST>
 __device__ __forceinline__ float token_scores(const float (&l)[NE], float (&y)[NE], float (&r)[NE], bool& live) {
   float total = 0.0f;
@@ -180,13 +180,11 @@ __device__ __forceinline__ float token_scores(const float (&l)[NE], float (&y)[N
 #pragma unroll
   for (int i = 0; i < NE; ++i) {
     if (SCORE == 0) {
-      y[i] = REST ? exp_of(fminf(l[i], 100.0f)) : __builtin_amdgcn_exp2f(l[i] * 1.44269502f);
-    } else if (REST) {
-      const float t = exp_of(-fabsf(l[i])), inv = __builtin_amdgcn_rcpf(1.0f + t);
-      r[i] = l[i] >= 0.0f ? t * inv : inv;
-      y[i] = l[i] >= 0.0f ? inv : t * inv;
+      y[i] = exp_of(l[i]);
     } else {
-      y[i] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(l[i] * -1.44269502f));
+      const float t = exp_of(-fabsf(l[i])), inv = __builtin_amdgcn_rcpf(1.0f + t);
+      if (REST) r[i] = l[i] >= 0.0f ? t * inv : inv;
+      y[i] = l[i] >= 0.0f ? inv : t * inv;
     }
     total += y[i];
   }
