@@ -18,6 +18,7 @@
 // Measured on 16384 x 4096 bf16: forward with checkpoint 80 us (476 MB, 6.0 TB/s),
 // gradient 75 us (411 MB, 5.5); with the 128x1 operands, 8192 x 4096, 67 us (309
 // MB, 4.6).  A large device copy moves 5.1 TB/s on this card.
+#include <float.h>
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -240,7 +241,7 @@ __global__ __launch_bounds__(kTileThreads, 4) void gate_grad_tile_kernel(GateGra
   __shared__ __align__(16) uint8_t tbuf[3 * 128 * kTPitch];
   __shared__ __align__(16) float col_s[3][128], col_y[3][128];
   __shared__ float row_s[2][128];
-  __shared__ int odd;  // a column's scale is not a plain one
+  __shared__ int odd;  // a column's scale is not a plain one, or its maximum is infinite
   float(*part)[32][128] = reinterpret_cast<float(*)[32][128]>(tbuf);  // 48 of its 54 KB, before the bytes
 
   const int tid = threadIdx.x, cg = tid & 15, rg = tid >> 4;
@@ -310,7 +311,7 @@ __global__ __launch_bounds__(kTileThreads, 4) void gate_grad_tile_kernel(GateGra
     const TileScale sc = RULE == 0 ? scale_amax(m) : scale_pow2(m);
     col_s[o][c] = sc.s;
     col_y[o][c] = sc.y;
-    if (RULE == 0 && !plain_amax(m)) odd = 1;
+    if (RULE == 0 ? !plain_amax(m) : !(m <= FLT_MAX)) odd = 1;
     if (o < 2)
       p.st[(o * p.inner + c0 + c) * p.st_rs + tr * p.st_ts] = sc.s;
     else
@@ -334,8 +335,11 @@ __global__ __launch_bounds__(kTileThreads, 4) void gate_grad_tile_kernel(GateGra
       const int c = cg * 8 + j;
       float x[4] = {v[o][0][j], v[o][1][j], v[o][2][j], v[o][3][j]};
       uint32_t w;
-      if (RULE == 1) {
+      if (RULE == 1 && !slow) {
         w = pack4_unclamped(x[0] * y[j], x[1] * y[j], x[2] * y[j], x[3] * y[j]);
+      } else if (RULE == 1) {
+        // (the scale of an infinite maximum is finite: its quotients saturate)
+        w = pack4_e4m3(x[0] * y[j], x[1] * y[j], x[2] * y[j], x[3] * y[j]);
       } else if (!slow) {
         w = pack4_unclamped(div_by_scale(x[0], s[j], y[j]), div_by_scale(x[1], s[j], y[j]), div_by_scale(x[2], s[j], y[j]),
                             div_by_scale(x[3], s[j], y[j]));

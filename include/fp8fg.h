@@ -442,9 +442,12 @@ FP8FG_API int fp8_combine_backward(const void* dy, int type, int64_t z_rows, int
  *
  *   u      : [rows][2 inner] of u_type BF16 or F32, row pitch ldu: the gate g in
  *            the first inner columns, the linear half l in the others.
- *   a      = (g * sigmoid(g)) * l in fp32 (where that overflows, the scale is
- *            infinite).  The sigmoid takes g below -87 for -87, so that |g *
- *            sigmoid(g)| stays at 1.5e-36 there; above 87 it is 1.
+ *   a      = (g * sigmoid(g)) * l in fp32.  The sigmoid takes g below -87 for
+ *            -87, so that |g * sigmoid(g)| stays at 1.5e-36 there; above 87 it is
+ *            1.  Where a (or, in the functions below, a gradient) overflows,
+ *            the amax rule's scale of the tile is infinite and its bytes mean
+ *            nothing; the power-of-two rule's scale is 2^120, and the tile's
+ *            infinite values saturate.
  *   q, s   : E4M3 bytes [rows][inner] and 1x128 scales of the fp32 a, by the
  *            rules of fp8_quantize_rowtile
  *   uq, us : E4M3 bytes [rows][2 inner] and 1x128 scales of u; uq may be null
