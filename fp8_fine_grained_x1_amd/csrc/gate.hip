@@ -32,31 +32,32 @@ namespace {
 
 constexpr int kGThreads = 256;
 
-// exp(-|..|) in sigmoid(g) = 1 / (1 + exp(-g)): gates are held to [-87, 87] there.  Below
-// -87 the sigmoid stays at 2^-125.5 instead of falling on to 0, above 87 it
-// is 1 in fp32.  r = 1 - s without cancellation.
+// sigmoid(g) = 1 / (1 + exp(-g)) and g sigmoid(g): gates are held to [-87, 87] in the
+// exponent, and from below in the product.  Below -87 the sigmoid stays at 2^-125.5
+// instead of falling on to 0, above 87 it is 1 in fp32.  r = 1 - s without
+// cancellation.  A NaN stays one: the limits are IEEE 754's minimum and maximum (an
+// instruction each; med3 and max would give -87).
 struct Sigmoid {
-  float s, r;
+  float s, r, silu;
 };
 __device__ __forceinline__ Sigmoid sigmoid_of(float g) {
-  const float x = __builtin_amdgcn_fmed3f(g, -87.0f, 87.0f);
+  const float low = __builtin_elementwise_maximum(g, -87.0f);
+  const float x = __builtin_elementwise_minimum(low, 87.0f);
   const float t = x * -1.44269502f;                       // -x RN32(log2 e)
   float e = __builtin_fmaf(x, -1.44269502f, -t);          // the product's rounding error
   e = __builtin_fmaf(x, -1.92596299e-8f, e);              // log2 e - RN32(log2 e)
   const float c = __builtin_fmaf(e, 0.693147181f, 1.0f);  // 2^e to first order
   const float p = __builtin_amdgcn_exp2f(t) * c;
   const float s = __builtin_amdgcn_rcpf(1.0f + p);
-  return {s, p * s};
+  return {s, p * s, low * s};
 }
-__device__ __forceinline__ float silu_of(float g, float s) { return fmaxf(g, -87.0f) * s; }
 
 struct GateParts {
   float dg, dl, a;
 };
 __device__ __forceinline__ GateParts gate_parts(float da, float g, float l) {
   const Sigmoid s = sigmoid_of(g);
-  const float silu = silu_of(g, s.s);
-  return {da * l * __builtin_fmaf(silu, s.r, s.s), da * silu, silu * l};
+  return {da * l * __builtin_fmaf(s.silu, s.r, s.s), da * s.silu, s.silu * l};
 }
 
 // 8 lanes own a tile of 128 columns, 16 each, in two runs of 8 that start GAP
@@ -142,7 +143,7 @@ __global__ __launch_bounds__(kGThreads) void gate_kernel(GateArgs p, GateGrid gr
     decode_raw16<XT>(g, a);
     decode_raw16<XT>(l, b);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = silu_of(a[i], sigmoid_of(a[i]).s) * b[i];
+    for (int i = 0; i < 16; ++i) v[i] = sigmoid_of(a[i]).silu * b[i];
     quantize_tile<RULE, GAP, PAST>(v, p.q + row * p.ldq + col, p.s + row * p.s_rs + tc * p.s_ts);
     if constexpr (KEEP) {
       uint8_t* k = p.uq + row * p.lduq + col;
@@ -339,14 +340,14 @@ __global__ __launch_bounds__(kTileThreads, 4) void gate_grad_tile_kernel(GateGra
         w = pack4_unclamped(x[0] * y[j], x[1] * y[j], x[2] * y[j], x[3] * y[j]);
       } else if (RULE == 1) {
         // (the scale of an infinite maximum is finite: its quotients saturate)
-        w = pack4_e4m3(x[0] * y[j], x[1] * y[j], x[2] * y[j], x[3] * y[j]);
+        w = pack4_saturated(x[0] * y[j], x[1] * y[j], x[2] * y[j], x[3] * y[j]);
       } else if (!slow) {
         w = pack4_unclamped(div_by_scale(x[0], s[j], y[j]), div_by_scale(x[1], s[j], y[j]), div_by_scale(x[2], s[j], y[j]),
                             div_by_scale(x[3], s[j], y[j]));
       } else {
         const float pre = s[j] < kTinyScale ? kTinyLift : 1.0f;
         quotients<RULE, 4>(x, TileScale{s[j], s[j] * pre, y[j], pre});
-        w = pack4_e4m3(x[0], x[1], x[2], x[3]);
+        w = pack4_saturated(x[0], x[1], x[2], x[3]);
       }
       const int chunk = (rg >> 2) ^ ((c >> 4) & 7);
       *reinterpret_cast<uint32_t*>(tbuf + (o * 128 + c) * kTPitch + chunk * 16 + (rg & 3) * 4) = w;

@@ -3,6 +3,7 @@
 // the norms around a block (block_norm.hip).
 #pragma once
 
+#include <float.h>
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -156,6 +157,14 @@ __device__ __forceinline__ uint32_t pack4_unclamped(float a, float b, float c, f
   return (uint32_t)w;
 }
 
+// Four E4M3 bytes of any quotients: beyond 448 they saturate, a NaN stays one
+// (as it does above, so that a row's bytes do not depend on which form its
+// wave takes).
+__device__ __forceinline__ uint32_t pack4_saturated(float a, float b, float c, float d) {
+  const auto held = [](float x) { return __builtin_elementwise_minimum(__builtin_elementwise_maximum(x, -kE4M3Max), kE4M3Max); };
+  return pack4_unclamped(held(a), held(b), held(c), held(d));
+}
+
 // Whether scale_amax and its quotients need none of their steps for tiny
 // scales, infinities and NaN.
 constexpr float kLeastPlain = 0x1p-55f;
@@ -188,8 +197,14 @@ __device__ __forceinline__ float quantize(float (&v)[N], float m, uint32_t (&out
   }
   const TileScale sc = RULE == 0 ? scale_amax(m) : scale_pow2(m);
   quotients<RULE, N>(v, sc);
+  // (under the power-of-two rule 448 of the scale are at least a finite maximum)
+  if (RULE == 1 && __builtin_amdgcn_ballot_w64(!(m <= FLT_MAX)) == 0) {
 #pragma unroll
-  for (int i = 0; i < N / 4; ++i) out[i] = pack4_e4m3(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    for (int i = 0; i < N / 4; ++i) out[i] = pack4_unclamped(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    return sc.s;
+  }
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) out[i] = pack4_saturated(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
   return sc.s;
 }
 
