@@ -37,18 +37,25 @@ constexpr int kGThreads = 256;
 // instead of falling on to 0, above 87 it is 1 in fp32.  r = 1 - s without
 // cancellation.  A NaN stays one: the limits are IEEE 754's minimum and maximum (an
 // instruction each; med3 and max would give -87).
+//
+// The correction step of the quotient is by 1 - y - p y, so that the sum's own rounding
+// is made good too: dg, dl and a are then closer to 64 bits than a composition of
+// fp32 operations (root mean square 0.75 to 0.87 roundings, the composition 0.85 to
+// 1.6; without the step up to 0.97, and the gradient of 16384 x 4096 takes 74 us).
+// RN32(ln 2) is off by 2^-28.5, which makes up to 4 roundings of the exponential of
+// the farthest gates; a second constant there costs 3 us more.
 struct Sigmoid {
   float s, r, silu;
 };
 __device__ __forceinline__ Sigmoid sigmoid_of(float g) {
   const float low = __builtin_elementwise_maximum(g, -87.0f);
   const float x = __builtin_elementwise_minimum(low, 87.0f);
-  const float t = x * -1.44269502f;                       // -x RN32(log2 e)
-  float e = __builtin_fmaf(x, -1.44269502f, -t);          // the product's rounding error
-  e = __builtin_fmaf(x, -1.92596299e-8f, e);              // log2 e - RN32(log2 e)
-  const float c = __builtin_fmaf(e, 0.693147181f, 1.0f);  // 2^e to first order
-  const float p = __builtin_amdgcn_exp2f(t) * c;
-  const float s = __builtin_amdgcn_rcpf(1.0f + p);
+  const float t = x * -1.44269502f;                        // RN(-x RN32(log2 e))
+  const float e = __builtin_fmaf(t, -0.693147181f, -x);    // -x - t ln 2
+  const float q = __builtin_amdgcn_exp2f(t);
+  const float p = __builtin_fmaf(q, e, q);                 // 2^t exp(e) to first order
+  const float y = __builtin_amdgcn_rcpf(1.0f + p);
+  const float s = __builtin_fmaf(__builtin_fmaf(-p, y, 1.0f - y), y, y);
   return {s, p * s, low * s};
 }
 
