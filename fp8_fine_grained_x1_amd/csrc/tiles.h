@@ -173,8 +173,10 @@ __device__ __forceinline__ bool plain_amax(float m) { return m >= kLeastPlain &&
 // RN(m / 448) and RN(1 / s) of such an m, as scale_amax has them, in 8
 // instructions instead of 26.  Both are correction steps in fused
 // multiply-adds (Markstein, as in div_by_scale): from RN(1 / 448) for every m,
-// and from the hardware's reciprocal for every s -- checked for all 2^23
-// significands.
+// and from the hardware's reciprocal for every s -- which a step of one
+// correction does not give for any reciprocal within an ulp, but does for
+// this one: tests/test_gpu_tile_scale_sweep.py has the scales and quotients of all
+// 2^23 significands of m.
 __device__ __forceinline__ TileScale plain_scale(float m) {
   const float inv448 = 1.0f / 448.0f;
   const float q = m * inv448;

@@ -447,8 +447,9 @@ FP8FG_API int fp8_combine_backward(const void* dy, int type, int64_t z_rows, int
  *            1.  Where a (or, in the functions below, a gradient) overflows,
  *            the amax rule's scale of the tile is infinite and its bytes mean
  *            nothing; the power-of-two rule's scale is 2^120, and the tile's
- *            infinite values saturate.  A NaN in u or da shows in every value
- *            that it enters (bytes 0x7F or 0xFF) and has no part in the scales.
+ *            infinite values saturate.  A quiet NaN in u or da (arithmetic makes
+ *            no others) shows in every value that it enters (bytes 0x7F or 0xFF)
+ *            and has no part in the scales.
  *   q, s   : E4M3 bytes [rows][inner] and 1x128 scales of the fp32 a, by the
  *            rules of fp8_quantize_rowtile
  *   uq, us : E4M3 bytes [rows][2 inner] and 1x128 scales of u; uq may be null
