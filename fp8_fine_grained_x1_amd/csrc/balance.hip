@@ -393,38 +393,37 @@ struct BalancePieces {
 template <int LT, int LPT, int NE, bool VEC, int SCORE>
 __global__ __launch_bounds__(kPartThreads<NE>) void balance_part_kernel(BalanceArgs p, FastDiv by_k, BalancePieces q) {
   __shared__ BalanceLds m;
-  for (int64_t c = blockIdx.x; c < q.chunks; c += gridDim.x) {
-    const int64_t lo = c * q.chunk, hi = lo + q.chunk < p.rows ? lo + q.chunk : p.rows;
-    int64_t at = lo;
-    Bounds w;
-    bool known = false;
-    while (at < hi) {
-      // (loads return in order: the bounds first; nearly every piece starts where the last one
-      // ended, so that its tokens need not wait for them)
-      if (!known) w = load_bounds(p.offsets, p.seqs, p.rows, at);
-      Ahead<NE> h;
-      load_ahead<LT, LPT, NE, VEC>(p, by_k, at, hi, h);
-      const Seq f = seq_of(w, p.seqs, at);
-      if (f.s >= p.seqs) {
-        if (!known || w.base + 64 > p.seqs) break;
-        known = false;
-        continue;
-      }
-      known = true;
-      if (f.first > at) {
-        at = f.first;
-        continue;
-      }
-      const int64_t b = f.end < hi ? f.end : hi, piece = c + f.s;
-      sum_tokens<LT, LPT, NE, VEC, SCORE>(p, by_k, at, b, h, m);
-      at = b;
-      for (int e = threadIdx.x; e < p.experts; e += kPartThreads<NE>) {
-        q.sum[piece * p.experts + e] = column_sum<kPartThreads<NE> / 64>(m, e);
-        q.count[piece * p.experts + e] = m.hist[e];
-      }
-      if (threadIdx.x == 0) q.live[piece] = live_sum<kPartThreads<NE> / 64>(m);
-      __syncthreads();  // (the next piece writes m again)
+  const int64_t c = blockIdx.x;
+  const int64_t lo = c * q.chunk, hi = lo + q.chunk < p.rows ? lo + q.chunk : p.rows;
+  int64_t at = lo;
+  Bounds w;
+  bool known = false;
+  while (at < hi) {
+    // (loads return in order: the bounds first; nearly every piece starts where the last one
+    // ended, so that its tokens need not wait for them)
+    if (!known) w = load_bounds(p.offsets, p.seqs, p.rows, at);
+    Ahead<NE> h;
+    load_ahead<LT, LPT, NE, VEC>(p, by_k, at, hi, h);
+    const Seq f = seq_of(w, p.seqs, at);
+    if (f.s >= p.seqs) {
+      if (!known || w.base + 64 > p.seqs) break;
+      known = false;
+      continue;
     }
+    known = true;
+    if (f.first > at) {
+      at = f.first;
+      continue;
+    }
+    const int64_t b = f.end < hi ? f.end : hi, piece = c + f.s;
+    sum_tokens<LT, LPT, NE, VEC, SCORE>(p, by_k, at, b, h, m);
+    at = b;
+    for (int e = threadIdx.x; e < p.experts; e += kPartThreads<NE>) {
+      q.sum[piece * p.experts + e] = column_sum<kPartThreads<NE> / 64>(m, e);
+      q.count[piece * p.experts + e] = m.hist[e];
+    }
+    if (threadIdx.x == 0) q.live[piece] = live_sum<kPartThreads<NE> / 64>(m);
+    __syncthreads();  // (the next piece writes m again)
   }
 }
 
@@ -611,8 +610,8 @@ hipError_t balance_as(const BalanceArgs& a, hipStream_t st) {
   q.sum = reinterpret_cast<float*>(a.workspace);
   q.count = reinterpret_cast<int32_t*>(q.sum + pieces * a.experts);
   q.live = q.count + pieces * a.experts;
-  const unsigned blocks = (unsigned)(q.chunks < kMaxBlocks ? q.chunks : kMaxBlocks);
-  hipLaunchKernelGGL((balance_part_kernel<LT, LPT, NE, VEC, SCORE>), dim3(blocks), dim3(kPartThreads<NE>), 0, st, a, by_k, q);
+  // (at most 2^19 chunks: 2^31 rows, 4096 to each)
+  hipLaunchKernelGGL((balance_part_kernel<LT, LPT, NE, VEC, SCORE>), dim3((unsigned)q.chunks), dim3(kPartThreads<NE>), 0, st, a, by_k, q);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (a.experts % 4 == 0)
