@@ -491,6 +491,8 @@ void gate_like(const Tensor* gate, const Tensor& x, const Tensor& gamma) {
   if (!gate) return;
   if (gate->dim() == 2) {
     like(gate, x, "gate");
+    // (a pitch of 0, as of an expanded row, would be taken for a gate per column)
+    need(pitch(*gate) >= gate->size(1), "gate", "must have rows of its own (one row for all is a vector of the gammas' type)");
     return;
   }
   vec1(gate, x.size(1), x, false, "gate");
