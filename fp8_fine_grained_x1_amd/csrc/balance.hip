@@ -119,15 +119,16 @@ __device__ __forceinline__ float token_max(float v) {
   return v;
 }
 
-// exp(x) within 2 ulp, 0 below 2^-126 and for a NaN; above 2^128 it is infinite or NaN.
-__device__ __forceinline__ float exp_of(float x) {
-  x = fmaxf(x, -120.0f);
-  const float t = x * 1.44269502f;                        // RN32(log2 e)
-  float e = __builtin_fmaf(x, 1.44269502f, -t);
-  e = __builtin_fmaf(x, 1.92596299e-8f, e);               // log2 e - RN32(log2 e)
+// exp(x) = 2^t exp(x - t ln 2), t = RN(x RN32(log2 e)): within an ulp of the
+// hardware's 2^t and |x| 2^-28 of RN32(ln 2), of which a softmax's shares have the
+// differences' alone.  x at least -120; infinite or NaN above 2^128.
+__device__ __forceinline__ float exp_from(float x) {
+  const float t = x * 1.44269502f;
   const float p = __builtin_amdgcn_exp2f(t);
-  return __builtin_fmaf(p, e * 0.693147181f, p);
+  return __builtin_fmaf(p, __builtin_fmaf(t, -0.693147181f, x), p);
 }
+// 0 below 2^-126 and for a NaN.
+__device__ __forceinline__ float exp_of(float x) { return exp_from(fmaxf(x, -120.0f)); }
 
 // RN-close 1 / x of a normal x.
 __device__ __forceinline__ float reciprocal(float x) {
@@ -172,7 +173,8 @@ __device__ __forceinline__ float scores_below_top(const float (&l)[NE], float (&
 // does not grow with its logit.  The sum tells: with one below 1 (softmax) or 1/2
 // (sigmoid), above 2^100 or NaN in the wave the scores are formed again
 // below the largest logit.  That maximum and its checks cost half of the
-// instructions.  (A NaN logit comes out as 0, as a masked one.)
+// instructions.  (A NaN logit comes out as a masked one; far up it ends in a NaN
+// of the sum.)
 template <int LPT, int NE, int SCORE, bool REST>
 __device__ __forceinline__ float token_scores(const float (&l)[NE], float (&y)[NE], float (&r)[NE], bool& live) {
   float total = 0.0f;
@@ -181,10 +183,13 @@ __device__ __forceinline__ float token_scores(const float (&l)[NE], float (&y)[N
   for (int i = 0; i < NE; ++i) {
     if (SCORE == 0) {
       y[i] = exp_of(l[i]);
-    } else {
+    } else if (REST) {
       const float t = exp_of(-fabsf(l[i])), inv = __builtin_amdgcn_rcpf(1.0f + t);
-      if (REST) r[i] = l[i] >= 0.0f ? t * inv : inv;
+      r[i] = l[i] >= 0.0f ? t * inv : inv;
       y[i] = l[i] >= 0.0f ? inv : t * inv;
+    } else {
+      // (from -87 on down, and for a NaN, 2^-125.5)
+      y[i] = __builtin_amdgcn_rcpf(1.0f + exp_from(-fmaxf(l[i], -87.0f)));
     }
     total += y[i];
   }

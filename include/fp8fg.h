@@ -518,7 +518,8 @@ FP8FG_API int fp8_swiglu_backward_128x1(const void* da, int type, int64_t rows, 
  *   logits : [rows][experts] of l_type, row pitch ldl, as fp8_route takes them;
  *            score is its score.  share[t][i] = s_i / sum_j s_j (softmax: s
  *            itself).  A logit of -inf or NaN masks its expert, whose share is
- *            0; a token whose experts are all masked (padding) is not counted.
+ *            0 (in a sigmoid's sums below 2^-124, as of any logit below -87);
+ *            a token whose experts are all masked (padding) is not counted.
  *   idx    : int32 [rows][k], row pitch ld_idx, as fp8_route gives them;
  *            entries outside [0, experts) are not counted.
  *   offsets: DEVICE int32 [seqs + 1], nondecreasing (not checked; held within
