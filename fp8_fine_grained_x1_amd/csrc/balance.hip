@@ -21,7 +21,7 @@
 // result depends on the order in which workgroups run.
 //
 // The bytes are few (16384 x 256 f32: 17 MB, 3.4 us at a device copy's rate); what
-// counts is latency: two dependent launches (9 and 5 us of 14), the loads of
+// counts is latency: two dependent launches (9 and 5 us of 14 to 15), the loads of
 // bounds, then of tokens, and the fetching of code that each workgroup runs
 // through once or twice.  With the loops unrolled and both scores in one kernel the first
 // took 12 us; with the largest logit of every token 14.
@@ -172,9 +172,10 @@ __device__ __forceinline__ float scores_below_top(const float (&l)[NE], float (&
 // a sum that is not small, and without a difference to round a score's error
 // does not grow with its logit.  The sum tells: with one below 1 (softmax) or 1/2
 // (sigmoid), above 2^100 or NaN in the wave the scores are formed again
-// below the largest logit.  That maximum and its checks cost half of the
-// instructions.  (A NaN logit comes out as a masked one; far up it ends in a NaN
-// of the sum.)
+// below the largest logit (16384 x 256, softmax: around 0 11 us, around -8, where all
+// waves do, 14).  That maximum and its checks cost half of the instructions.  (A NaN
+// logit comes out as a masked one; one whose exponential overflows makes the sum
+// infinite or NaN.)
 template <int LPT, int NE, int SCORE, bool REST>
 __device__ __forceinline__ float token_scores(const float (&l)[NE], float (&y)[NE], float (&r)[NE], bool& live) {
   float total = 0.0f;
@@ -509,7 +510,7 @@ constexpr int kGradThreads = 256;
 
 // A wave takes `run` consecutive tokens (per lane group every kPer-th of
 // them); the next token's logits and base are loaded while this one is formed.
-// 16384 x 256 f32 with base: 12.2 us (50 MB, 4.1 TB/s; 16 waves per CU: with 32
+// 16384 x 256 f32 with base: 12.1 us (50 MB, 4.2 TB/s; 16 waves per CU: with 32
 // and two tokens to each 13 to 14, with 8 as many).
 template <int LT, int LPT, int NE, bool VEC, int SCORE>
 __global__ __launch_bounds__(kGradThreads) void balance_grad_kernel(BalanceGradArgs p, int64_t run) {

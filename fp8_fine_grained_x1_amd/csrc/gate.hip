@@ -12,12 +12,12 @@
 //               of a.  (Both quantizers are passed straight through.)
 // Every output is rounded once, from the fp32 value.
 //
-// All three kernels are bound by HBM, closely: an element costs 36 vector
-// instructions forward and 35 backward, which keep the vector units busy in 86 and 90%
-// of the cycles; still, leaving the sigmoids out changes the times by 2% at most.
-// Measured on 16384 x 4096 bf16: forward with checkpoint 80 us (476 MB, 6.0 TB/s),
-// gradient 75 us (411 MB, 5.5); with the 128x1 operands, 8192 x 4096, 67 us (309
-// MB, 4.6).  A large device copy moves 5.1 TB/s on this card.
+// An element costs 36 vector instructions in either direction, which keep the
+// vector units busy in 85% of the forward's cycles, which HBM bounds, and 94% of
+// the gradient's, which they bound.  Measured on 16384 x 4096 bf16: forward with
+// checkpoint 80 us (476 MB, 6.0 TB/s), gradient 74 to 78 us over boxes (411 MB,
+// 5.4); with the 128x1 operands, 8192 x 4096, 67 to 72 us (309 MB, 4.5).  A large
+// device copy moves 5.1 TB/s on this card.
 #include <float.h>
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -70,9 +70,9 @@ __device__ __forceinline__ GateParts gate_parts(float da, float g, float l) {
 // 8 lanes own a tile of 128 columns, 16 each, in two runs of 8 that start GAP
 // apart: 8 (16 columns in a row: 16-byte accesses of E4M3 bytes) or 64 (runs
 // of neighbouring lanes adjoin: contiguous 16-byte accesses of bf16).  Where
-// most bytes are E4M3 the first gains (gradient of 16384 x 4096: 75 us, 79),
-// where most are written in bf16 the second (with du and a, 5003 x 2048: 26.7
-// us, 28.1); the forward pass hardly cares (82.4, 83.7).
+// most bytes are E4M3 the first gains (gradient of 16384 x 4096: 77.6 us, 79.5),
+// where most are written in bf16 the second (with du and a, 5003 x 2048: 27.9
+// us, 28.9); the forward pass takes the first (80.7, 85.8).
 template <int GAP>
 __device__ __forceinline__ uint32_t lane_column() { return (threadIdx.x & 7) * (GAP == 8 ? 16 : 8); }
 
@@ -236,12 +236,13 @@ __global__ __launch_bounds__(kGThreads) void gate_grad_kernel(GateGradArgs p, Ga
 // the transposed bytes are staged there, so that a wave stores whole 128-byte
 // rows.
 //
-// 96 values to a thread: 512 threads at 125 registers, two workgroups to a CU.
+// 96 values to a thread: 512 threads at 124 registers, two workgroups to a CU.
 // (256 threads that formed every value once per tiling, at 256 registers: 160
-// us on 8192 x 4096, this 67.)  What bounds it is the run of load, maxima, bytes
+// us on 8192 x 4096, this 67 on that box.)  What bounds it is the run of load, maxima, bytes
 // and stores in only two workgroups per CU: without the sigmoids and quotients
-// 96% of the time remains, without the transposed stores 84%.  Loading the
-// next block ahead spills 97 registers (156 us).
+// 96% of the time remains, without the transposed stores 84%.  LDS is active in 16% of
+// the cycles, two fifths of them bank conflicts.  Loading the next block ahead
+// spills 97 registers (156 us).
 constexpr int kTileThreads = 512;
 
 template <int XT, int RULE>
@@ -371,7 +372,8 @@ __global__ __launch_bounds__(kTileThreads, 4) void gate_grad_tile_kernel(GateGra
   }
 }
 
-// (One tile for each 8 lanes: 6 to 8 waves on a SIMD keep enough loads in flight.)
+// (One tile for each 8 lanes: by their registers 6 to 8 waves fit a SIMD forward, 6 or 7 in
+// the gradient, 4 or 5 with du and a.)
 constexpr int64_t kMaxGateBlocks = 1 << 20;
 
 // Workgroups for `rows` (all of them: how many are in use is known on the

@@ -405,7 +405,7 @@ struct BlockNormGradArgs {
 };
 int64_t block_norm_strips(int64_t rows, int64_t cols);
 hipError_t launch_block_norm_grad(const BlockNormGradArgs& a, hipStream_t st);
-// Widest row a workgroup of 512 threads holds in registers.
+// Widest row a workgroup of 1024 threads holds, 16 elements to each.
 constexpr int64_t kBlockNormMaxCols = 16384;
 
 }  // namespace fp8fg

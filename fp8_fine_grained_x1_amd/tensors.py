@@ -303,7 +303,8 @@ def swiglu_backward(da, uq, us, used=None, want_du=False, want_a=False, pow2=Fal
 def swiglu_backward_128x1(da, uq, us, pow2=False, scale_layout="group_major", stream=None):
     """The same gradient with the operands of both weight gradients: 128x1
     tiles, transposed, of [dgate | dlin] and of the gate's result (rows a
-    multiple of 128).  Returns (dq, ds, dqT, dsT, aqT, asT)."""
+    multiple of 128, of one expert: a tile knows no bounds).  Returns (dq, ds, dqT,
+    dsT, aqT, asT)."""
     return _call("swiglu_backward_128x1", stream, da, (da, uq, us),
                  (da, uq, us, _rule(pow2), _of(_LAYOUT, scale_layout, "scale_layout")))
 

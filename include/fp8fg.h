@@ -500,7 +500,9 @@ FP8FG_API int fp8_swiglu_backward(const void* da, int type, int64_t rows, int64_
  *   dqt, dst : 128x1 tiles of [dg | dl], transposed: bytes [2 inner][rows],
  *              scales dst[c * dst_rs + (r / 128) * dst_ts]
  *   aqt, ast : 128x1 tiles of a, transposed: bytes [inner][rows]
- *   All are written.  Requires rows % 128 == 0 and inner % 128 == 0.
+ *   All are written.  Requires rows % 128 == 0 and inner % 128 == 0.  The rows
+ *   are one expert's (a dense or shared one): there are no bounds, and a tile of
+ *   128 rows that holds two experts' has one scale for both.
  *   Limits also: rows / 128 <= 65535.
  */
 FP8FG_API int fp8_swiglu_backward_128x1(const void* da, int type, int64_t rows, int64_t inner,
@@ -570,7 +572,8 @@ FP8FG_API int fp8_balance_loss_backward(const float* dloss, const void* logits, 
  *   rstd_post[m] = 1 / sqrt(sum_c z^2 / cols + eps)
  *   t[m][c]  = ((z * rstd_post) * gamma_post[c]) * gate, in fp32
  *   h[m][c]  = RN(residual_scale * r + block_scale * t) in x_type
- *   rstd, y, q, s: the norm of h with gamma, as fp8_rmsnorm_quantize's
+ *   rstd, y, q, s: the norm of h with gamma, defined as fp8_rmsnorm_quantize's
+ *            (its sums are in another order: last bits may differ)
  *
  *   z, r, h, y : x_type BF16 or F32 with row pitches ldz, ldr, ldh, ldy.  h is
  *            needed; y, q with s, rstd_post and rstd may be null.
